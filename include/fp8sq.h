@@ -95,6 +95,15 @@ extern "C" {
 #define FP8SQ_AMAX_MAX 0
 #define FP8SQ_AMAX_MOST_RECENT 1
 
+/* activations: identity, max(x, 0), x Phi(x) with the normal distribution
+ * function, its tanh form x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2, and
+ * x / (1 + exp(-x)) */
+#define FP8SQ_ACT_NONE 0
+#define FP8SQ_ACT_RELU 1
+#define FP8SQ_ACT_GELU 2
+#define FP8SQ_ACT_GELU_TANH 3
+#define FP8SQ_ACT_SILU 4
+
 /* recipes ([TS] Part 01 / [TE] Format.HYBRID; [W14] "E4M3 is enough
  * everywhere" with fine-grained scaling) */
 #define FP8SQ_RECIPE_HYBRID 0     /* x, W in E4M3; dY in E5M2 */
@@ -408,6 +417,99 @@ FP8SQ_API int fp8_layernorm_linear_fwd(const void* x, const float* gamma, const 
 FP8SQ_API int fp8_linear_fwd_noalloc(const void* x, const void* w, int64_t M, int64_t N, int64_t K,
                                      const float* bias, void* y, int y_dtype, void* stream);
 
+/* ---- 5c. a feed-forward sublayer around the FP8 linear ----------------------
+ * The pages stop at the linear layer; these are the operators a transformer's
+ * feed-forward sublayer puts around it (te.LayerNorm and te.LayerNormMLP of
+ * [TE] name the same parts).  Inputs and outputs must not overlap.
+ *
+ * fp8_layernorm_fwd: s = x + residual (rounded to the type, written to
+ *   sum_out; s = x without a residual), mu = sum(s)/K, var = sum((s - mu)^2)/K,
+ *   rstd = 1/sqrt(var + eps), y = (s - mu) rstd gamma + beta, in fp32.
+ *     dtype         of x, residual, sum_out, y [M][K]: BF16 or F32
+ *     residual, sum_out  both or neither; beta may be NULL (zero)
+ *     mu_out, rstd_out   f32 [M] or NULL (the backward pass needs them)
+ *   Any M >= 0 and K >= 1; x, residual, sum_out, y, gamma, beta 16-byte
+ *   aligned.
+ * fp8_layernorm_bwd: with xh = (x - mu) rstd and w = dy gamma,
+ *   dx = rstd (w - mean(w) - xh mean(w xh)) + dres,
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy (fp32, in a
+ *   fixed order: the same call gives the same bits).
+ *     x is what the forward normalised (its sum_out where it had a residual),
+ *     mu and rstd what it returned (fp8_layernorm_quantize's serve too);
+ *     dres [M][K] (the residual branch's gradient) or NULL.
+ *     workspace  device, >= fp8_layernorm_bwd_workspace_bytes(M, K), 16-byte
+ *                aligned; its contents do not matter.
+ *   M == 0 gives dgamma = dbeta = 0.
+ */
+FP8SQ_API int fp8_layernorm_fwd(const void* x, const void* residual, int dtype, const float* gamma, const float* beta,
+                                float eps, int64_t M, int64_t K, void* sum_out, void* y, float* mu_out, float* rstd_out,
+                                void* stream);
+FP8SQ_API size_t fp8_layernorm_bwd_workspace_bytes(int64_t M, int64_t K);
+FP8SQ_API int fp8_layernorm_bwd(const void* dy, const void* x, const void* dres, int dtype, const float* gamma,
+                                const float* mu, const float* rstd, int64_t M, int64_t K, void* dx, float* dgamma,
+                                float* dbeta, void* workspace, size_t ws_bytes, void* stream);
+
+/* fp8_gemm_act: a per-tensor-scaled product with bias, activation and residual
+ * in its epilogue:
+ *   z = (sum_k dec(A[m][k]) dec(B[n][k])) sA sB + bias[n]
+ *   y = act(z) + residual[m][n]                       (fp32 arithmetic)
+ *   A [M][K], B [N][K] FP8 codes (K contiguous), a_scale / b_scale f32[1]
+ *   bias f32 [N] or NULL; residual [M][N] of res_dtype or NULL
+ *   z_out  bf16 [M][N] or NULL: z, for fp8_act_bwd
+ *   D      [M][N] of d_dtype or NULL: y
+ *   q_out  u8 [M][N] or NULL: the codes sat_RNE_fp8(y * m) in q_format under
+ *          the delayed state q_state (m = q_state[H]; max|y| is max-combined
+ *          into q_state[0]), cast from the fp32 y
+ *   At least one of z_out, D, q_out.  K > 0, K % 16 == 0, N % 8 == 0 (% 16
+ *   with q_out); M >= 0; D, z, residual, bias, q_out 16-byte aligned.
+ *   workspace  NULL, or device memory of fp8_gemm_act_workspace_bytes(M, N, K)
+ *     bytes, 256-byte aligned, all zero before its first use.  With it a
+ *     product of few rows (serving: single tokens) splits K over the SMs; the
+ *     call leaves it as it needs to find it.  Calls that may overlap on the
+ *     GPU need one each; after FP8SQ_ERR_TIMEOUT zero it again.  The size is 0
+ *     where the split does not apply.
+ * fp8_act_bwd: the elementwise backward pass: dz = dy act'(z), its codes under
+ *   a delayed state (q_out), dz itself (dz_out, bf16) and dbias = sum over
+ *   rows of dz (fp32, before the cast, in a fixed order), each optional.  The
+ *   products dx = dz W and dW = dz^T x are fp8_gemm_layout on the codes.
+ *     dy, z bf16 [M][N]; any M, N >= 0; 16-byte aligned
+ *     workspace  >= fp8_act_bwd_workspace_bytes(M, N) if dbias is asked for
+ *
+ * fp8_glu_fwd: a gated feed-forward block's two projections, activation and
+ *   product: [g | u] = (A W^T) sA sW, W = [W_gate; W_up] u8 [2F][K],
+ *   h = act(g) u.
+ *   gu_out  bf16 [M][2F] or NULL: g, then u (for fp8_glu_bwd)
+ *   h_out   bf16 [M][F] or NULL; q_out u8 [M][F] or NULL: codes of the fp32 h
+ *           under q_state, as in fp8_gemm_act.  At least one of the two.
+ *   F % 16 == 0, K % 16 == 0, K > 0.  workspace as in fp8_gemm_act, of
+ *   fp8_glu_fwd_workspace_bytes(M, F, K) bytes.
+ * fp8_glu_bwd: from the gradient of the block's output, dY [M][K] codes, and
+ *   the down projection's codes Wd [K][F] as its forward holds them:
+ *   dh = (dY Wd) sdY sW, dg = dh u act'(g), du = dh act(g); q_dgu u8 [M][2F]
+ *   receives the codes of [dg | du] under q_state (dh itself is never
+ *   written).  The products dx = [dg | du] W, dW = [dg | du]^T x and
+ *   dWd = dY^T h are fp8_gemm_layout on the codes, with W as stored.
+ *   F % 16 == 0, K % 16 == 0, K > 0.
+ */
+FP8SQ_API size_t fp8_gemm_act_workspace_bytes(int64_t M, int64_t N, int64_t K);
+FP8SQ_API int fp8_gemm_act(const uint8_t* A, int a_format, const float* a_scale, const uint8_t* B, int b_format,
+                           const float* b_scale, int64_t M, int64_t N, int64_t K, int act, const float* bias,
+                           const void* residual, int res_dtype, void* z_out, void* D, int d_dtype, uint8_t* q_out,
+                           int q_format, float* q_state, int q_history_len, void* workspace, size_t ws_bytes,
+                           void* stream);
+FP8SQ_API size_t fp8_act_bwd_workspace_bytes(int64_t M, int64_t N);
+FP8SQ_API int fp8_act_bwd(const void* dy, const void* z, int64_t M, int64_t N, int act, float* dbias, void* dz_out,
+                          uint8_t* q_out, int q_format, float* q_state, int q_history_len, void* workspace,
+                          size_t ws_bytes, void* stream);
+FP8SQ_API size_t fp8_glu_fwd_workspace_bytes(int64_t M, int64_t F, int64_t K);
+FP8SQ_API int fp8_glu_fwd(const uint8_t* A, int a_format, const float* a_scale, const uint8_t* W, int w_format,
+                          const float* w_scale, int64_t M, int64_t F, int64_t K, int act, void* gu_out, void* h_out,
+                          uint8_t* q_out, int q_format, float* q_state, int q_history_len, void* workspace,
+                          size_t ws_bytes, void* stream);
+FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scale, const uint8_t* Wd, int w_format,
+                          const float* w_scale, int64_t M, int64_t F, int64_t K, const void* gu, int act,
+                          uint8_t* q_dgu, int q_format, float* q_state, int q_history_len, void* stream);
+
 /* ---- 6. diagnostics --------------------------------------------------------
  * fp8_device_status: synchronises the current device and returns
  *   FP8SQ_ERR_TIMEOUT if any bounded device-side wait of this library ran out
@@ -422,7 +524,7 @@ FP8SQ_API int fp8_linear_fwd_noalloc(const void* x, const void* w, int64_t M, in
  *   cleared.
  * fp8_last_error: message for the calling thread's last non-zero status
  *   (static thread-local storage; never NULL).
- * fp8_abi_version: 7.  Changes from 6: fp8_linear_fwd / fp8_linear_bwd,
+ * fp8_abi_version: 7.  Section 5c only adds entry points to it.  Changes from 6: fp8_linear_fwd / fp8_linear_bwd,
  *   fp8_linear_workspace_bytes and fp8_quantize_rows_cols accept
  *   TILE_1x128_POW2 (the fine-grained units with power-of-two scales).
  *   Changes from 5 to 6: fp8_gemm_cast added (the GEMM's

@@ -19,6 +19,7 @@ TILE_1x128_POW2, BLOCK_128x128_POW2, MX32_FLOOR_TILED = 7, 8, 9
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 RECIPE_HYBRID, RECIPE_E4M3 = 0, 1
 K_MAJOR, MN_MAJOR = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WRONG_ARCH, ERR_CUDA, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +73,16 @@ def lib() -> ctypes.CDLL:
                 "fp8_layernorm_quantize": (I, [P, P, P, c.c_float, I64, I64, I, P, I, P, P, P, P, P]),
                 "fp8_layernorm_linear_fwd": (I, [P, P, P, c.c_float, P, I64, I64, I64, P, P, I, P, Z, P, P, P, P,
                                                  I, P]),
+                "fp8_layernorm_fwd": (I, [P, P, I, P, P, c.c_float, I64, I64, P, P, P, P, P]),
+                "fp8_layernorm_bwd_workspace_bytes": (Z, [I64, I64]),
+                "fp8_layernorm_bwd": (I, [P, P, P, I, P, P, P, I64, I64, P, P, P, P, Z, P]),
+                "fp8_gemm_act_workspace_bytes": (Z, [I64, I64, I64]),
+                "fp8_gemm_act": (I, [P, I, P, P, I, P, I64, I64, I64, I, P, P, I, P, P, I, P, I, P, I, P, Z, P]),
+                "fp8_act_bwd_workspace_bytes": (Z, [I64, I64]),
+                "fp8_act_bwd": (I, [P, P, I64, I64, I, P, P, P, I, P, I, P, Z, P]),
+                "fp8_glu_fwd_workspace_bytes": (Z, [I64, I64, I64]),
+                "fp8_glu_fwd": (I, [P, I, P, P, I, P, I64, I64, I64, I, P, P, P, I, P, I, P, Z, P]),
+                "fp8_glu_bwd": (I, [P, I, P, P, I, P, I64, I64, I64, P, I, P, I, P, I, P]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
@@ -363,6 +374,176 @@ def fp8_linear_fwd_noalloc(x, w, y, bias=None, stream=None) -> None:
     _opt(bias, "bias", T.float32, 4 * N)
     _check(lib().fp8_linear_fwd_noalloc(_ptr(x), _ptr(w), M, N, K, _ptr(bias), _ptr(y), _dtype_code(y),
                                         _stream(stream)))
+
+
+# ------------------------------------------------- feed-forward sublayer
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _matrix(t, name: str, rows: int, cols: int, dtype):
+    """an operand or output [rows][cols] whose shape the call's sizes come from"""
+    _need(t, name, dtype)
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+
+
+def _vector(t, name: str, n: int, dtype=None):
+    _need(t, name, dtype if dtype is not None else _t().float32)
+    if t.numel() < n:
+        raise ValueError(f"{name}: {t.numel()} elements, needs {n}")
+
+
+def _cast_args(q, name: str, rows: int, cols: int, state, history_len: int):
+    if q is None:
+        return
+    _matrix(q, name, rows, cols, _t().uint8)
+    _vector(state, "q_state", history_len + 2)
+
+
+def _gemm_operands(A, a_scale, B, b_scale, a_name: str, b_name: str):
+    T = _t()
+    for t, name in ((A, a_name), (B, b_name)):
+        _need(t, name, T.uint8)
+        if t.dim() != 2:
+            raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
+    _vector(a_scale, "a_scale", 1)
+    _vector(b_scale, "b_scale", 1)
+
+
+def fp8_layernorm_fwd(x, gamma, beta, eps: float, y, mu=None, rstd=None, residual=None, sum_out=None,
+                      stream=None) -> None:
+    """y = LayerNorm(x) gamma + beta; with a residual, of sum_out = x + residual."""
+    M, K = x.shape
+    code = _dtype_code(x)
+    _need(x, "x")
+    _matrix(y, "y", M, K, x.dtype)
+    _vector(gamma, "gamma", K)
+    if beta is not None:
+        _vector(beta, "beta", K)
+    if (residual is None) != (sum_out is None):
+        raise ValueError("residual and sum_out come together")
+    if residual is not None:
+        _matrix(residual, "residual", M, K, x.dtype)
+        _matrix(sum_out, "sum_out", M, K, x.dtype)
+    for t, name in ((mu, "mu"), (rstd, "rstd")):
+        if t is not None:
+            _vector(t, name, M)
+    _check(lib().fp8_layernorm_fwd(_ptr(x), _ptr(residual), code, _ptr(gamma), _ptr(beta), eps, M, K, _ptr(sum_out),
+                                   _ptr(y), _ptr(mu), _ptr(rstd), _stream(stream)))
+
+
+def fp8_layernorm_bwd_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().fp8_layernorm_bwd_workspace_bytes(M, K))
+
+
+def fp8_layernorm_bwd(dy, x, gamma, mu, rstd, dx, dgamma, dbeta, workspace, dres=None, stream=None) -> None:
+    """dx (+ dres), dgamma and dbeta of a LayerNorm from its input x and saved mu, rstd."""
+    M, K = x.shape
+    code = _dtype_code(x)
+    _need(x, "x")
+    _matrix(dy, "dy", M, K, x.dtype)
+    _matrix(dx, "dx", M, K, x.dtype)
+    if dres is not None:
+        _matrix(dres, "dres", M, K, x.dtype)
+    for t, name, n in ((gamma, "gamma", K), (mu, "mu", M), (rstd, "rstd", M), (dgamma, "dgamma", K),
+                       (dbeta, "dbeta", K)):
+        _vector(t, name, n)
+    _need(workspace, "workspace", _t().uint8)
+    _check(lib().fp8_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(dres), code, _ptr(gamma), _ptr(mu), _ptr(rstd), M, K,
+                                   _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace),
+                                   _stream(stream)))
+
+
+def fp8_gemm_act_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().fp8_gemm_act_workspace_bytes(M, N, K))
+
+
+def fp8_gemm_act(A, a_format: int, a_scale, B, b_format: int, b_scale, act: int, D=None, bias=None, residual=None,
+                 z_out=None, q_out=None, q_format: int = E4M3, q_state=None, history_len: int = 0, workspace=None,
+                 stream=None) -> None:
+    """y = act(z) + residual, z = A B^T sA sB + bias, into D (bf16 / fp32) and / or FP8 codes q_out; z into z_out."""
+    T = _t()
+    _gemm_operands(A, a_scale, B, b_scale, "A", "B")
+    M, K = A.shape
+    N = B.shape[0]
+    _matrix(B, "B", N, K, T.uint8)
+    if D is not None:
+        _matrix(D, "D", M, N, D.dtype)
+    if residual is not None:
+        _matrix(residual, "residual", M, N, residual.dtype)
+    if z_out is not None:
+        _matrix(z_out, "z_out", M, N, T.bfloat16)
+    if bias is not None:
+        _vector(bias, "bias", N)
+    _cast_args(q_out, "q_out", M, N, q_state, history_len)
+    _opt(workspace, "workspace", T.uint8)
+    _check(lib().fp8_gemm_act(_ptr(A), a_format, _ptr(a_scale), _ptr(B), b_format, _ptr(b_scale), M, N, K, act,
+                              _ptr(bias), _ptr(residual), BF16 if residual is None else _dtype_code(residual),
+                              _ptr(z_out), _ptr(D), BF16 if D is None else _dtype_code(D), _ptr(q_out), q_format,
+                              _ptr(q_state), history_len, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def fp8_act_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(lib().fp8_act_bwd_workspace_bytes(M, N))
+
+
+def fp8_act_bwd(dy, z, act: int, dbias=None, dz=None, q_out=None, q_format: int = E5M2, q_state=None,
+                history_len: int = 0, workspace=None, stream=None) -> None:
+    """dz = dy act'(z): FP8 codes q_out, bf16 dz, and dbias = the column sums of dz."""
+    T = _t()
+    M, N = z.shape
+    _need(z, "z", T.bfloat16)
+    _matrix(dy, "dy", M, N, T.bfloat16)
+    if dbias is not None:
+        _vector(dbias, "dbias", N)
+    if dz is not None:
+        _matrix(dz, "dz", M, N, T.bfloat16)
+    _cast_args(q_out, "q_out", M, N, q_state, history_len)
+    _opt(workspace, "workspace", T.uint8)
+    _check(lib().fp8_act_bwd(_ptr(dy), _ptr(z), M, N, act, _ptr(dbias), _ptr(dz), _ptr(q_out), q_format,
+                             _ptr(q_state), history_len, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def fp8_glu_fwd_workspace_bytes(M: int, F: int, K: int) -> int:
+    return int(lib().fp8_glu_fwd_workspace_bytes(M, F, K))
+
+
+def fp8_glu_fwd(A, a_format: int, a_scale, W, w_format: int, w_scale, act: int, h_out=None, gu_out=None, q_out=None,
+                q_format: int = E4M3, q_state=None, history_len: int = 0, workspace=None, stream=None) -> None:
+    """h = act(g) u with [g | u] = A W^T sA sW, W = [W_gate; W_up]: into h_out (bf16) and / or FP8 codes q_out;
+    [g | u] into gu_out."""
+    T = _t()
+    _gemm_operands(A, a_scale, W, w_scale, "A", "W")
+    M, K = A.shape
+    F = W.shape[0] // 2
+    _matrix(W, "W", 2 * F, K, T.uint8)
+    if h_out is not None:
+        _matrix(h_out, "h_out", M, F, T.bfloat16)
+    if gu_out is not None:
+        _matrix(gu_out, "gu_out", M, 2 * F, T.bfloat16)
+    _cast_args(q_out, "q_out", M, F, q_state, history_len)
+    _opt(workspace, "workspace", T.uint8)
+    _check(lib().fp8_glu_fwd(_ptr(A), a_format, _ptr(a_scale), _ptr(W), w_format, _ptr(w_scale), M, F, K, act,
+                             _ptr(gu_out), _ptr(h_out), _ptr(q_out), q_format, _ptr(q_state), history_len,
+                             _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def fp8_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scale, gu, act: int, q_dgu, q_format: int,
+                q_state, history_len: int, stream=None) -> None:
+    """codes of [dg | du] from the block's output gradient dY [M][K], the down projection Wd [K][F] and the
+    forward's [g | u]."""
+    T = _t()
+    _gemm_operands(dY, dy_scale, Wd, w_scale, "dY", "Wd")
+    M, K = dY.shape
+    F = Wd.shape[1]
+    _matrix(Wd, "Wd", K, F, T.uint8)
+    _matrix(gu, "gu", M, 2 * F, T.bfloat16)
+    if q_dgu is None:
+        raise ValueError("q_dgu is required")
+    _cast_args(q_dgu, "q_dgu", M, 2 * F, q_state, history_len)
+    _check(lib().fp8_glu_bwd(_ptr(dY), dy_format, _ptr(dy_scale), _ptr(Wd), w_format, _ptr(w_scale), M, F, K,
+                             _ptr(gu), act, _ptr(q_dgu), q_format, _ptr(q_state), history_len, _stream(stream)))
 
 
 def fp8_selftest_wait_timeout(limit_us: int, waited_out, stream=None) -> None:

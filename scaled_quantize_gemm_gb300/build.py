@@ -13,8 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfp8sq.so")
-SOURCES = ["quantize.cu", "gemm.cu", "api.cu", "noalloc.cu"]
-HEADERS = ["ptx.cuh", "internal.h", os.path.join("..", "..", "include", "fp8sq.h")]
+SOURCES = ["quantize.cu", "gemm.cu", "ffn.cu", "rowops.cu", "api.cu", "api_ffn.cu", "noalloc.cu"]
+HEADERS = ["ptx.cuh", "act.cuh", "gemm_common.cuh", "internal.h", os.path.join("..", "..", "include", "fp8sq.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

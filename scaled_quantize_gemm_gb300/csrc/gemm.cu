@@ -30,6 +30,7 @@
 
 #include <mutex>
 
+#include "gemm_common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -68,38 +69,6 @@ cudaError_t smem_attr_once(const void* kern, int bytes)
     return e;
 }
 
-struct TileSched {
-    int num_m, num_n, group;
-    __device__ __forceinline__ void coords(int t, int& mb, int& nb) const
-    {
-        const int per_group = group * num_n;
-        const int g = t / per_group;
-        const int first = g * group;
-        const int gs = min(num_m - first, group);
-        const int r = t - g * per_group;
-        mb = first + r % gs;
-        nb = r / gs;
-    }
-};
-
-// M-tiles per group of the rasterisation.  The concurrent tiles of one wave
-// cover `group` M-tiles and about concurrent / group N-tiles, so they hold
-// (group x tile_m + concurrent / group x tile_n) rows of K bytes in L2, and
-// B is read from DRAM num_m / group times.  The largest group of 32, 16, 8
-// whose wave stays within 48 MB (about a third of L2) is taken; 8 otherwise.
-// Measured on the GB300 (per-tensor pair kernel, 16384 x 14336 x 4096 / 8192^3
-// / 16384 x 4096 x 14336, us): group 8: 533.5 / 302.0 / 529.7; 16: 524.5 /
-// 297.5 / 532.3; 32: 522.0 / 307.8 / 552.5.  The MX kernel at 8192^3: 16:
-// 355.8, 32: 353.4, 64: 379.2.
-static int raster_group(int64_t K, int tile_m, int tile_n, int concurrent)
-{
-    for (int g = 32; g > 8; g /= 2) {
-        const int64_t rows = (int64_t)g * tile_m + (int64_t)((concurrent + g - 1) / g) * tile_n;
-        if (rows * K <= (int64_t)48 << 20) return g;
-    }
-    return 8;
-}
-
 struct EpiParams {
     int M, N, K;
     const float* sA;     // mode 0: 1 float; mode 1: [M][K/128]
@@ -113,10 +82,6 @@ struct EpiParams {
     float* qstate = nullptr;
     int qH = 0, qfmt = 0;
 };
-
-constexpr int BM = 128;
-constexpr int BK = 128;  // bytes = elements for 8-bit operands
-constexpr int A_BYTES = BM * BK;
 
 // ------------------------------------------------------------------ epilogue store
 // 32 consecutive columns of one row: v[j] is column col0 + j.
@@ -162,7 +127,6 @@ __device__ __forceinline__ void store_row32(const EpiParams& p, int row, int col
 // a fully out-of-range store never lets a pending one be overwritten.  Writing
 // whole 32-byte row segments through the TMA instead of 16-byte per-lane
 // stores halves the L2 write requests and takes the stores off the LSU.
-constexpr int kStageBytes = 1024;   // per epilogue warp
 
 template <bool OUT_BF16>
 __device__ __forceinline__ void stage_store(uint8_t* buf, const CUtensorMap* tmD, const float* v, int col0, int row0,
@@ -199,57 +163,7 @@ __device__ __forceinline__ void stage_store(uint8_t* buf, const CUtensorMap* tmD
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
-// One lane's 32-byte staging row: 16 bf16 or 8 fp32 outputs.
-template <bool OUT_BF16>
-__device__ __forceinline__ void stage_row(uint8_t* rowp, const float* v)
-{
-    if (OUT_BF16) {
-#pragma unroll
-        for (int q4 = 0; q4 < 2; ++q4) {
-            uint4 w4;
-            __nv_bfloat162 h0 = __floats2bfloat162_rn(v[8 * q4 + 0], v[8 * q4 + 1]);
-            __nv_bfloat162 h1 = __floats2bfloat162_rn(v[8 * q4 + 2], v[8 * q4 + 3]);
-            __nv_bfloat162 h2 = __floats2bfloat162_rn(v[8 * q4 + 4], v[8 * q4 + 5]);
-            __nv_bfloat162 h3 = __floats2bfloat162_rn(v[8 * q4 + 6], v[8 * q4 + 7]);
-            w4.x = *reinterpret_cast<uint32_t*>(&h0);
-            w4.y = *reinterpret_cast<uint32_t*>(&h1);
-            w4.z = *reinterpret_cast<uint32_t*>(&h2);
-            w4.w = *reinterpret_cast<uint32_t*>(&h3);
-            *reinterpret_cast<uint4*>(rowp + 16 * q4) = w4;
-        }
-    } else {
-        *reinterpret_cast<float4*>(rowp) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(rowp + 16) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-}
-// Bulk tensor store of a 32 x 32-byte staging buffer (one bulk group per call
-// site's commit).
-__device__ __forceinline__ void bulk_store_2d(const CUtensorMap* m, int x, int y, const uint8_t* buf)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(x), "r"(y), "r"(smem_addr(buf))
-                 : "memory");
-}
-
-__device__ __forceinline__ void stage_store_drain(int lane)
-{
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    __syncwarp();
-}
-
 // ------------------------------------------------------------------ shared layout
-template <int BN, int STAGES, int NACC, int EPI_STAGE_WARPS = 0>
-struct Smem {
-    static constexpr int B_BYTES = BN * BK;
-    static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int BAR_OFF = STAGES * STAGE;
-    static constexpr int NBARS = 2 * STAGES + 2 * NACC + 1;
-    static constexpr int STG_OFF = BAR_OFF + 512;                      // epilogue staging (1 KB per warp)
-    static constexpr int BYTES = STG_OFF + EPI_STAGE_WARPS * kStageBytes + 1024;   // + alignment slack
-    static_assert(NBARS * 8 + 16 <= 512, "barriers and the TMEM holder fit before the staging area");
-};
-
 // Common prologue: barriers, tensor memory, early exit if the error word is set.
 template <int STAGES, int NACC, int EPI_WARPS>
 __device__ __forceinline__ bool gemm_setup(uint8_t* smem, int bar_off, uint32_t tmem_cols,
@@ -1364,14 +1278,12 @@ bool encode_tmap_2d(CUtensorMap* m, int u16, const void* ptr, uint64_t inner, ui
     return r == CUDA_SUCCESS;
 }
 
-// 2-D u8 tensor [rows][inner] (inner contiguous), box box_rows x 128 bytes, 128-byte swizzle
-static bool make_tmap(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint32_t box_rows)
+bool make_tmap(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint32_t box_rows)
 {
     return encode_tmap_2d(m, 0, ptr, inner, rows, 128u, box_rows);
 }
 
-// instruction descriptor, kind::f8f6f4: D fp32, A/B format, both K-major, N, M = 128
-static uint32_t make_idesc(int a_fmt, int b_fmt, int n)
+uint32_t make_idesc(int a_fmt, int b_fmt, int n)
 {
     uint32_t d = 0;
     d |= 1u << 4;                       // D format: F32
@@ -1396,16 +1308,12 @@ static uint32_t make_idesc_mx(int a_fmt, int b_fmt, int n)
     return d;
 }
 
-// 2-D tensor map of the output D [M][N] for the staged epilogue stores: box
-// 32 rows x 32 bytes, no swizzle (stores clip at the matrix edge)
-// 2-D tensor map of 8-bit codes Q [M][N] for the staged code stores: box
-// 32 rows x 32 bytes, no swizzle
-static bool make_tmap_codes(CUtensorMap* m, void* Q, int64_t M, int64_t N)
+bool make_tmap_codes(CUtensorMap* m, void* Q, int64_t M, int64_t N, int64_t pitch)
 {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
-    cuuint64_t strides[1] = {(cuuint64_t)N};
+    cuuint64_t strides[1] = {(cuuint64_t)(pitch ? pitch : N)};
     cuuint32_t box[2] = {32u, 32u};
     cuuint32_t estr[2] = {1u, 1u};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, Q, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1413,13 +1321,13 @@ static bool make_tmap_codes(CUtensorMap* m, void* Q, int64_t M, int64_t N)
            CUDA_SUCCESS;
 }
 
-static bool make_tmap_out(CUtensorMap* m, void* D, int64_t M, int64_t N, bool bf16)
+bool make_tmap_out(CUtensorMap* m, void* D, int64_t M, int64_t N, bool bf16, int64_t pitch)
 {
     auto fn = encode_fn();
     if (!fn) return false;
     const uint64_t esz = bf16 ? 2 : 4;
     cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
-    cuuint64_t strides[1] = {(cuuint64_t)(N * esz)};
+    cuuint64_t strides[1] = {(cuuint64_t)((pitch ? pitch : N) * esz)};
     cuuint32_t box[2] = {(cuuint32_t)(32 / esz), 32u};
     cuuint32_t estr[2] = {1u, 1u};
     return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, D, dims, strides, box,
@@ -1610,6 +1518,27 @@ cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t st, int sms, const char*
     }
     *why = "GEMM mode not built";
     return cudaErrorNotSupported;
+}
+
+// The error word's device address, looked up once per device (the other
+// translation units' kernels report their bounded waits into the same word).
+cudaError_t device_error_word(int** word)
+{
+    static std::atomic<int*> cache[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int* w = cache[dev].load(std::memory_order_relaxed);
+    if (!w) {
+        void* p = nullptr;
+        e = cudaGetSymbolAddress(&p, g_dev_error);
+        if (e != cudaSuccess) return e;
+        w = static_cast<int*>(p);
+        cache[dev].store(w, std::memory_order_relaxed);
+    }
+    *word = w;
+    return cudaSuccess;
 }
 
 int read_device_error(int clear)

@@ -73,6 +73,8 @@ struct GemmArgs {
 cudaError_t launch_gemm(const GemmArgs& g, cudaStream_t st, int sms, const char** why);
 // Raises a kernel's dynamic shared-memory limit to `bytes`, once per device.
 cudaError_t smem_attr_once(const void* kern, int bytes);
+// device address of the GEMM kernels' error word on the current device
+cudaError_t device_error_word(int** word);
 int gemm_ctas(const GemmArgs& g, int sms);   // SMs its persistent grid occupies, -1 if unknown
 int read_device_error(int clear);   // 0 or the GEMM kernels' device error word
 // launches a kernel whose bounded wait is made to run out (failure-path test)
@@ -81,6 +83,73 @@ cudaError_t launch_selftest_wait(uint64_t limit_ns, int* waited_out, cudaStream_
 // 2-byte elements (else 1-byte)
 bool encode_tmap_2d(CUtensorMap* m, int u16, const void* ptr, uint64_t inner, uint64_t rows, uint32_t box_inner,
                     uint32_t box_rows);
+
+// ffn.cu: products with their elementwise work in the epilogue (per-tensor scales)
+enum { kFfnAct = 0, kFfnGlu = 1, kFfnGluBwd = 2 };
+struct FfnArgs {
+    int kind = kFfnAct;
+    int64_t M = 0, N = 0, K = 0;     // N: output columns (glu: features F, B is [2F][K]; glu_bwd: B is [K][F])
+    const uint8_t* A = nullptr;
+    const uint8_t* B = nullptr;
+    int a_format = kE4M3, b_format = kE4M3;
+    const float* a_scale = nullptr;
+    const float* b_scale = nullptr;
+    int act = 0;
+    const float* bias = nullptr;
+    const void* residual = nullptr;
+    int res_dtype = kBF16;
+    void* D = nullptr;
+    int d_dtype = kBF16;
+    void* Z = nullptr;               // bf16 [M][N] (glu: [M][2F])
+    const void* gu = nullptr;        // glu_bwd: bf16 [M][2F]
+    uint8_t* q_out = nullptr;        // [M][N] (glu_bwd: [M][2F])
+    int q_format = kE4M3;
+    float* q_state = nullptr;
+    int q_history_len = 0;
+    void* workspace = nullptr;       // ffn_workspace bytes, or null
+};
+size_t ffn_workspace(int kind, int64_t M, int64_t N, int64_t K);
+cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** why);
+
+// rowops.cu: LayerNorm forward / backward, the elementwise backward of an
+// activation with its bias gradient
+struct LnArgs {
+    int64_t M = 0, K = 0;
+    int dtype = kBF16;               // of x, residual, sum, y, dy, dres, dx
+    const void* x = nullptr;
+    const float* gamma = nullptr;
+    const float* beta = nullptr;
+    float eps = 0.0f;
+    const void* residual = nullptr;  // forward: added to x
+    void* sum = nullptr;             // forward: x + residual as rounded
+    void* y = nullptr;
+    float* mu = nullptr;
+    float* rstd = nullptr;
+    const void* dy = nullptr;        // backward
+    const void* dres = nullptr;
+    void* dx = nullptr;
+    float* dgamma = nullptr;
+    float* dbeta = nullptr;
+    void* workspace = nullptr;
+};
+cudaError_t launch_layernorm_fwd(const LnArgs& a, cudaStream_t st, int sms);
+cudaError_t launch_layernorm_bwd(const LnArgs& a, cudaStream_t st, int sms);
+size_t layernorm_bwd_workspace(int64_t M, int64_t K);
+struct ActBwdArgs {
+    int64_t M = 0, N = 0;
+    const void* dy = nullptr;        // bf16
+    const void* z = nullptr;         // bf16
+    int act = 0;
+    float* dbias = nullptr;
+    void* dz = nullptr;              // bf16 or null
+    uint8_t* q = nullptr;
+    int q_format = kE5M2;
+    float* q_state = nullptr;
+    int q_history_len = 0;
+    void* workspace = nullptr;
+};
+cudaError_t launch_act_bwd(const ActBwdArgs& a, cudaStream_t st, int sms);
+size_t act_bwd_workspace(int64_t M, int64_t N);
 
 // api.cu: the calling thread's error message and the sm_103 device check
 int api_fail(int code, const char* fmt, ...);
