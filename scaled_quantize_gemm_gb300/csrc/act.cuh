@@ -1,8 +1,10 @@
 // act.cuh -- activations and their derivatives in fp32, for the epilogues and
-// the elementwise backward pass.
+// the elementwise backward pass.  Two elements at a time: the multiplies and
+// adds are packed f32x2 instructions, half the issue slots of two scalar ones
+// (the elementwise backward pass is bound by issue slots next to DRAM).
 //
 //   relu       max(x, 0)                       derivative 1 for x > 0, else 0
-//   gelu       x Phi(x), Phi = (1 + erf(x / sqrt 2)) / 2
+//   gelu       x Phi(x), Phi the normal distribution function
 //   gelu_tanh  (x / 2) (1 + tanh t), t = sqrt(2 / pi) (x + 0.044715 x^3)
 //   silu       x / (1 + exp(-x))
 // (1 + tanh t) / 2 is the logistic function of 2 t, so gelu_tanh and silu are
@@ -10,7 +12,11 @@
 // s takes the hardware exponential and reciprocal: a few units of 2^-24
 // beside the argument's own rounding, far below half a step of any stored
 // type but fp32, and 1 - s is formed from exp(-u) itself, so it keeps its
-// relative precision where s is near 1.  A NaN goes through every form.
+// relative precision where s is near 1.
+// Phi takes formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions (1964): erfc(y) = (a1 t + ... + a5 t^5) exp(-y^2), t = 1 / (1 + p y),
+// y >= 0, absolute error at most 1.5e-7; its exponential is the one the
+// derivative's density needs.  A NaN goes through every form.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -38,54 +44,112 @@ __device__ __forceinline__ void act_dispatch(int act, F&& f)
     }
 }
 
-constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
-constexpr float kGeluB = 0.044715f;
-
-// logistic argument u(x) of the two sigmoid forms
-template <int ACT>
-__device__ __forceinline__ float act_u(float x)
+__device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float ex2_approx(float v)
 {
-    if constexpr (ACT == kActSilu) return x;
-    else return kGeluA * x * fmaf(kGeluB * x, x, 1.0f);
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float2 ex2_2(float2 v) { return make_float2(ex2_approx(v.x), ex2_approx(v.y)); }
+__device__ __forceinline__ float2 rcp_2(float2 v) { return make_float2(rcp_approx(v.x), rcp_approx(v.y)); }
+// bounds that a NaN passes through
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 max2_nan(float2 a, float b) { return make_float2(max_nan(a.x, b), max_nan(a.y, b)); }
+__device__ __forceinline__ float2 min2_nan(float2 a, float b) { return make_float2(min_nan(a.x, b), min_nan(a.y, b)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluA = 1.5957691216057308f;          // 2 sqrt(2 / pi): u = A x (1 + B x^2)
+constexpr float kGeluB = 0.044715f;
+constexpr float kErfP = 0.3275911f;                    // Abramowitz and Stegun 7.1.26
+constexpr float kErfA1 = 0.254829592f, kErfA2 = -0.284496736f, kErfA3 = 1.421413741f, kErfA4 = -1.453152027f,
+                kErfA5 = 1.061405429f;
+
+// exp(-u(x)) of the two sigmoid forms (2 to the scaled argument)
+template <int ACT>
+__device__ __forceinline__ float2 act_exp(float2 x, float2 xx)
+{
+    if constexpr (ACT == kActSilu) return ex2_2(__fmul2_rn(x, f2(-kLog2e)));
+    else return ex2_2(__fmul2_rn(x, __ffma2_rn(xx, f2(-kLog2e * kGeluA * kGeluB), f2(-kLog2e * kGeluA))));
+}
+
+// Phi(x) and exp(-x^2 / 2)
+__device__ __forceinline__ float2 normal_cdf(float2 x, float2& ex)
+{
+    const float2 ax = make_float2(fabsf(x.x), fabsf(x.y));
+    ex = ex2_2(__fmul2_rn(__fmul2_rn(x, x), f2(-0.5f * kLog2e)));
+    const float2 t = rcp_2(__ffma2_rn(ax, f2(kErfP * 0.70710678118654752f), f2(1.0f)));
+    float2 p = __ffma2_rn(t, f2(0.5f * kErfA5), f2(0.5f * kErfA4));
+    p = __ffma2_rn(p, t, f2(0.5f * kErfA3));
+    p = __ffma2_rn(p, t, f2(0.5f * kErfA2));
+    p = __ffma2_rn(p, t, f2(0.5f * kErfA1));
+    p = __fmul2_rn(__fmul2_rn(p, t), ex);              // Phi(-|x|)
+    return make_float2(x.x > 0.0f ? 1.0f - p.x : p.x, x.y > 0.0f ? 1.0f - p.y : p.y);
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_f(float x)
+__device__ __forceinline__ float2 act_f2(float2 x)
 {
     if constexpr (ACT == kActNone) return x;
-    else if constexpr (ACT == kActRelu) return x > 0.0f ? x : (x != x ? x : 0.0f);
-    else if constexpr (ACT == kActGelu) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
-    // exp(-u) = inf (u below -88) gives x / inf = -0, the limit
-    else return __fdividef(x, 1.0f + __expf(-act_u<ACT>(x)));
+    else if constexpr (ACT == kActRelu) return max2_nan(x, 0.0f);
+    else if constexpr (ACT == kActGelu) {
+        float2 ex;
+        return __fmul2_rn(x, normal_cdf(x, ex));
+    } else {
+        // exp(-u) = inf (u far below 0) gives x * 0 = -0, the limit
+        const float2 e = act_exp<ACT>(x, __fmul2_rn(x, x));
+        return __fmul2_rn(x, rcp_2(__fadd2_rn(e, f2(1.0f))));
+    }
 }
 
 // f = act(x), d = act'(x)
 template <int ACT>
-__device__ __forceinline__ void act_fd(float x, float& f, float& d)
+__device__ __forceinline__ void act_fd2(float2 x, float2& f, float2& d)
 {
     if constexpr (ACT == kActNone) {
         f = x;
-        d = 1.0f;
+        d = f2(1.0f);
     } else if constexpr (ACT == kActRelu) {
-        f = act_f<ACT>(x);
-        d = x > 0.0f ? 1.0f : (x != x ? x : 0.0f);
+        f = max2_nan(x, 0.0f);
+        d = make_float2(x.x > 0.0f ? 1.0f : (x.x != x.x ? x.x : 0.0f), x.y > 0.0f ? 1.0f : (x.y != x.y ? x.y : 0.0f));
     } else if constexpr (ACT == kActGelu) {
-        const float phi = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
-        f = x * phi;
-        d = fmaf(x * 0.3989422804014327f, __expf(-0.5f * x * x), phi);
+        float2 ex;
+        const float2 phi = normal_cdf(x, ex);
+        f = __fmul2_rn(x, phi);
+        // |x| <= 40 in the second term (0 there): x exp(-x^2 / 2) stays finite
+        const float2 xc = min2_nan(max2_nan(x, -40.0f), 40.0f);
+        d = __ffma2_rn(__fmul2_rn(xc, f2(0.3989422804014327f)), ex, phi);
     } else {
-        // below u = -87 the value and the derivative are under 2^-118: taken as
-        // 0 before u' can overflow against them (u' only grows as x^2)
-        const float u = act_u<ACT>(x);
-        const float e = __expf(-u);
-        const float s = u < -87.0f ? 0.0f : __fdividef(1.0f, 1.0f + e);
-        const float xs = x * s;
-        f = xs;
-        float up;
-        if constexpr (ACT == kActSilu) up = 1.0f;
-        else up = kGeluA * fmaf(3.0f * kGeluB * x, x, 1.0f);
-        // 1 - s = e s; for large u e is 0 and the derivative s = 1
-        d = e == 0.0f || s == 0.0f ? s : fmaf(xs * (e * s), up, s);
+        // At |x| = C the value on the negative side and the derivative's
+        // distance from 0 or 1 are below 2^-102: x is held there, so that
+        // exp(-u) stays finite and u', which grows as x^2, meets no 0 * inf.
+        constexpr float C = ACT == kActSilu ? 80.0f : 9.5f;
+        const float2 xn = max2_nan(x, -C);
+        const float2 xc = min2_nan(xn, C);
+        const float2 xx = __fmul2_rn(xc, xc);
+        const float2 e = act_exp<ACT>(xc, xx);
+        const float2 s = rcp_2(__fadd2_rn(e, f2(1.0f)));
+        f = __fmul2_rn(xn, s);
+        float2 t = __fmul2_rn(__fmul2_rn(xc, s), __fmul2_rn(e, s));        // x s (1 - s)
+        if constexpr (ACT == kActSilu) d = __fadd2_rn(t, s);
+        else d = __ffma2_rn(t, __ffma2_rn(xx, f2(3.0f * kGeluA * kGeluB), f2(kGeluA)), s);
     }
 }
 

@@ -310,7 +310,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                         }
                         act_dispatch(p.act, [&](auto tag) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] *= act_f<decltype(tag)::act>(g[j]);
+                            for (int j = 0; j < 32; j += 2) {
+                                const float2 h = __fmul2_rn(make_float2(v[j], v[j + 1]),
+                                                            act_f2<decltype(tag)::act>(make_float2(g[j], g[j + 1])));
+                                v[j] = h.x;
+                                v[j + 1] = h.y;
+                            }
                         });
                         if (p.D) store32_bf16(static_cast<__nv_bfloat16*>(p.D) + (int64_t)row * p.N + col, left, v);
                         if (p.Q) {
@@ -340,7 +345,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                             if (p.Z) store32_bf16(p.Z + (int64_t)row * p.N + col, left, v);
                             act_dispatch(p.act, [&](auto tag) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = act_f<decltype(tag)::act>(v[j]);
+                                for (int j = 0; j < 32; j += 2) {
+                                    const float2 y = act_f2<decltype(tag)::act>(make_float2(v[j], v[j + 1]));
+                                    v[j] = y.x;
+                                    v[j + 1] = y.y;
+                                }
                             });
                             if (p.res) {
                                 if (p.res_f32) {
@@ -376,11 +385,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                             load32_bf16(s + p.N, left, w);
                             act_dispatch(p.act, [&](auto tag) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    float f, d;
-                                    act_fd<decltype(tag)::act>(g[j], f, d);
-                                    g[j] = v[j] * w[j] * d;
-                                    w[j] = v[j] * f;
+                                for (int j = 0; j < 32; j += 2) {
+                                    float2 f, d;
+                                    act_fd2<decltype(tag)::act>(make_float2(g[j], g[j + 1]), f, d);
+                                    const float2 dh = make_float2(v[j], v[j + 1]);
+                                    const float2 dg = __fmul2_rn(__fmul2_rn(dh, make_float2(w[j], w[j + 1])), d);
+                                    const float2 du = __fmul2_rn(dh, f);
+                                    g[j] = dg.x;
+                                    g[j + 1] = dg.y;
+                                    w[j] = du.x;
+                                    w[j + 1] = du.y;
                                 }
                             });
                             max32(amax, g, left);
@@ -407,6 +421,331 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+// ================================================================== few rows
+// Up to 64 rows (serving: single tokens and small batches): the time is the
+// weights' bytes, so the roles are swapped -- 128 weight rows are the M of
+// the MMA and the tokens, padded to NT, its N -- and the K loop is split over
+// all SMs.  The work is the list of (weight tile, 128-wide K block) pairs in
+// tile order; CTA i of G takes the i-th G-th of it, so every SM streams the
+// same number of bytes whatever the sizes, and a tile's K range belongs to
+// one or a few neighbouring CTAs.  A CTA that holds all of a tile's K blocks
+// finishes it from tensor memory; otherwise each writes its fp32 partial sums
+// to the workspace and the last one to arrive (a counter per tile, which it
+// sets back to 0) adds them in CTA order, so the result does not depend on
+// the order of arrival, and runs the epilogue.  No CTA waits for another.
+// glu: a stage holds the gate and the up rows of 128 features, accumulated in
+// two column ranges of the same lanes, so a thread holds both.
+//   warp 0 producer, warp 1 MMA, warps 2-5 epilogue (TMEM lane = weight row)
+constexpr int kRowsThreads = 192;
+constexpr int kRowsMaxM = 64;
+constexpr int kRowsMaxCtas = 192;                 // partial slots in the workspace
+constexpr int kRowsMaxTiles = 16384;              // counters in the workspace
+constexpr size_t kRowsCounterBytes = kRowsMaxTiles * sizeof(uint32_t);
+
+template <int KIND, int NT>
+struct RowsLayout {
+    static constexpr int NW = KIND == kEpiGlu ? 2 : 1;                  // weight tiles per stage
+    static constexpr int STAGE = NW * A_BYTES + NT * BK;
+    static constexpr int STAGES = (200 * 1024) / STAGE;
+    static constexpr int BAR_OFF = STAGES * STAGE;
+    static constexpr int BYTES = BAR_OFF + 512 + 1024;
+    static constexpr int ACC = NW * NT;                                  // columns of one accumulator
+    static constexpr uint32_t TMEM_COLS = 2 * ACC < 32 ? 32 : 2 * ACC;
+    static_assert((2 * STAGES + 5) * 8 + 8 <= 512, "barriers");
+};
+
+struct RowsParams {
+    int tiles, nkb, split;
+    uint32_t* counters;
+    float* part;              // [CTA][2][NW * NT][128]
+};
+
+// first work item of CTA i
+__device__ __forceinline__ int rows_start(const RowsParams& w, int i)
+{
+    const int64_t g = gridDim.x;
+    if (!w.split) return (int)((int64_t)i * w.tiles / g) * w.nkb;
+    return (int)((int64_t)i * ((int64_t)w.tiles * w.nkb) / g);
+}
+// the CTA that holds work item u (split work)
+__device__ __forceinline__ int rows_owner(const RowsParams& w, int u)
+{
+    return (int)((((int64_t)u + 1) * gridDim.x - 1) / ((int64_t)w.tiles * w.nkb));
+}
+
+template <int KIND, int NT>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    k_ffn_rows(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, FfnParams p,
+               RowsParams w, uint32_t idesc)
+{
+    pdl_enter();
+    using L = RowsLayout<KIND, NT>;
+    constexpr int STAGES = L::STAGES, NW = L::NW, ACC = L::ACC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* empty = full + STAGES;
+    uint64_t* afull = empty + STAGES;
+    uint64_t* aempty = afull + 2;
+    uint64_t* drain = aempty + 2;
+    uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
+    __shared__ int s_skip;
+    __shared__ int s_last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        s_skip = *reinterpret_cast<volatile int*>(p.err);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&afull[b], 1);
+            mbar_init(&aempty[b], 4);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmX);
+    }
+    __syncthreads();
+    if (s_skip) return;
+    if (warp == 1) {
+        tmem_alloc(holder, L::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *holder;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err(bar, parity, p.err); };
+    const int u0 = rows_start(w, blockIdx.x), u1 = rows_start(w, blockIdx.x + 1);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool aborted = false;
+            int tile = u0 / w.nkb, kb = u0 - tile * w.nkb;
+            for (int u = u0; u < u1; ++u) {
+                if (!wait(&empty[stage], phase ^ 1u)) {
+                    aborted = true;
+                    break;
+                }
+                uint8_t* sw = smem + stage * L::STAGE;
+                mbar_arrive_expect_tx(&full[stage], (uint32_t)L::STAGE);
+                tma_load_2d(sw, &tmW, kb * BK, tile * BM, &full[stage]);
+                if (NW == 2) tma_load_2d(sw + A_BYTES, &tmW, kb * BK, p.N + tile * BM, &full[stage]);
+                tma_load_2d(sw + NW * A_BYTES, &tmX, kb * BK, 0, &full[stage]);
+                ++issued;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++kb == w.nkb) {
+                    kb = 0;
+                    ++tile;
+                }
+            }
+            if (aborted) {
+                // wait for the copies still in flight before the CTA can exit
+                int n = issued < STAGES ? issued : STAGES;
+                int s = stage;
+                uint32_t ph = phase;
+                for (int i = 0; i < n; ++i) {
+                    if (--s < 0) {
+                        s = STAGES - 1;
+                        ph ^= 1u;
+                    }
+                    wait_drain(&full[s], ph);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, seg = 0;
+            uint32_t phase = 0;
+            bool aborted = false;
+            for (int u = u0; u < u1 && !aborted; ++seg) {
+                const int b = seg & 1;
+                const int end = min(u1, (u / w.nkb + 1) * w.nkb);
+                if (!wait(&aempty[b], ((uint32_t)(seg >> 1) & 1u) ^ 1u)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)(b * ACC);
+                for (uint32_t first = 0; u < end; ++u) {
+                    if (!wait(&full[stage], phase)) {
+                        aborted = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sw = smem_addr(smem + stage * L::STAGE);
+                    const uint64_t dx = sdesc_kmajor_sw128(sw + NW * A_BYTES);
+#pragma unroll
+                    for (int h = 0; h < NW; ++h) {
+                        const uint64_t dw = sdesc_kmajor_sw128(sw + h * A_BYTES);
+#pragma unroll
+                        for (int k = 0; k < BK / 32; ++k)
+                            mma_f8f6f4(d + h * NT, dw + 2 * k, dx + 2 * k, idesc, k != 0 ? 1u : first);
+                    }
+                    first = 1;
+                    mma_commit(&empty[stage]);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!aborted) mma_commit(&afull[b]);
+            }
+            if (aborted) {
+                mma_commit(drain);
+                wait_drain(drain, 0);
+            }
+        }
+    } else {
+        const int quarter = warp & 3;
+        const int wr = quarter * 32 + lane;                 // weight row within the tile
+        const float scale = __ldg(p.sA) * __ldg(p.sB);
+        const float qm = p.Q ? p.qstate[p.qH] : 1.0f;
+        uint32_t amax = 0;
+        int seg = 0;
+        for (int u = u0; u < u1; ++seg) {
+            const int b = seg & 1;
+            const int tile = u / w.nkb, kb0 = u - tile * w.nkb;
+            const int end = min(u1, (tile + 1) * w.nkb);
+            const bool whole = kb0 == 0 && end == (tile + 1) * w.nkb;
+            u = end;
+            if (!bar_all(1, 128, wait(&afull[b], (uint32_t)(seg >> 1) & 1u))) break;
+            tc_fence_after();
+            float acc[ACC];
+            {
+                uint32_t r[ACC];
+                const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * ACC);
+#pragma unroll
+                for (int c = 0; c < ACC; c += 16) tmem_ld_32x32b_x16(taddr + c, r + c);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < ACC; ++c) acc[c] = __uint_as_float(r[c]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aempty[b]);
+            if (!whole) {
+                float* mine = w.part + ((int64_t)blockIdx.x * 2 + (kb0 == 0 ? 1 : 0)) * (ACC * 128) + wr;
+#pragma unroll
+                for (int c = 0; c < ACC; ++c)
+                    if (c % NT < p.M) __stcg(mine + c * 128, acc[c]);
+                const int c0 = rows_owner(w, tile * w.nkb), c1 = rows_owner(w, (tile + 1) * w.nkb - 1);
+                __threadfence();
+                bar_all(1, 128, true);
+                if (threadIdx.x == 64) {
+                    const uint32_t n = (uint32_t)(c1 - c0);
+                    const bool last = atomicAdd(&w.counters[tile], 1u) == n;
+                    if (last) w.counters[tile] = 0;
+                    s_last = last;
+                }
+                bar_all(1, 128, true);
+                if (!s_last) continue;
+                __threadfence();
+                for (int c = c0; c <= c1; ++c) {
+                    const float* src = w.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * (ACC * 128) + wr;
+#pragma unroll
+                    for (int j = 0; j < ACC; ++j) {
+                        if (j % NT < p.M) {
+                            const float v = __ldcg(src + j * 128);
+                            acc[j] = c == c0 ? v : acc[j] + v;
+                        }
+                    }
+                }
+            }
+            const int n = tile * BM + wr;
+            if (n < p.N) {
+                if constexpr (KIND == kEpiAct) {
+                    const float bias = p.bias ? __ldg(p.bias + n) : 0.0f;
+#pragma unroll
+                    for (int m = 0; m < NT; ++m)
+                        if (m < p.M) {
+                            acc[m] = acc[m] * scale;
+                            if (p.bias) acc[m] += bias;
+                            if (p.Z) p.Z[(int64_t)m * p.N + n] = __float2bfloat16_rn(acc[m]);
+                        }
+                    act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int m = 0; m < NT; m += 2)
+                            if (m < p.M) {
+                                const float2 y = act_f2<decltype(tag)::act>(make_float2(acc[m], m + 1 < p.M ? acc[m + 1] : 0.0f));
+                                acc[m] = y.x;
+                                acc[m + 1] = y.y;
+                            }
+                    });
+#pragma unroll
+                    for (int m = 0; m < NT; ++m)
+                        if (m < p.M) {
+                            const int64_t o = (int64_t)m * p.N + n;
+                            if (p.res) acc[m] += p.res_f32 ? __ldg(static_cast<const float*>(p.res) + o)
+                                                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[o]);
+                            if (p.D) {
+                                if (p.d_f32) static_cast<float*>(p.D)[o] = acc[m];
+                                else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(acc[m]);
+                            }
+                        }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < NT; ++m)
+                        if (m < p.M) {
+                            acc[m] *= scale;
+                            acc[NT + m] *= scale;
+                            if (p.Z) {
+                                __nv_bfloat16* z = p.Z + (int64_t)m * 2 * p.N + n;
+                                z[0] = __float2bfloat16_rn(acc[m]);
+                                z[p.N] = __float2bfloat16_rn(acc[NT + m]);
+                            }
+                        }
+                    act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int m = 0; m < NT; m += 2)
+                            if (m < p.M) {
+                                const bool two = m + 1 < p.M;
+                                const float2 h = __fmul2_rn(
+                                    make_float2(acc[NT + m], two ? acc[NT + m + 1] : 0.0f),
+                                    act_f2<decltype(tag)::act>(make_float2(acc[m], two ? acc[m + 1] : 0.0f)));
+                                acc[m] = h.x;
+                                acc[m + 1] = h.y;
+                            }
+                    });
+                    if (p.D) {
+#pragma unroll
+                        for (int m = 0; m < NT; ++m)
+                            if (m < p.M)
+                                static_cast<__nv_bfloat16*>(p.D)[(int64_t)m * p.N + n] = __float2bfloat16_rn(acc[m]);
+                    }
+                }
+                if (p.Q) {
+#pragma unroll
+                    for (int m = 0; m < NT; ++m)
+                        if (m < p.M) {
+                            amax = max(amax, abs_bits(acc[m]));
+                            const float v = __fmul_rn(acc[m], qm);
+                            p.Q[(int64_t)m * p.N + n] =
+                                (uint8_t)(p.qfmt == kE4M3 ? cvt_e4m3x2(v, 0.0f) : cvt_e5m2x2(v, 0.0f));
+                        }
+                }
+            }
+            __syncwarp();
+        }
+        if (p.Q) {
+            amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+            if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.qstate), amax);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, L::TMEM_COLS);
     }
 }
 
@@ -448,19 +787,61 @@ static cudaError_t ffn_clusters(const void* kern, int kind, int* clusters)
     return cudaSuccess;
 }
 
+static int rows_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+// the split of few rows over K applies: bytes of its counters and partial sums
 size_t ffn_workspace(int kind, int64_t M, int64_t N, int64_t K)
 {
-    (void)kind;
-    (void)M;
-    (void)N;
     (void)K;
-    return 0;
+    if (M > kRowsMaxM || (N + BM - 1) / BM > kRowsMaxTiles) return 0;
+    const int acc = (kind == kFfnGlu ? 2 : 1) * rows_nt(M);
+    return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * acc * 128 * sizeof(float);
+}
+
+template <int KIND, int NT>
+static cudaError_t launch_rows(const FfnArgs& a, const FfnParams& p, cudaStream_t st, int sms, const char** why)
+{
+    using L = RowsLayout<KIND, NT>;
+    CUtensorMap tw, tx;
+    if (!make_tmap(&tw, a.B, a.K, L::NW * a.N, BM) || !make_tmap(&tx, a.A, a.K, a.M, NT)) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+    RowsParams w = {};
+    w.tiles = (int)((a.N + BM - 1) / BM);
+    w.nkb = (int)((a.K + BK - 1) / BK);
+    const int64_t work = (int64_t)w.tiles * w.nkb;
+    w.split = a.workspace != nullptr;
+    int64_t grid = sms < kRowsMaxCtas ? sms : kRowsMaxCtas;
+    if (w.split) {
+        w.counters = static_cast<uint32_t*>(a.workspace);
+        w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kRowsCounterBytes);
+        // at least four K blocks a CTA: below that the join costs more than the split saves
+        const int64_t most = (work + 3) / 4;
+        grid = grid < most ? grid : most;
+    } else {
+        grid = grid < w.tiles ? grid : w.tiles;
+    }
+    auto kern = k_ffn_rows<KIND, NT>;
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), L::BYTES);
+    if (e != cudaSuccess) return e;
+    launch_k(kern, (unsigned)grid, kRowsThreads, L::BYTES, st, tw, tx, p, w, make_idesc(a.b_format, a.a_format, NT));
+    return cudaGetLastError();
+}
+
+template <int KIND>
+static cudaError_t launch_rows_nt(const FfnArgs& a, const FfnParams& p, cudaStream_t st, int sms, const char** why)
+{
+    switch (rows_nt(a.M)) {
+    case 16: return launch_rows<KIND, 16>(a, p, st, sms, why);
+    case 32: return launch_rows<KIND, 32>(a, p, st, sms, why);
+    default: return launch_rows<KIND, 64>(a, p, st, sms, why);
+    }
 }
 
 cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** why)
 {
     *why = nullptr;
-    (void)sms;
     if (a.M == 0 || a.N == 0) return cudaSuccess;
     FfnParams p = {};
     p.M = (int)a.M;
@@ -483,6 +864,8 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     cudaError_t e = device_error_word(&p.err);
     if (e != cudaSuccess) return e;
     const bool glu = a.kind == kFfnGlu, bwd = a.kind == kFfnGluBwd;
+    if (!bwd && ffn_workspace(a.kind, a.M, a.N, a.K) != 0 && (int64_t)((a.N + BM - 1) / BM) * ((a.K + BK - 1) / BK) < ((int64_t)1 << 31))
+        return glu ? launch_rows_nt<kEpiGlu>(a, p, st, sms, why) : launch_rows_nt<kEpiAct>(a, p, st, sms, why);
     CUtensorMap ta, tb;
     const bool ok_b = bwd ? make_tmap(&tb, a.B, a.N, a.K, BK) : make_tmap(&tb, a.B, a.K, glu ? 2 * a.N : a.N, kFfnBH);
     if (!make_tmap(&ta, a.A, a.K, a.M, BM) || !ok_b) {

@@ -169,9 +169,9 @@ __global__ void __launch_bounds__(256) k_act_bwd_any(const __nv_bfloat16* __rest
     if (c < N)
         act_dispatch(act, [&](auto tag) {
             for (int64_t r = blockIdx.y; r < R; r += gridDim.y) {
-                float f, d;
-                act_fd<decltype(tag)::act>(to_f(z[r * N + c]), f, d);
-                d = __fmul_rn(d, to_f(dy[r * N + c]));   // dz itself is summed, whatever else is stored
+                float2 f2_, d2;
+                act_fd2<decltype(tag)::act>(f2(to_f(z[r * N + c])), f2_, d2);
+                float d = __fmul_rn(d2.x, to_f(dy[r * N + c]));   // dz itself is summed, whatever else is stored
                 sum += d;
                 if (dz) dz[r * N + c] = __float2bfloat16_rn(d);
                 if (q) {
@@ -188,12 +188,418 @@ __global__ void __launch_bounds__(256) k_act_bwd_any(const __nv_bfloat16* __rest
     }
 }
 
+// ------------------------------------------------------------------ vectors
+// VEC consecutive elements of T as floats.  ALIGNED vectors are 16, 8, 4 or 2
+// bytes: the widest that divides a row.
+template <int BYTES>
+struct RawVec;
+template <>
+struct RawVec<16> { using type = uint4; };
+template <>
+struct RawVec<8> { using type = uint2; };
+template <>
+struct RawVec<4> { using type = uint32_t; };
+template <>
+struct RawVec<2> { using type = uint16_t; };
+
+template <typename T, int VEC>
+struct Pack {
+    using Raw = typename RawVec<sizeof(T) * VEC>::type;
+    static __device__ __forceinline__ void to_floats(const Raw& raw, float (&v)[VEC])
+    {
+        const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = to_f(e[j]);
+    }
+    static __device__ __forceinline__ Raw from_floats(const float (&v)[VEC])
+    {
+        Raw raw;
+        T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) e[j] = from_f<T>(v[j]);
+        return raw;
+    }
+};
+// fp32 parameters of VEC consecutive columns
+template <int VEC>
+__device__ __forceinline__ void load_param(const float* __restrict__ p, int c, float (&v)[VEC])
+{
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(p + c + j));
+            v[j] = w.x;
+            v[j + 1] = w.y;
+            v[j + 2] = w.z;
+            v[j + 3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = __ldg(p + c + j);
+    }
+}
+// Sum over the warps of a CTA, the same bits in every thread; `red` holds one
+// float a warp and is not written again before another barrier.
+__device__ __forceinline__ float block_total(const float* red, int warps)
+{
+    const int lane = threadIdx.x & 31;
+    return warp_sum(lane < warps ? red[lane] : 0.0f);
+}
+
+// ------------------------------------------------------------------ LayerNorm forward
+// A CTA takes one row at a time and holds it in registers (16 columns a
+// thread) from the sum to the output, so x and the residual are read once and
+// y (and the sum) written once; no row is prefetched, the loads of a CTA's
+// row overlap the reductions of the others on its SM.
+constexpr int kLnCols = 16;         // columns a thread holds
+template <typename T, int VEC>
+__global__ void __launch_bounds__(1024) k_ln_fwd(const T* __restrict__ x, const T* __restrict__ res,
+                                                 const float* __restrict__ gamma, const float* __restrict__ beta,
+                                                 float eps, int64_t R, int K, T* __restrict__ sum, T* __restrict__ y,
+                                                 float* __restrict__ mu, float* __restrict__ rstd)
+{
+    pdl_enter();
+    constexpr int NV = kLnCols / VEC;
+    using P = Pack<T, VEC>;
+    using Raw = typename P::Raw;
+    __shared__ float red[2][32];
+    const int t = threadIdx.x, nt = blockDim.x, warp = t >> 5, warps = nt >> 5;
+    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+        const int64_t base = r * K;
+        float v[NV][VEC];
+        Raw raw[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + t) * VEC;
+            if (c < K) raw[i] = *reinterpret_cast<const Raw*>(x + base + c);
+            else raw[i] = Raw{};
+        }
+        if (res) {
+            Raw rr[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + t) * VEC;
+                if (c < K) rr[i] = *reinterpret_cast<const Raw*>(res + base + c);
+                else rr[i] = Raw{};
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + t) * VEC;
+                float w[VEC];
+                P::to_floats(raw[i], v[i]);
+                P::to_floats(rr[i], w);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] += w[j];
+                raw[i] = P::from_floats(v[i]);          // the sum as stored
+                if (c < K) *reinterpret_cast<Raw*>(sum + base + c) = raw[i];
+            }
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            P::to_floats(raw[i], v[i]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s += v[i][j];
+        }
+        s = warp_sum(s);
+        if (warps > 1) {
+            if ((t & 31) == 0) red[0][warp] = s;
+            __syncthreads();
+            s = block_total(red[0], warps);
+        }
+        const float mean = s / (float)K;
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = (i * nt + t) * VEC < K;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                v[i][j] -= mean;
+                if (in) s = fmaf(v[i][j], v[i][j], s);
+            }
+        }
+        s = warp_sum(s);
+        if (warps > 1) {
+            if ((t & 31) == 0) red[1][warp] = s;
+            __syncthreads();
+            s = block_total(red[1], warps);
+        }
+        const float rs = 1.0f / sqrtf(s / (float)K + eps);
+        if (t == 0) {
+            if (mu) mu[r] = mean;
+            if (rstd) rstd[r] = rs;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + t) * VEC;
+            if (c >= K) continue;
+            float g[VEC], b[VEC] = {};
+            load_param<VEC>(gamma, c, g);
+            if (beta) load_param<VEC>(beta, c, b);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) g[j] = fmaf(v[i][j] * rs, g[j], b[j]);
+            *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(g);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ LayerNorm backward
+// A CTA takes rows r = blockIdx.x, + gridDim.x, ... and each thread the same
+// (up to) 16 columns of every row, so dgamma and dbeta accumulate in its
+// registers and go to the workspace once per CTA.  x, dy and dres of the next
+// STAGES - 1 rows are in flight (cp.async) while a row is worked on: a thread
+// copies exactly the elements that it will read, so the ring needs no barrier
+// and no wait on another thread, and a row costs one barrier, for its two sums.
+__device__ __forceinline__ void cp_async4(void* s, const void* g)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s)), "l"(g) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename Raw>
+__device__ __forceinline__ void stage_vec(Raw* s, const void* g)
+{
+    if constexpr (sizeof(Raw) == 16) cp_async16(s, g);
+    else if constexpr (sizeof(Raw) == 4) cp_async4(s, g);
+    else *s = *static_cast<const Raw*>(g);       // 2 bytes: below cp.async's smallest size
+}
+
+template <typename T, int VEC, int STAGES>
+__global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const T* __restrict__ x,
+                                                 const T* __restrict__ dres, const float* __restrict__ gamma,
+                                                 const float* __restrict__ mu, const float* __restrict__ rstd,
+                                                 int64_t R, int K, T* __restrict__ dx, float* __restrict__ part)
+{
+    pdl_enter();
+    constexpr int NV = kLnCols / VEC;
+    using P = Pack<T, VEC>;
+    using Raw = typename P::Raw;
+    extern __shared__ __align__(16) uint8_t ln_ring[];
+    __shared__ float red[2][2][32];
+    const int t = threadIdx.x, nt = blockDim.x, warp = t >> 5, warps = nt >> 5;
+    const int narr = dres ? 3 : 2;
+    // [stage][array][vector i][thread]
+    Raw* ring = reinterpret_cast<Raw*>(ln_ring);
+    auto slot = [&](int st, int arr, int i) -> Raw* { return ring + ((st * narr + arr) * NV + i) * nt + t; };
+    auto stage = [&](int st, int64_t r) {
+        if (r < R) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + t) * VEC;
+                if (c < K) {
+                    stage_vec(slot(st, 0, i), x + r * K + c);
+                    stage_vec(slot(st, 1, i), dy + r * K + c);
+                    if (dres) stage_vec(slot(st, 2, i), dres + r * K + c);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    float ag[NV][VEC] = {}, ab[NV][VEC] = {};
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) stage(s, blockIdx.x + (int64_t)s * gridDim.x);
+    int st = 0, par = 0;
+    const float inv = 1.0f / (float)K;
+    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+        int ahead = st + STAGES - 1;
+        if (ahead >= STAGES) ahead -= STAGES;
+        stage(ahead, r + (int64_t)(STAGES - 1) * gridDim.x);
+        const float mean = __ldg(mu + r), rs = __ldg(rstd + r);
+        cp_async_wait<STAGES - 1>();
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + t) * VEC;
+            if (c >= K) continue;
+            float xv[VEC], dv[VEC], g[VEC];
+            P::to_floats(*slot(st, 0, i), xv);
+            P::to_floats(*slot(st, 1, i), dv);
+            load_param<VEC>(gamma, c, g);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float xh = (xv[j] - mean) * rs, w = dv[j] * g[j];
+                ag[i][j] = fmaf(dv[j], xh, ag[i][j]);
+                ab[i][j] += dv[j];
+                s1 += w;
+                s2 = fmaf(w, xh, s2);
+            }
+        }
+        s1 = warp_sum(s1);
+        s2 = warp_sum(s2);
+        if (warps > 1) {
+            if ((t & 31) == 0) {
+                red[par][0][warp] = s1;
+                red[par][1][warp] = s2;
+            }
+            __syncthreads();
+            s1 = block_total(red[par][0], warps);
+            s2 = block_total(red[par][1], warps);
+        }
+        const float c1 = s1 * inv, c2 = s2 * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + t) * VEC;
+            if (c >= K) continue;
+            float xv[VEC], dv[VEC], g[VEC];
+            P::to_floats(*slot(st, 0, i), xv);
+            P::to_floats(*slot(st, 1, i), dv);
+            load_param<VEC>(gamma, c, g);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float xh = (xv[j] - mean) * rs;
+                dv[j] = rs * (fmaf(dv[j], g[j], -c1) - xh * c2);
+            }
+            if (dres) {
+                P::to_floats(*slot(st, 2, i), xv);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) dv[j] += xv[j];
+            }
+            *reinterpret_cast<Raw*>(dx + r * K + c) = P::from_floats(dv);
+        }
+        par ^= 1;
+        if (++st == STAGES) st = 0;
+    }
+    float* pg = part + (int64_t)blockIdx.x * 2 * K;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * nt + t) * VEC;
+        if (c >= K) continue;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            pg[c + j] = ag[i][j];
+            pg[K + c + j] = ab[i][j];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ activation backward
+// Rows of a multiple of 8 elements: a warp takes 256 columns (8 a lane) and
+// the CTA's eight warps every eighth row of its slab, two rows at a time; the
+// eight warps' column sums are added through shared memory in warp order.
+constexpr int kActCols = 256;
+template <int ACT>
+__device__ __forceinline__ void act_bwd_rows(const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ z,
+                                             int64_t r0, int64_t r1, int64_t N, int64_t c, __nv_bfloat16* __restrict__ dz,
+                                             uint8_t* __restrict__ q, int fmt, float m, float2 (&sum)[4], uint32_t& amax)
+{
+#pragma unroll 2
+    for (int64_t r = r0; r < r1; r += 8) {
+        const uint4 zr = __ldcs(reinterpret_cast<const uint4*>(z + r * N + c));
+        const uint4 dr = __ldcs(reinterpret_cast<const uint4*>(dy + r * N + c));
+        const uint32_t zw[4] = {zr.x, zr.y, zr.z, zr.w}, dw[4] = {dr.x, dr.y, dr.z, dr.w};
+        float2 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float2 f, d;
+            act_fd2<ACT>(make_float2(__uint_as_float(zw[j] << 16), __uint_as_float(zw[j] & 0xFFFF0000u)), f, d);
+            v[j] = __fmul2_rn(d, make_float2(__uint_as_float(dw[j] << 16), __uint_as_float(dw[j] & 0xFFFF0000u)));
+            sum[j] = __fadd2_rn(sum[j], v[j]);
+        }
+        if (dz) {
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w[2 * j] = v[j].x;
+                w[2 * j + 1] = v[j].y;
+            }
+            *reinterpret_cast<uint4*>(dz + r * N + c) = Pack<__nv_bfloat16, 8>::from_floats(w);
+        }
+        if (q) {
+            uint32_t w[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                amax = max(amax, max(__float_as_uint(v[j].x) & 0x7FFFFFFFu, __float_as_uint(v[j].y) & 0x7FFFFFFFu));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 a = __fmul2_rn(v[2 * j], f2(m)), b = __fmul2_rn(v[2 * j + 1], f2(m));
+                w[j] = fmt == kE4M3 ? (cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16))
+                                    : (cvt_e5m2x2(a.x, a.y) | (cvt_e5m2x2(b.x, b.y) << 16));
+            }
+            *reinterpret_cast<uint2*>(q + r * N + c) = make_uint2(w[0], w[1]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256, 4) k_act_bwd(const __nv_bfloat16* __restrict__ dy,
+                                                    const __nv_bfloat16* __restrict__ z, int act, int64_t R, int64_t N,
+                                                    int64_t slab, __nv_bfloat16* __restrict__ dz,
+                                                    uint8_t* __restrict__ q, int fmt, float* qstate, int H,
+                                                    float* __restrict__ part)
+{
+    pdl_enter();
+    __shared__ float2 cols[8][4][32];
+    __shared__ uint32_t red[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * kActCols + 8 * lane;
+    const int64_t r0 = (int64_t)blockIdx.y * slab;
+    const int64_t r1 = r0 + slab < R ? r0 + slab : R;
+    const float m = q ? qstate[H] : 1.0f;
+    float2 sum[4] = {};
+    uint32_t amax = 0;
+    if (c < N)
+        act_dispatch(act, [&](auto tag) {
+            act_bwd_rows<decltype(tag)::act>(dy, z, r0 + warp, r1, N, c, dz, q, fmt, m, sum, amax);
+        });
+    if (part) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cols[warp][j][lane] = sum[j];
+    }
+    if (q) {
+        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+        if (lane == 0) red[warp] = amax;
+    }
+    __syncthreads();
+    if (part && warp < 4 && c < N) {         // warp j adds pair j of every lane's columns
+        float2 s = cols[0][warp][lane];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) s = __fadd2_rn(s, cols[w][warp][lane]);
+        *reinterpret_cast<float2*>(part + (int64_t)blockIdx.y * N + c + 2 * warp) = s;
+    }
+    if (q && threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) amax = max(amax, red[w]);
+        atomicMax(reinterpret_cast<unsigned int*>(qstate), amax);
+    }
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t parts_for(int64_t rows) { return rows < kMaxParts ? rows : kMaxParts; }
+
+// CTAs of a kernel that are resident at once
+int resident(const void* kern, int threads, int smem, int sms)
+{
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        per_sm = 1;
+    }
+    return per_sm * sms;
+}
+
+template <typename T, int VEC>
+cudaError_t ln_fwd_rows(const LnArgs& a, cudaStream_t st, int sms)
+{
+    const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
+    auto kern = k_ln_fwd<T, VEC>;
+    const int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, 0, sms);
+    launch_k(kern, (unsigned)(a.M < cap ? a.M : cap), threads, 0, st, static_cast<const T*>(a.x),
+             static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, (int)a.K, static_cast<T*>(a.sum),
+             static_cast<T*>(a.y), a.mu, a.rstd);
+    return cudaGetLastError();
+}
 
 template <typename T>
 cudaError_t ln_fwd(const LnArgs& a, cudaStream_t st, int sms)
 {
+    constexpr int WIDE = 16 / (int)sizeof(T), NARROW = WIDE / 4;     // 16 and 4 bytes
+    if (a.K <= 1024 * kLnCols) {
+        if (a.K % WIDE == 0) return ln_fwd_rows<T, WIDE>(a, st, sms);
+        if (a.K % NARROW == 0) return ln_fwd_rows<T, NARROW>(a, st, sms);
+        return ln_fwd_rows<T, 1>(a, st, sms);
+    }
     const int64_t cap = (int64_t)sms * 8;
     launch_k(k_ln_fwd_any<T>, (unsigned)(a.M < cap ? a.M : cap), 256, 0, st, static_cast<const T*>(a.x),
              static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, a.K, static_cast<T*>(a.sum),
@@ -201,19 +607,58 @@ cudaError_t ln_fwd(const LnArgs& a, cudaStream_t st, int sms)
     return cudaGetLastError();
 }
 
+constexpr int kSmemCta = 227 * 1024;
+
+template <typename T, int VEC, int STAGES>
+cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int smem, int* parts)
+{
+    const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
+    auto kern = k_ln_bwd<T, VEC, STAGES>;
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), kSmemCta - 2048);
+    if (e != cudaSuccess) return e;
+    int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, smem, sms);
+    cap = cap < parts_for(a.M) ? cap : parts_for(a.M);
+    *parts = (int)cap;
+    launch_k(kern, (unsigned)cap, threads, smem, st, static_cast<const T*>(a.dy), static_cast<const T*>(a.x),
+             static_cast<const T*>(a.dres), a.gamma, (const float*)a.mu, (const float*)a.rstd, a.M, (int)a.K,
+             static_cast<T*>(a.dx), static_cast<float*>(a.workspace));
+    return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t ln_bwd_vec(const LnArgs& a, cudaStream_t st, int sms, int* parts)
+{
+    const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
+    const int stage = threads * kLnCols * (int)sizeof(T) * (a.dres ? 3 : 2);
+    const int room = kSmemCta - 2048;
+    if (3 * stage <= room) return ln_bwd_rows<T, VEC, 3>(a, st, sms, 3 * stage, parts);
+    if (2 * stage <= room) return ln_bwd_rows<T, VEC, 2>(a, st, sms, 2 * stage, parts);
+    return ln_bwd_rows<T, VEC, 1>(a, st, sms, stage, parts);
+}
+
 template <typename T>
 cudaError_t ln_bwd(const LnArgs& a, cudaStream_t st, int sms)
 {
+    constexpr int WIDE = 16 / (int)sizeof(T), NARROW = WIDE / 4;
     float* part = static_cast<float*>(a.workspace);
     int parts = 0;
     if (a.M > 0) {
-        const int64_t cap = (int64_t)sms * 8;
-        launch_k(k_ln_bwd_dx_any<T>, (unsigned)(a.M < cap ? a.M : cap), 256, 0, st, static_cast<const T*>(a.dy),
-                 static_cast<const T*>(a.x), static_cast<const T*>(a.dres), a.gamma, (const float*)a.mu,
-                 (const float*)a.rstd, a.M, a.K, static_cast<T*>(a.dx));
-        parts = (int)parts_for(a.M);
-        launch_k(k_ln_bwd_gb_any<T>, dim3((unsigned)cdiv(a.K, 256), parts), 256, 0, st, static_cast<const T*>(a.dy),
-                 static_cast<const T*>(a.x), (const float*)a.mu, (const float*)a.rstd, a.M, a.K, part);
+        cudaError_t e = cudaSuccess;
+        if (a.K <= 1024 * kLnCols) {
+            e = a.K % WIDE == 0     ? ln_bwd_vec<T, WIDE>(a, st, sms, &parts)
+                : a.K % NARROW == 0 ? ln_bwd_vec<T, NARROW>(a, st, sms, &parts)
+                                    : ln_bwd_vec<T, 1>(a, st, sms, &parts);
+            if (e != cudaSuccess) return e;
+        } else {
+            const int64_t cap = (int64_t)sms * 8;
+            launch_k(k_ln_bwd_dx_any<T>, (unsigned)(a.M < cap ? a.M : cap), 256, 0, st, static_cast<const T*>(a.dy),
+                     static_cast<const T*>(a.x), static_cast<const T*>(a.dres), a.gamma, (const float*)a.mu,
+                     (const float*)a.rstd, a.M, a.K, static_cast<T*>(a.dx));
+            parts = (int)parts_for(a.M);
+            launch_k(k_ln_bwd_gb_any<T>, dim3((unsigned)cdiv(a.K, 256), parts), 256, 0, st,
+                     static_cast<const T*>(a.dy), static_cast<const T*>(a.x), (const float*)a.mu,
+                     (const float*)a.rstd, a.M, a.K, part);
+        }
     }
     launch_k(k_col_reduce, (unsigned)cdiv(2 * a.K, 32), 256, 0, st, (const float*)part, parts, 2 * a.K, a.dgamma, a.K,
              a.dbeta);
@@ -239,14 +684,26 @@ cudaError_t launch_layernorm_bwd(const LnArgs& a, cudaStream_t st, int sms)
 
 cudaError_t launch_act_bwd(const ActBwdArgs& a, cudaStream_t st, int sms)
 {
-    (void)sms;
     if (a.N == 0) return cudaSuccess;
     float* part = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
-    const int parts = (int)parts_for(a.M);
-    if (a.M > 0)
+    int parts = 0;
+    if (a.M > 0 && a.N % 8 == 0) {
+        // slabs of rows: about four waves of CTAs, at least 8 rows each
+        const int64_t blocks = cdiv(a.N, kActCols);
+        int64_t slabs = 4 * (int64_t)resident(reinterpret_cast<const void*>(k_act_bwd), 256, 0, sms) / blocks;
+        const int64_t most = cdiv(a.M, 8) < kMaxParts ? cdiv(a.M, 8) : kMaxParts;
+        slabs = slabs < 1 ? 1 : slabs < most ? slabs : most;
+        const int64_t slab = cdiv(cdiv(a.M, slabs), 8) * 8;
+        parts = (int)cdiv(a.M, slab);
+        launch_k(k_act_bwd, dim3((unsigned)blocks, parts), 256, 0, st, static_cast<const __nv_bfloat16*>(a.dy),
+                 static_cast<const __nv_bfloat16*>(a.z), a.act, a.M, a.N, slab, static_cast<__nv_bfloat16*>(a.dz), a.q,
+                 a.q_format, a.q_state, a.q_history_len, part);
+    } else if (a.M > 0) {
+        parts = (int)parts_for(a.M);
         launch_k(k_act_bwd_any, dim3((unsigned)cdiv(a.N, 256), parts), 256, 0, st,
                  static_cast<const __nv_bfloat16*>(a.dy), static_cast<const __nv_bfloat16*>(a.z), a.act, a.M, a.N,
                  static_cast<__nv_bfloat16*>(a.dz), a.q, a.q_format, a.q_state, a.q_history_len, part);
+    }
     if (a.dbias)
         launch_k(k_col_reduce, (unsigned)cdiv(a.N, 32), 256, 0, st, (const float*)part, parts, a.N, a.dbias, a.N,
                  (float*)nullptr);
