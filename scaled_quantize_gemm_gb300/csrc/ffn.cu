@@ -99,6 +99,20 @@ __device__ __forceinline__ void max32(uint32_t& amax, const float (&v)[32], int 
     for (int j = 0; j < 32; ++j)
         if (j < left) amax = max(amax, abs_bits(v[j]));
 }
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N])
+{
+    static_assert(N == 4 || N == 8 || N == 16, "columns");
+    if constexpr (N == 4) tmem_ld_32x32b_x4(taddr, r);
+    else if constexpr (N == 8) tmem_ld_32x32b_x8(taddr, r);
+    else tmem_ld_32x32b_x16(taddr, r);
+}
+__device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
+{
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
 __device__ __forceinline__ void load32_bf16(const __nv_bfloat16* s, int left, float (&v)[32])
 {
 #pragma unroll
@@ -425,55 +439,162 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
 }
 
 // ================================================================== few rows
-// Up to 64 rows (serving: single tokens and small batches): the time is the
-// weights' bytes, so the roles are swapped -- 128 weight rows are the M of
-// the MMA and the tokens, padded to NT, its N -- and the K loop is split over
-// all SMs.  The work is the list of (weight tile, 128-wide K block) pairs in
-// tile order; CTA i of G takes the i-th G-th of it, so every SM streams the
-// same number of bytes whatever the sizes, and a tile's K range belongs to
-// one or a few neighbouring CTAs.  A CTA that holds all of a tile's K blocks
-// finishes it from tensor memory; otherwise each writes its fp32 partial sums
-// to the workspace and the last one to arrive (a counter per tile, which it
-// sets back to 0) adds them in CTA order, so the result does not depend on
-// the order of arrival, and runs the epilogue.  No CTA waits for another.
-// glu: a stage holds the gate and the up rows of 128 features, accumulated in
-// two column ranges of the same lanes, so a thread holds both.
-//   warp 0 producer, warp 1 MMA, warps 2-5 epilogue (TMEM lane = weight row)
-constexpr int kRowsThreads = 192;
-constexpr int kRowsMaxM = 64;
+// Products too small for 256 x 256 tiles on every SM: few rows (serving:
+// single tokens and small batches, where the time is the weights' bytes) or
+// few tiles.  The roles are swapped -- 128 weight rows are the M of the MMA
+// and NT tokens its N -- and the K loop is split over all SMs.  The work is
+// the list of (tile, 128-wide K block) pairs in tile order; CTA i of G takes
+// the i-th G-th of it, so every SM streams the same number of bytes whatever
+// the sizes, and a tile's K range belongs to one or a few neighbouring CTAs.
+// A CTA that holds all of a tile's K blocks finishes it from tensor memory;
+// otherwise each writes its fp32 partial sums to the workspace and the last
+// one to arrive (a counter per tile, which it sets back to 0) adds them in CTA
+// order, so the result does not depend on the order of arrival, and runs the
+// epilogue.  No CTA waits for another.
+// glu: a tile is the gate and the up rows of 64 features, lanes 0-63 and 64-127
+// of one accumulator; the pair meets in shared memory (a whole tile) or in the
+// partial sums.
+//   warp 0 producer, warp 1 MMA, warps 2-17 epilogue (TMEM lane = weight row,
+//   four warps per lane quarter, each a quarter of the tokens)
+// A lane of a finishing warp holds one output column, so a token's stores are
+// 32 consecutive columns: coalesced without staging.  Sixteen epilogue warps,
+// because the join is a read of a few partial tiles by one CTA: bytes in
+// flight (with eight, 14336 -> 4096 for 64 tokens spent 6.5 us in it).
+constexpr int kRowsEpiWarps = 16;
+constexpr int kRowsThreads = 32 * (2 + kRowsEpiWarps);
 constexpr int kRowsMaxCtas = 192;                 // partial slots in the workspace
 constexpr int kRowsMaxTiles = 16384;              // counters in the workspace
 constexpr size_t kRowsCounterBytes = kRowsMaxTiles * sizeof(uint32_t);
 
 template <int KIND, int NT>
 struct RowsLayout {
-    static constexpr int NW = KIND == kEpiGlu ? 2 : 1;                  // weight tiles per stage
-    static constexpr int STAGE = NW * A_BYTES + NT * BK;
-    static constexpr int STAGES = (200 * 1024) / STAGE;
-    static constexpr int BAR_OFF = STAGES * STAGE;
+    static constexpr bool GLU = KIND == kEpiGlu;
+    static constexpr int COLS = GLU ? BM / 2 : BM;                       // output columns of a tile
+    static constexpr int STAGE = A_BYTES + NT * BK;
+    static constexpr int SUMS = GLU ? BM * NT * 4 : 0;                   // a whole tile's sums
+    static constexpr int STAGES = (200 * 1024 - SUMS) / STAGE;
+    static constexpr int SUM_OFF = STAGES * STAGE;
+    static constexpr int BAR_OFF = SUM_OFF + SUMS;
     static constexpr int BYTES = BAR_OFF + 512 + 1024;
-    static constexpr int ACC = NW * NT;                                  // columns of one accumulator
-    static constexpr uint32_t TMEM_COLS = 2 * ACC < 32 ? 32 : 2 * ACC;
+    static constexpr uint32_t TMEM_COLS = 2 * NT;
+    static constexpr int SHARE = NT / 4;                                 // tokens of an epilogue warp
+    static constexpr int CH = SHARE < 8 ? SHARE : 8;                     // tokens of a chunk
     static_assert((2 * STAGES + 5) * 8 + 8 <= 512, "barriers");
+    static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512, "tensor memory");
 };
 
 struct RowsParams {
-    int tiles, nkb, split;
+    int wtiles, mtiles, nkb, split;      // tile = weight tile x mtiles + token tile
     uint32_t* counters;
-    float* part;              // [CTA][2][NW * NT][128]
+    float* part;                         // [CTA][2][NT / 4][128 weight rows][4 tokens]
 };
 
 // first work item of CTA i
 __device__ __forceinline__ int rows_start(const RowsParams& w, int i)
 {
     const int64_t g = gridDim.x;
-    if (!w.split) return (int)((int64_t)i * w.tiles / g) * w.nkb;
-    return (int)((int64_t)i * ((int64_t)w.tiles * w.nkb) / g);
+    const int tiles = w.wtiles * w.mtiles;
+    if (!w.split) return (int)((int64_t)i * tiles / g) * w.nkb;
+    return (int)((int64_t)i * ((int64_t)tiles * w.nkb) / g);
 }
 // the CTA that holds work item u (split work)
 __device__ __forceinline__ int rows_owner(const RowsParams& w, int u)
 {
-    return (int)((((int64_t)u + 1) * gridDim.x - 1) / ((int64_t)w.tiles * w.nkb));
+    return (int)((((int64_t)u + 1) * gridDim.x - 1) / ((int64_t)w.wtiles * w.mtiles * w.nkb));
+}
+
+// The residual of CH tokens of column n; the loads of a chunk are in flight
+// together, and a caller issues them ahead of its sums.
+template <int CH>
+__device__ __forceinline__ void rows_residual(const FfnParams& p, int m0, int n, float (&r)[CH])
+{
+    if (!p.res || n >= p.N) return;
+    if (p.res_f32) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (m0 + j < p.M) r[j] = __ldg(static_cast<const float*>(p.res) + (int64_t)(m0 + j) * p.N + n);
+    } else {
+        uint32_t b[CH];
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (m0 + j < p.M) b[j] = __ldg(static_cast<const uint16_t*>(p.res) + (int64_t)(m0 + j) * p.N + n);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) r[j] = __uint_as_float(b[j] << 16);
+    }
+}
+
+// The epilogue of CH tokens (m0 .. m0 + CH - 1) of weight row n: a holds the
+// raw sums (glu: of the gate, up those of the up row), r the residual.
+template <int KIND, int CH>
+__device__ __forceinline__ void rows_epilogue(const FfnParams& p, float (&a)[CH], float (&up)[CH],
+                                              const float (&r)[CH], int m0, int n, float scale, float qm,
+                                              uint32_t& amax)
+{
+    const int live = p.M - m0;                   // tokens of the chunk inside the matrix
+    if constexpr (KIND == kEpiAct) {
+        const float bias = p.bias ? __ldg(p.bias + n) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            a[j] = a[j] * scale;
+            if (p.bias) a[j] += bias;
+            if (p.Z && j < live) p.Z[(int64_t)(m0 + j) * p.N + n] = __float2bfloat16_rn(a[j]);
+        }
+        act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+            for (int j = 0; j < CH; j += 2)
+                if (j < live) {
+                    const float2 y = act_f2<decltype(tag)::act>(make_float2(a[j], a[j + 1]));
+                    a[j] = y.x;
+                    a[j + 1] = y.y;
+                }
+        });
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            if (p.res) a[j] += r[j];
+            if (p.D && j < live) {
+                const int64_t o = (int64_t)(m0 + j) * p.N + n;
+                if (p.d_f32) static_cast<float*>(p.D)[o] = a[j];
+                else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(a[j]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            a[j] *= scale;
+            up[j] *= scale;
+            if (p.Z && j < live) {
+                __nv_bfloat16* z = p.Z + (int64_t)(m0 + j) * 2 * p.N + n;
+                z[0] = __float2bfloat16_rn(a[j]);
+                z[p.N] = __float2bfloat16_rn(up[j]);
+            }
+        }
+        act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+            for (int j = 0; j < CH; j += 2)
+                if (j < live) {
+                    const float2 h = __fmul2_rn(make_float2(up[j], up[j + 1]),
+                                                act_f2<decltype(tag)::act>(make_float2(a[j], a[j + 1])));
+                    a[j] = h.x;
+                    a[j + 1] = h.y;
+                }
+        });
+        if (p.D) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (j < live)
+                    static_cast<__nv_bfloat16*>(p.D)[(int64_t)(m0 + j) * p.N + n] = __float2bfloat16_rn(a[j]);
+        }
+    }
+    if (p.Q) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (j < live) {
+                amax = max(amax, abs_bits(a[j]));
+                const float v = __fmul_rn(a[j], qm);
+                p.Q[(int64_t)(m0 + j) * p.N + n] =
+                    (uint8_t)(p.qfmt == kE4M3 ? cvt_e4m3x2(v, 0.0f) : cvt_e5m2x2(v, 0.0f));
+            }
+    }
 }
 
 template <int KIND, int NT>
@@ -481,9 +602,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     k_ffn_rows(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, FfnParams p,
                RowsParams w, uint32_t idesc)
 {
-    pdl_enter();
     using L = RowsLayout<KIND, NT>;
-    constexpr int STAGES = L::STAGES, NW = L::NW, ACC = L::ACC;
+    constexpr int STAGES = L::STAGES, CH = L::CH;
+    constexpr bool GLU = L::GLU;
+    constexpr int BOX = L::COLS;                 // weight rows of a load (glu: gate rows, then up rows)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -495,40 +617,63 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     __shared__ int s_skip;
     __shared__ int s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // what touches no global memory of the kernel before this one runs ahead
+    // of the wait on it
     if (threadIdx.x == 0) {
-        s_skip = *reinterpret_cast<volatile int*>(p.err);
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmX);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&afull[b], 1);
-            mbar_init(&aempty[b], 4);
+            mbar_init(&aempty[b], kRowsEpiWarps);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
-        prefetch_tmap(&tmW);
-        prefetch_tmap(&tmX);
     }
-    __syncthreads();
-    if (s_skip) return;
     if (warp == 1) {
         tmem_alloc(holder, L::TMEM_COLS);
         tmem_relinquish();
     }
+    const int u0 = rows_start(w, blockIdx.x), u1 = rows_start(w, blockIdx.x + 1);
+    if (threadIdx.x == 0) {
+        // The first stages' weights into L2 while the kernel before still
+        // runs.  L2 is where all SMs meet: should that kernel be writing
+        // them, the loads below, after the wait, still see what it wrote.
+        int tile = u0 / w.nkb, kb = u0 - tile * w.nkb;
+        int wt = tile / w.mtiles, mt = tile - wt * w.mtiles;
+        for (int i = 0; i < STAGES && u0 + i < u1; ++i) {
+            prefetch_l2_2d(&tmW, kb * BK, wt * BOX);
+            if (GLU) prefetch_l2_2d(&tmW, kb * BK, p.N + wt * BOX);
+            if (++kb == w.nkb) {
+                kb = 0;
+                if (++mt == w.mtiles) {
+                    mt = 0;
+                    ++wt;
+                }
+            }
+        }
+    }
+    pdl_enter();
+    if (threadIdx.x == 0) s_skip = *reinterpret_cast<volatile int*>(p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *holder;
+    const bool skip = s_skip != 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err(bar, parity, p.err); };
-    const int u0 = rows_start(w, blockIdx.x), u1 = rows_start(w, blockIdx.x + 1);
 
-    if (warp == 0) {
+    if (skip) {
+        // a wait ran out earlier: compute nothing
+    } else if (warp == 0) {
         if (lane == 0) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool aborted = false;
             int tile = u0 / w.nkb, kb = u0 - tile * w.nkb;
+            int wt = tile / w.mtiles, mt = tile - wt * w.mtiles;
             for (int u = u0; u < u1; ++u) {
                 if (!wait(&empty[stage], phase ^ 1u)) {
                     aborted = true;
@@ -536,9 +681,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
                 uint8_t* sw = smem + stage * L::STAGE;
                 mbar_arrive_expect_tx(&full[stage], (uint32_t)L::STAGE);
-                tma_load_2d(sw, &tmW, kb * BK, tile * BM, &full[stage]);
-                if (NW == 2) tma_load_2d(sw + A_BYTES, &tmW, kb * BK, p.N + tile * BM, &full[stage]);
-                tma_load_2d(sw + NW * A_BYTES, &tmX, kb * BK, 0, &full[stage]);
+                tma_load_2d(sw, &tmW, kb * BK, wt * BOX, &full[stage]);
+                if (GLU) tma_load_2d(sw + A_BYTES / 2, &tmW, kb * BK, p.N + wt * BOX, &full[stage]);
+                tma_load_2d(sw + A_BYTES, &tmX, kb * BK, mt * NT, &full[stage]);
                 ++issued;
                 if (++stage == STAGES) {
                     stage = 0;
@@ -546,9 +691,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
                 if (++kb == w.nkb) {
                     kb = 0;
-                    ++tile;
+                    if (++mt == w.mtiles) {
+                        mt = 0;
+                        ++wt;
+                    }
                 }
             }
+            // every load is under way: the next kernel's CTAs may take over the
+            // SMs as this grid's tail leaves them (all of this grid is resident)
+            pdl_trigger();
             if (aborted) {
                 // wait for the copies still in flight before the CTA can exit
                 int n = issued < STAGES ? issued : STAGES;
@@ -576,7 +727,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(b * ACC);
+                const uint32_t d = tmem_base + (uint32_t)(b * NT);
                 for (uint32_t first = 0; u < end; ++u) {
                     if (!wait(&full[stage], phase)) {
                         aborted = true;
@@ -584,14 +735,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t sw = smem_addr(smem + stage * L::STAGE);
-                    const uint64_t dx = sdesc_kmajor_sw128(sw + NW * A_BYTES);
+                    const uint64_t dw = sdesc_kmajor_sw128(sw), dx = sdesc_kmajor_sw128(sw + A_BYTES);
 #pragma unroll
-                    for (int h = 0; h < NW; ++h) {
-                        const uint64_t dw = sdesc_kmajor_sw128(sw + h * A_BYTES);
-#pragma unroll
-                        for (int k = 0; k < BK / 32; ++k)
-                            mma_f8f6f4(d + h * NT, dw + 2 * k, dx + 2 * k, idesc, k != 0 ? 1u : first);
-                    }
+                    for (int k = 0; k < BK / 32; ++k)
+                        mma_f8f6f4(d, dw + 2 * k, dx + 2 * k, idesc, k != 0 ? 1u : first);
                     first = 1;
                     mma_commit(&empty[stage]);
                     if (++stage == STAGES) {
@@ -608,131 +755,139 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
     } else {
         const int quarter = warp & 3;
+        const int part = (warp - 2) >> 2;                   // share of the tokens
         const int wr = quarter * 32 + lane;                 // weight row within the tile
         const float scale = __ldg(p.sA) * __ldg(p.sB);
         const float qm = p.Q ? p.qstate[p.qH] : 1.0f;
+        constexpr int ETH = 32 * kRowsEpiWarps;
+        const int et = threadIdx.x - 64;
+        float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
         uint32_t amax = 0;
         int seg = 0;
+        // glu: tokens 4 i .. 4 i + 3 of feature et % 64 from the sums of `parts`
+        // blocks; the block s is at src(s)
+        auto glu_quads = [&](int wt, int m_tile, int left, int parts, auto src, auto load) {
+            const int f = et & 63, n = wt * 64 + f;
+#pragma unroll 1
+            for (int i = et >> 6; 4 * i < left && i < NT / 4; i += ETH / 64) {
+                constexpr int SEG = 6;
+                float g[4] = {}, up[4] = {};
+#pragma unroll 1
+                for (int s0 = 0; s0 < parts; s0 += SEG) {
+                    float4 vg[SEG], vu[SEG];
+#pragma unroll
+                    for (int s = 0; s < SEG; ++s)
+                        if (s0 + s < parts) {
+                            const float4* q = reinterpret_cast<const float4*>(src(s0 + s)) + i * BM + f;
+                            vg[s] = load(q);
+                            vu[s] = load(q + 64);
+                        }
+#pragma unroll
+                    for (int s = 0; s < SEG; ++s)
+                        if (s0 + s < parts) {
+                            g[0] += vg[s].x;
+                            g[1] += vg[s].y;
+                            g[2] += vg[s].z;
+                            g[3] += vg[s].w;
+                            up[0] += vu[s].x;
+                            up[1] += vu[s].y;
+                            up[2] += vu[s].z;
+                            up[3] += vu[s].w;
+                        }
+                }
+                const float none[4] = {};
+                if (n < p.N) rows_epilogue<KIND, 4>(p, g, up, none, m_tile + 4 * i, n, scale, qm, amax);
+            }
+        };
         for (int u = u0; u < u1; ++seg) {
             const int b = seg & 1;
             const int tile = u / w.nkb, kb0 = u - tile * w.nkb;
+            const int wt = tile / w.mtiles, mt = tile - wt * w.mtiles;
             const int end = min(u1, (tile + 1) * w.nkb);
             const bool whole = kb0 == 0 && end == (tile + 1) * w.nkb;
             u = end;
-            if (!bar_all(1, 128, wait(&afull[b], (uint32_t)(seg >> 1) & 1u))) break;
+            const int n = wt * BOX + wr;                    // gemm_act: the lane's output column
+            const int t0 = part * L::SHARE;                 // this warp's first token in the tile
+            const int left = p.M - mt * NT;                 // tokens of the tile inside the matrix
+            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * NT);
+            if (!bar_all(1, ETH, wait(&afull[b], (uint32_t)(seg >> 1) & 1u))) break;
             tc_fence_after();
-            float acc[ACC];
-            {
-                uint32_t r[ACC];
-                const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * ACC);
-#pragma unroll
-                for (int c = 0; c < ACC; c += 16) tmem_ld_32x32b_x16(taddr + c, r + c);
+            // this CTA's block of sums: in shared memory for a whole glu tile
+            // (the barrier above says that the last one has been read)
+            float* mine = GLU && whole ? sums : w.part + ((int64_t)blockIdx.x * 2 + (kb0 == 0 ? 1 : 0)) * (NT * BM);
+#pragma unroll 1
+            for (int c = t0; c < t0 + L::SHARE && c < left; c += CH) {
+                float rs[CH];
+                if (!GLU && whole) rows_residual<CH>(p, mt * NT + c, n, rs);
+                uint32_t r[CH];
+                tmem_ld_cols<CH>(taddr + c, r);
                 tmem_ld_wait();
+                if (GLU || !whole) {
 #pragma unroll
-                for (int c = 0; c < ACC; ++c) acc[c] = __uint_as_float(r[c]);
+                    for (int j = 0; j < CH; j += 4)
+                        if (c + j < left)
+                            *reinterpret_cast<uint4*>(mine + (c + j) * BM + 4 * wr) =
+                                make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+                } else if (n < p.N) {
+                    float a[CH];
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) a[j] = __uint_as_float(r[j]);
+                    rows_epilogue<KIND, CH>(p, a, a, rs, mt * NT + c, n, scale, qm, amax);
+                }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&aempty[b]);
-            if (!whole) {
-                float* mine = w.part + ((int64_t)blockIdx.x * 2 + (kb0 == 0 ? 1 : 0)) * (ACC * 128) + wr;
-#pragma unroll
-                for (int c = 0; c < ACC; ++c)
-                    if (c % NT < p.M) __stcg(mine + c * 128, acc[c]);
-                const int c0 = rows_owner(w, tile * w.nkb), c1 = rows_owner(w, (tile + 1) * w.nkb - 1);
-                __threadfence();
-                bar_all(1, 128, true);
-                if (threadIdx.x == 64) {
-                    const uint32_t n = (uint32_t)(c1 - c0);
-                    const bool last = atomicAdd(&w.counters[tile], 1u) == n;
-                    if (last) w.counters[tile] = 0;
-                    s_last = last;
+            if (whole) {
+                if constexpr (GLU) {
+                    bar_all(1, ETH, true);
+                    glu_quads(wt, mt * NT, left, 1, [&](int) { return sums; }, [](const float4* q) { return *q; });
+                    __syncwarp();
                 }
-                bar_all(1, 128, true);
-                if (!s_last) continue;
-                __threadfence();
-                for (int c = c0; c <= c1; ++c) {
-                    const float* src = w.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * (ACC * 128) + wr;
-#pragma unroll
-                    for (int j = 0; j < ACC; ++j) {
-                        if (j % NT < p.M) {
-                            const float v = __ldcg(src + j * 128);
-                            acc[j] = c == c0 ? v : acc[j] + v;
-                        }
-                    }
-                }
+                continue;
             }
-            const int n = tile * BM + wr;
-            if (n < p.N) {
-                if constexpr (KIND == kEpiAct) {
-                    const float bias = p.bias ? __ldg(p.bias + n) : 0.0f;
+            // the barrier orders every thread's partial sums before the one
+            // release, and the one acquire before every thread's reads
+            const int c0 = rows_owner(w, tile * w.nkb), c1 = rows_owner(w, (tile + 1) * w.nkb - 1);
+            bar_all(1, ETH, true);
+            if (et == 0) {
+                const bool last = atomic_add_acq_rel(&w.counters[tile], 1u) == (uint32_t)(c1 - c0);
+                if (last) w.counters[tile] = 0;
+                s_last = last;
+            }
+            bar_all(1, ETH, true);
+            // the first CTA holds the tile in its last slot, the others in their first
+            auto block = [&](int s) { return w.part + ((int64_t)(c0 + s) * 2 + (s == 0 ? 1 : 0)) * (NT * BM); };
+            if (s_last) {
+                if constexpr (GLU) {
+                    glu_quads(wt, mt * NT, left, c1 - c0 + 1, block, [](const float4* q) { return __ldcg(q); });
+                } else if (n < p.N) {
+                    // quads of tokens, up to eight loads a thread in flight
+                    constexpr int SEG = 8;
+                    const int parts = c1 - c0 + 1;
+#pragma unroll 1
+                    for (int c = t0; c < t0 + L::SHARE && c < left; c += 4) {
+                        float rs[4], a[4] = {};
+                        rows_residual<4>(p, mt * NT + c, n, rs);
+#pragma unroll 1
+                        for (int s0 = 0; s0 < parts; s0 += SEG) {
+                            float4 v[SEG];
 #pragma unroll
-                    for (int m = 0; m < NT; ++m)
-                        if (m < p.M) {
-                            acc[m] = acc[m] * scale;
-                            if (p.bias) acc[m] += bias;
-                            if (p.Z) p.Z[(int64_t)m * p.N + n] = __float2bfloat16_rn(acc[m]);
+                            for (int s = 0; s < SEG; ++s)
+                                if (s0 + s < parts)
+                                    v[s] = __ldcg(reinterpret_cast<const float4*>(block(s0 + s) + c * BM + 4 * wr));
+#pragma unroll
+                            for (int s = 0; s < SEG; ++s)
+                                if (s0 + s < parts) {
+                                    a[0] += v[s].x;
+                                    a[1] += v[s].y;
+                                    a[2] += v[s].z;
+                                    a[3] += v[s].w;
+                                }
                         }
-                    act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                        for (int m = 0; m < NT; m += 2)
-                            if (m < p.M) {
-                                const float2 y = act_f2<decltype(tag)::act>(make_float2(acc[m], m + 1 < p.M ? acc[m + 1] : 0.0f));
-                                acc[m] = y.x;
-                                acc[m + 1] = y.y;
-                            }
-                    });
-#pragma unroll
-                    for (int m = 0; m < NT; ++m)
-                        if (m < p.M) {
-                            const int64_t o = (int64_t)m * p.N + n;
-                            if (p.res) acc[m] += p.res_f32 ? __ldg(static_cast<const float*>(p.res) + o)
-                                                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[o]);
-                            if (p.D) {
-                                if (p.d_f32) static_cast<float*>(p.D)[o] = acc[m];
-                                else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(acc[m]);
-                            }
-                        }
-                } else {
-#pragma unroll
-                    for (int m = 0; m < NT; ++m)
-                        if (m < p.M) {
-                            acc[m] *= scale;
-                            acc[NT + m] *= scale;
-                            if (p.Z) {
-                                __nv_bfloat16* z = p.Z + (int64_t)m * 2 * p.N + n;
-                                z[0] = __float2bfloat16_rn(acc[m]);
-                                z[p.N] = __float2bfloat16_rn(acc[NT + m]);
-                            }
-                        }
-                    act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                        for (int m = 0; m < NT; m += 2)
-                            if (m < p.M) {
-                                const bool two = m + 1 < p.M;
-                                const float2 h = __fmul2_rn(
-                                    make_float2(acc[NT + m], two ? acc[NT + m + 1] : 0.0f),
-                                    act_f2<decltype(tag)::act>(make_float2(acc[m], two ? acc[m + 1] : 0.0f)));
-                                acc[m] = h.x;
-                                acc[m + 1] = h.y;
-                            }
-                    });
-                    if (p.D) {
-#pragma unroll
-                        for (int m = 0; m < NT; ++m)
-                            if (m < p.M)
-                                static_cast<__nv_bfloat16*>(p.D)[(int64_t)m * p.N + n] = __float2bfloat16_rn(acc[m]);
+                        rows_epilogue<KIND, 4>(p, a, a, rs, mt * NT + c, n, scale, qm, amax);
                     }
-                }
-                if (p.Q) {
-#pragma unroll
-                    for (int m = 0; m < NT; ++m)
-                        if (m < p.M) {
-                            amax = max(amax, abs_bits(acc[m]));
-                            const float v = __fmul_rn(acc[m], qm);
-                            p.Q[(int64_t)m * p.N + n] =
-                                (uint8_t)(p.qfmt == kE4M3 ? cvt_e4m3x2(v, 0.0f) : cvt_e5m2x2(v, 0.0f));
-                        }
                 }
             }
             __syncwarp();
@@ -787,15 +942,30 @@ static cudaError_t ffn_clusters(const void* kern, int kind, int* clusters)
     return cudaSuccess;
 }
 
-static int rows_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+// Token columns of a few-rows tile.
+static int rows_nt(int kind, int64_t M)
+{
+    if (M <= 16) return 16;
+    if (M <= 32) return 32;
+    return M <= 64 || kind == kFfnGlu ? 64 : 128;
+}
+static int rows_cols(int kind) { return kind == kFfnGlu ? BM / 2 : BM; }
 
-// the split of few rows over K applies: bytes of its counters and partial sums
+// The few-rows kernel takes a product of at most 64 rows, and a larger one
+// whose tiles (128 weight rows x NT tokens) all run at once; `ctas` bounds
+// the SMs.
+static bool rows_applies(int kind, int64_t M, int64_t N, int64_t K, int64_t ctas)
+{
+    const int64_t wt = (N + rows_cols(kind) - 1) / rows_cols(kind), nt = rows_nt(kind, M), mt = (M + nt - 1) / nt;
+    if (wt * mt > kRowsMaxTiles || wt * mt * ((K + BK - 1) / BK) >= ((int64_t)1 << 31)) return false;
+    return M <= 64 || wt * mt <= ctas;
+}
+
+// bytes of the split's counters and partial sums, 0 where it never applies
 size_t ffn_workspace(int kind, int64_t M, int64_t N, int64_t K)
 {
-    (void)K;
-    if (M > kRowsMaxM || (N + BM - 1) / BM > kRowsMaxTiles) return 0;
-    const int acc = (kind == kFfnGlu ? 2 : 1) * rows_nt(M);
-    return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * acc * 128 * sizeof(float);
+    if (!rows_applies(kind, M, N, K, kRowsMaxCtas)) return 0;
+    return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * rows_nt(kind, M) * BM * sizeof(float);
 }
 
 template <int KIND, int NT>
@@ -803,24 +973,26 @@ static cudaError_t launch_rows(const FfnArgs& a, const FfnParams& p, cudaStream_
 {
     using L = RowsLayout<KIND, NT>;
     CUtensorMap tw, tx;
-    if (!make_tmap(&tw, a.B, a.K, L::NW * a.N, BM) || !make_tmap(&tx, a.A, a.K, a.M, NT)) {
+    if (!make_tmap(&tw, a.B, a.K, L::GLU ? 2 * a.N : a.N, L::COLS) || !make_tmap(&tx, a.A, a.K, a.M, NT)) {
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
     RowsParams w = {};
-    w.tiles = (int)((a.N + BM - 1) / BM);
+    w.wtiles = (int)((a.N + L::COLS - 1) / L::COLS);
+    w.mtiles = (int)((a.M + NT - 1) / NT);
     w.nkb = (int)((a.K + BK - 1) / BK);
-    const int64_t work = (int64_t)w.tiles * w.nkb;
-    w.split = a.workspace != nullptr;
+    const int64_t tiles = (int64_t)w.wtiles * w.mtiles, work = tiles * w.nkb;
     int64_t grid = sms < kRowsMaxCtas ? sms : kRowsMaxCtas;
+    // Splitting K shortens the longest CTA from whole tiles to an equal share
+    // and adds the join, about 3 us: what an SM streams of 128 KB in that time.
+    w.split = a.workspace != nullptr && ((tiles + grid - 1) / grid * w.nkb - work / grid) * L::STAGE > 128 * 1024;
     if (w.split) {
         w.counters = static_cast<uint32_t*>(a.workspace);
         w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kRowsCounterBytes);
-        // at least four K blocks a CTA: below that the join costs more than the split saves
-        const int64_t most = (work + 3) / 4;
+        const int64_t most = (work + 3) / 4;      // at least four K blocks a CTA
         grid = grid < most ? grid : most;
     } else {
-        grid = grid < w.tiles ? grid : w.tiles;
+        grid = grid < tiles ? grid : tiles;
     }
     auto kern = k_ffn_rows<KIND, NT>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), L::BYTES);
@@ -832,10 +1004,11 @@ static cudaError_t launch_rows(const FfnArgs& a, const FfnParams& p, cudaStream_
 template <int KIND>
 static cudaError_t launch_rows_nt(const FfnArgs& a, const FfnParams& p, cudaStream_t st, int sms, const char** why)
 {
-    switch (rows_nt(a.M)) {
+    switch (rows_nt(a.kind, a.M)) {
     case 16: return launch_rows<KIND, 16>(a, p, st, sms, why);
     case 32: return launch_rows<KIND, 32>(a, p, st, sms, why);
-    default: return launch_rows<KIND, 64>(a, p, st, sms, why);
+    case 64: return launch_rows<KIND, 64>(a, p, st, sms, why);
+    default: return launch_rows<kEpiAct, 128>(a, p, st, sms, why);
     }
 }
 
@@ -864,7 +1037,7 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     cudaError_t e = device_error_word(&p.err);
     if (e != cudaSuccess) return e;
     const bool glu = a.kind == kFfnGlu, bwd = a.kind == kFfnGluBwd;
-    if (!bwd && ffn_workspace(a.kind, a.M, a.N, a.K) != 0 && (int64_t)((a.N + BM - 1) / BM) * ((a.K + BK - 1) / BK) < ((int64_t)1 << 31))
+    if (!bwd && rows_applies(a.kind, a.M, a.N, a.K, sms < kRowsMaxCtas ? sms : kRowsMaxCtas))
         return glu ? launch_rows_nt<kEpiGlu>(a, p, st, sms, why) : launch_rows_nt<kEpiAct>(a, p, st, sms, why);
     CUtensorMap ta, tb;
     const bool ok_b = bwd ? make_tmap(&tb, a.B, a.N, a.K, BK) : make_tmap(&tb, a.B, a.K, glu ? 2 * a.N : a.N, kFfnBH);

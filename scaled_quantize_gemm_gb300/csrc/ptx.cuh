@@ -20,8 +20,8 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p)
 // kernel's CTAs exit.  Every kernel of this library starts with pdl_enter(),
 // which waits until every kernel it depends on has completed with its memory
 // operations visible, so the kernel's reads and writes keep plain stream
-// order.  No kernel triggers its dependents early
-// (griddepcontrol.launch_dependents): measured on the GB300, an early
+// order.  Kernels do not trigger their dependents early
+// (griddepcontrol.launch_dependents; but see pdl_trigger): measured on the GB300, an early
 // trigger let chains of waiting CTAs build up behind the persistent GEMMs
 // (a fine-grained backward took 278 us with it, 239 us without, 248 us with
 // no programmatic launch at all).  A no-op for a launch without the
@@ -29,6 +29,14 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p)
 __device__ __forceinline__ void pdl_enter()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets the next kernel on the stream launch before this grid has ended (its
+// pdl_enter still waits for the end).  Only for grids that are resident as a
+// whole, once they have issued their loads: k_ffn_rows.
+__device__ __forceinline__ void pdl_trigger()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ FP8 cast
@@ -163,6 +171,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
+// the box of a 2-D tiled map into L2
+__device__ __forceinline__ void prefetch_l2_2d(const CUtensorMap* m, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
 // 1-D bulk copy global -> shared (16-byte aligned addresses, size % 16 == 0)
 __device__ __forceinline__ void bulk_load_1d(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 {
@@ -248,7 +263,22 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         : "r"(taddr)
         : "memory");
 }
-// 32 lanes x 16 consecutive 32-bit columns
+// 32 lanes x 4, 8 or 16 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r)
 {
     asm volatile(

@@ -133,25 +133,28 @@ __global__ void __launch_bounds__(256) k_ln_bwd_gb_any(const T* __restrict__ dy,
 }
 
 // out0[c] = sum over p of part[p][c] for c < n0, out1[c - n0] for the rest
-// (rows of n columns); a CTA takes 32 columns, eight warps an eighth of the
-// parts each, added in a fixed order
-__global__ void __launch_bounds__(256) k_col_reduce(const float* __restrict__ part, int parts, int64_t n,
-                                                    float* __restrict__ out0, int64_t n0, float* __restrict__ out1)
+// (rows of n columns); a CTA takes 32 columns, each of its 32 warps every 32nd
+// part, and the warps' sums are added in a fixed order
+__global__ void __launch_bounds__(1024) k_col_reduce(const float* __restrict__ part, int parts, int64_t n,
+                                                     float* __restrict__ out0, int64_t n0, float* __restrict__ out1)
 {
     pdl_enter();
-    __shared__ float s[8][32];
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float a = 0.0f;
-    if (c < n)
-        for (int p = w; p < parts; p += 8) a += part[(int64_t)p * n + c];
+    if (c < n) {
+#pragma unroll 8
+        for (int p = w; p < parts; p += 32) a += __ldcs(part + (int64_t)p * n + c);
+    }
     s[w][lane] = a;
     __syncthreads();
-    if (w == 0 && c < n) {
-        const float v = ((s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane])) +
-                        ((s[4][lane] + s[5][lane]) + (s[6][lane] + s[7][lane]));
-        if (c < n0) out0[c] = v;
-        else out1[c - n0] = v;
+    // warp w takes column w: its lanes hold the 32 partial sums
+    const float v = warp_sum(s[lane][w]);
+    const int64_t cw = (int64_t)blockIdx.x * 32 + w;
+    if (lane == 0 && cw < n) {
+        if (cw < n0) out0[cw] = v;
+        else out1[cw - n0] = v;
     }
 }
 
@@ -345,11 +348,13 @@ __global__ void __launch_bounds__(1024) k_ln_fwd(const T* __restrict__ x, const 
 
 // ------------------------------------------------------------------ LayerNorm backward
 // A CTA takes rows r = blockIdx.x, + gridDim.x, ... and each thread the same
-// (up to) 16 columns of every row, so dgamma and dbeta accumulate in its
-// registers and go to the workspace once per CTA.  x, dy and dres of the next
-// STAGES - 1 rows are in flight (cp.async) while a row is worked on: a thread
-// copies exactly the elements that it will read, so the ring needs no barrier
-// and no wait on another thread, and a row costs one barrier, for its two sums.
+// C columns of every row, so dgamma and dbeta accumulate in its registers and
+// go to the workspace once per CTA.  x, dy and dres of the next STAGES - 1 rows
+// are in flight (cp.async) while a row is worked on: a thread copies exactly
+// the elements that it will read, so the ring needs no barrier and no wait on
+// another thread, and a row costs one barrier, for its two sums.  C = 8 keeps
+// the row's normalised values and dy gamma in registers across that barrier;
+// C = 16 (rows over 8192) reads them from the ring again.
 __device__ __forceinline__ void cp_async4(void* s, const void* g)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s)), "l"(g) : "memory");
@@ -367,14 +372,15 @@ __device__ __forceinline__ void stage_vec(Raw* s, const void* g)
     else *s = *static_cast<const Raw*>(g);       // 2 bytes: below cp.async's smallest size
 }
 
-template <typename T, int VEC, int STAGES>
+template <typename T, int VEC, int C, int STAGES>
 __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const T* __restrict__ x,
                                                  const T* __restrict__ dres, const float* __restrict__ gamma,
                                                  const float* __restrict__ mu, const float* __restrict__ rstd,
                                                  int64_t R, int K, T* __restrict__ dx, float* __restrict__ part)
 {
     pdl_enter();
-    constexpr int NV = kLnCols / VEC;
+    constexpr int NV = C / VEC;
+    constexpr bool KEEP = C == 8;
     using P = Pack<T, VEC>;
     using Raw = typename P::Raw;
     extern __shared__ __align__(16) uint8_t ln_ring[];
@@ -398,37 +404,61 @@ __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const
         }
         cp_async_commit();
     };
-    float ag[NV][VEC] = {}, ab[NV][VEC] = {};
+    // columns past K hold zeros in every array, so they add nothing
+    auto fetch = [&](int st, int arr, float2 (&v)[C / 2]) {
+        float f[NV][VEC];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) P::to_floats((i * nt + t) * VEC < K ? *slot(st, arr, i) : Raw{}, f[i]);
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j)
+            v[j] = make_float2(f[(2 * j) / VEC][(2 * j) % VEC], f[(2 * j + 1) / VEC][(2 * j + 1) % VEC]);
+    };
+    auto params = [&](float2 (&v)[C / 2]) {
+        float f[NV][VEC] = {};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * nt + t) * VEC < K) load_param<VEC>(gamma, (i * nt + t) * VEC, f[i]);
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j)
+            v[j] = make_float2(f[(2 * j) / VEC][(2 * j) % VEC], f[(2 * j + 1) / VEC][(2 * j + 1) % VEC]);
+    };
+    float2 ag[C / 2] = {}, ab[C / 2] = {}, gam[C / 2];
+    if constexpr (KEEP) params(gam);
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) stage(s, blockIdx.x + (int64_t)s * gridDim.x);
     int st = 0, par = 0;
     const float inv = 1.0f / (float)K;
+    float mean = 0.0f, rs = 0.0f;
+    if (blockIdx.x < R) {
+        mean = __ldg(mu + blockIdx.x);
+        rs = __ldg(rstd + blockIdx.x);
+    }
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         int ahead = st + STAGES - 1;
         if (ahead >= STAGES) ahead -= STAGES;
         stage(ahead, r + (int64_t)(STAGES - 1) * gridDim.x);
-        const float mean = __ldg(mu + r), rs = __ldg(rstd + r);
+        const int64_t rn = r + gridDim.x < R ? r + gridDim.x : r;
+        const float mean_n = __ldg(mu + rn), rs_n = __ldg(rstd + rn);
         cp_async_wait<STAGES - 1>();
-        float s1 = 0.0f, s2 = 0.0f;
+        float2 xh[C / 2], w[C / 2];
+        auto load_row = [&]() {
+            fetch(st, 0, xh);
+            fetch(st, 1, w);
+            if constexpr (!KEEP) params(gam);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + t) * VEC;
-            if (c >= K) continue;
-            float xv[VEC], dv[VEC], g[VEC];
-            P::to_floats(*slot(st, 0, i), xv);
-            P::to_floats(*slot(st, 1, i), dv);
-            load_param<VEC>(gamma, c, g);
+            for (int j = 0; j < C / 2; ++j) xh[j] = __fmul2_rn(__fadd2_rn(xh[j], f2(-mean)), f2(rs));
+        };
+        load_row();
+        float2 t1 = f2(0.0f), t2 = f2(0.0f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float xh = (xv[j] - mean) * rs, w = dv[j] * g[j];
-                ag[i][j] = fmaf(dv[j], xh, ag[i][j]);
-                ab[i][j] += dv[j];
-                s1 += w;
-                s2 = fmaf(w, xh, s2);
-            }
+        for (int j = 0; j < C / 2; ++j) {
+            ag[j] = __ffma2_rn(w[j], xh[j], ag[j]);
+            ab[j] = __fadd2_rn(ab[j], w[j]);
+            w[j] = __fmul2_rn(w[j], gam[j]);
+            t1 = __fadd2_rn(t1, w[j]);
+            t2 = __ffma2_rn(w[j], xh[j], t2);
         }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
+        float s1 = warp_sum(t1.x + t1.y), s2 = warp_sum(t2.x + t2.y);
         if (warps > 1) {
             if ((t & 31) == 0) {
                 red[par][0][warp] = s1;
@@ -439,26 +469,32 @@ __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const
             s2 = block_total(red[par][1], warps);
         }
         const float c1 = s1 * inv, c2 = s2 * inv;
+        if constexpr (!KEEP) {
+            load_row();
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) w[j] = __fmul2_rn(w[j], gam[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j)
+            w[j] = __fmul2_rn(__ffma2_rn(xh[j], f2(-c2), __fadd2_rn(w[j], f2(-c1))), f2(rs));
+        if (dres) {
+            fetch(st, 2, xh);
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) w[j] = __fadd2_rn(w[j], xh[j]);
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + t) * VEC;
-            if (c >= K) continue;
-            float xv[VEC], dv[VEC], g[VEC];
-            P::to_floats(*slot(st, 0, i), xv);
-            P::to_floats(*slot(st, 1, i), dv);
-            load_param<VEC>(gamma, c, g);
+            float v[VEC];
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float xh = (xv[j] - mean) * rs;
-                dv[j] = rs * (fmaf(dv[j], g[j], -c1) - xh * c2);
+                const int e = i * VEC + j;
+                v[j] = (e & 1) ? w[e / 2].y : w[e / 2].x;
             }
-            if (dres) {
-                P::to_floats(*slot(st, 2, i), xv);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) dv[j] += xv[j];
-            }
-            *reinterpret_cast<Raw*>(dx + r * K + c) = P::from_floats(dv);
+            if (c < K) *reinterpret_cast<Raw*>(dx + r * K + c) = P::from_floats(v);
         }
+        mean = mean_n;
+        rs = rs_n;
         par ^= 1;
         if (++st == STAGES) st = 0;
     }
@@ -469,8 +505,9 @@ __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const
         if (c >= K) continue;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            pg[c + j] = ag[i][j];
-            pg[K + c + j] = ab[i][j];
+            const int e = i * VEC + j;
+            pg[c + j] = (e & 1) ? ag[e / 2].y : ag[e / 2].x;
+            pg[K + c + j] = (e & 1) ? ab[e / 2].y : ab[e / 2].x;
         }
     }
 }
@@ -485,10 +522,26 @@ __device__ __forceinline__ void act_bwd_rows(const __nv_bfloat16* __restrict__ d
                                              int64_t r0, int64_t r1, int64_t N, int64_t c, __nv_bfloat16* __restrict__ dz,
                                              uint8_t* __restrict__ q, int fmt, float m, float2 (&sum)[4], uint32_t& amax)
 {
-#pragma unroll 2
+    // the loads run two of the warp's rows ahead of the arithmetic
+    constexpr int AHEAD = 2;
+    uint4 zn[AHEAD], dn[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (r0 + 8 * i < r1) {
+            zn[i] = __ldcs(reinterpret_cast<const uint4*>(z + (r0 + 8 * i) * N + c));
+            dn[i] = __ldcs(reinterpret_cast<const uint4*>(dy + (r0 + 8 * i) * N + c));
+        }
     for (int64_t r = r0; r < r1; r += 8) {
-        const uint4 zr = __ldcs(reinterpret_cast<const uint4*>(z + r * N + c));
-        const uint4 dr = __ldcs(reinterpret_cast<const uint4*>(dy + r * N + c));
+        const uint4 zr = zn[0], dr = dn[0];
+#pragma unroll
+        for (int i = 0; i + 1 < AHEAD; ++i) {
+            zn[i] = zn[i + 1];
+            dn[i] = dn[i + 1];
+        }
+        if (r + 8 * AHEAD < r1) {
+            zn[AHEAD - 1] = __ldcs(reinterpret_cast<const uint4*>(z + (r + 8 * AHEAD) * N + c));
+            dn[AHEAD - 1] = __ldcs(reinterpret_cast<const uint4*>(dy + (r + 8 * AHEAD) * N + c));
+        }
         const uint32_t zw[4] = {zr.x, zr.y, zr.z, zr.w}, dw[4] = {dr.x, dr.y, dr.z, dr.w};
         float2 v[4];
 #pragma unroll
@@ -609,11 +662,10 @@ cudaError_t ln_fwd(const LnArgs& a, cudaStream_t st, int sms)
 
 constexpr int kSmemCta = 227 * 1024;
 
-template <typename T, int VEC, int STAGES>
-cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int smem, int* parts)
+template <typename T, int VEC, int C, int STAGES>
+cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int threads, int smem, int* parts)
 {
-    const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
-    auto kern = k_ln_bwd<T, VEC, STAGES>;
+    auto kern = k_ln_bwd<T, VEC, C, STAGES>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), kSmemCta - 2048);
     if (e != cudaSuccess) return e;
     int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, smem, sms);
@@ -625,15 +677,23 @@ cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int smem, int
     return cudaGetLastError();
 }
 
+// three stages of the ring where they fit, else two or one
+template <typename T, int VEC, int C>
+cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
+{
+    const int threads = 32 * (int)cdiv(a.K, 32 * C);
+    const int stage = threads * C * (int)sizeof(T) * (a.dres ? 3 : 2);
+    const int room = kSmemCta - 2048;
+    if (3 * stage <= room) return ln_bwd_rows<T, VEC, C, 3>(a, st, sms, threads, 3 * stage, parts);
+    if (2 * stage <= room) return ln_bwd_rows<T, VEC, C, 2>(a, st, sms, threads, 2 * stage, parts);
+    return ln_bwd_rows<T, VEC, C, 1>(a, st, sms, threads, stage, parts);
+}
+
 template <typename T, int VEC>
 cudaError_t ln_bwd_vec(const LnArgs& a, cudaStream_t st, int sms, int* parts)
 {
-    const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
-    const int stage = threads * kLnCols * (int)sizeof(T) * (a.dres ? 3 : 2);
-    const int room = kSmemCta - 2048;
-    if (3 * stage <= room) return ln_bwd_rows<T, VEC, 3>(a, st, sms, 3 * stage, parts);
-    if (2 * stage <= room) return ln_bwd_rows<T, VEC, 2>(a, st, sms, 2 * stage, parts);
-    return ln_bwd_rows<T, VEC, 1>(a, st, sms, stage, parts);
+    if (a.K <= 1024 * 8) return ln_bwd_cols<T, VEC, 8>(a, st, sms, parts);
+    return ln_bwd_cols<T, VEC, 16>(a, st, sms, parts);
 }
 
 template <typename T>
@@ -660,7 +720,7 @@ cudaError_t ln_bwd(const LnArgs& a, cudaStream_t st, int sms)
                      (const float*)a.rstd, a.M, a.K, part);
         }
     }
-    launch_k(k_col_reduce, (unsigned)cdiv(2 * a.K, 32), 256, 0, st, (const float*)part, parts, 2 * a.K, a.dgamma, a.K,
+    launch_k(k_col_reduce, (unsigned)cdiv(2 * a.K, 32), 1024, 0, st, (const float*)part, parts, 2 * a.K, a.dgamma, a.K,
              a.dbeta);
     return cudaGetLastError();
 }
@@ -705,7 +765,7 @@ cudaError_t launch_act_bwd(const ActBwdArgs& a, cudaStream_t st, int sms)
                  static_cast<__nv_bfloat16*>(a.dz), a.q, a.q_format, a.q_state, a.q_history_len, part);
     }
     if (a.dbias)
-        launch_k(k_col_reduce, (unsigned)cdiv(a.N, 32), 256, 0, st, (const float*)part, parts, a.N, a.dbias, a.N,
+        launch_k(k_col_reduce, (unsigned)cdiv(a.N, 32), 1024, 0, st, (const float*)part, parts, a.N, a.dbias, a.N,
                  (float*)nullptr);
     return cudaGetLastError();
 }
