@@ -54,58 +54,139 @@ constexpr int kFfnStages = 6;
 constexpr int kFfnEpiWarps = 8;                  // two per TMEM lane quarter
 constexpr int kFfnThreads = 32 * (2 + kFfnEpiWarps);
 constexpr int kFfnBN = 256, kFfnBH = 128;
-using FfnSmem = Smem<kFfnBH, kFfnStages, 2>;
+using FfnSmem = Smem<kFfnBH, kFfnStages, 2, 4 * kFfnEpiWarps>;   // per epilogue warp: four 1 KB staging boxes
 
 // ------------------------------------------------------------------ epilogue pieces
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+__device__ __forceinline__ uint32_t pack_bf16(float2 v)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store32_bf16(__nv_bfloat16* d, int left, const float (&v)[32])
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// |v| as fp32 bits: their unsigned maximum is the amax, a NaN above everything
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// the first `left` of 32 columns, nothing where keep is 0
+__device__ __forceinline__ void max32(uint32_t& amax, const float2 (&v)[16], int left, uint32_t keep)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (2 * j < left) m = max(m, max(abs_bits(v[j].x), abs_bits(v[j].y)));
+    amax = max(amax, m & keep);
+}
+// 32 codes of one row
+__device__ __forceinline__ void codes32(uint32_t (&w)[8], const float2 (&v)[16], float m, int fmt)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 a = __fmul2_rn(v[2 * j], f2(m)), b = __fmul2_rn(v[2 * j + 1], f2(m));
+        w[j] = fmt == kE4M3 ? (cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16))
+                            : (cvt_e5m2x2(a.x, a.y) | (cvt_e5m2x2(b.x, b.y) << 16));
+    }
+}
+__device__ __forceinline__ void store32_bf16(__nv_bfloat16* d, int left, const float2 (&v)[16])
 {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
         if (8 * c + 8 <= left)
-            *reinterpret_cast<uint4*>(d + 8 * c) =
-                make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                           pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+            *reinterpret_cast<uint4*>(d + 8 * c) = make_uint4(pack_bf16(v[4 * c]), pack_bf16(v[4 * c + 1]),
+                                                              pack_bf16(v[4 * c + 2]), pack_bf16(v[4 * c + 3]));
 }
-__device__ __forceinline__ void store32_f32(float* d, int left, const float (&v)[32])
-{
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (4 * c + 4 <= left)
-            *reinterpret_cast<float4*>(d + 4 * c) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-}
-__device__ __forceinline__ void store32_codes(uint8_t* q, int left, const float (&v)[32], float m, int fmt)
+__device__ __forceinline__ void store32_codes(uint8_t* q, int left, const float2 (&v)[16], float m, int fmt)
 {
     uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float a = __fmul_rn(v[4 * j], m), b = __fmul_rn(v[4 * j + 1], m);
-        const float c = __fmul_rn(v[4 * j + 2], m), d = __fmul_rn(v[4 * j + 3], m);
-        w[j] = fmt == kE4M3 ? (cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16))
-                            : (cvt_e5m2x2(a, b) | (cvt_e5m2x2(c, d) << 16));
-    }
+    codes32(w, v, m, fmt);
     if (16 <= left) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
     if (32 <= left) *reinterpret_cast<uint4*>(q + 16) = make_uint4(w[4], w[5], w[6], w[7]);
 }
-// the largest |v| as fp32 bits, a NaN above everything
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-__device__ __forceinline__ void max32(uint32_t& amax, const float (&v)[32], int left)
-{
+
+// Staged bulk stores of one epilogue warp: 4 KB, four boxes of 32 rows x 32
+// bytes.  A row segment of 32 bytes per lane and one bulk store per box write
+// whole sectors to L2, where 16-byte stores by lane write each sector twice.
+// Boxes go out as they are filled; when the four are used up the warp waits
+// until the earlier ones have been read.
+struct Stager {
+    uint8_t* buf;
+    int lane, slot;
+    // a chunk's first box waits until the previous chunk's have been read
+    __device__ __forceinline__ void next_chunk() { slot = 4; }
+    __device__ __forceinline__ void reset()
+    {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        slot = 0;
+    }
+    __device__ __forceinline__ uint8_t* take(int boxes)
+    {
+        if (slot + boxes > 4) reset();
+        uint8_t* p = buf + slot * kStageBytes;
+        slot += boxes;
+        return p + 32 * lane;
+    }
+    // bulk stores of `boxes` boxes of `cols` columns each at (col, row0)
+    __device__ __forceinline__ void send(const CUtensorMap* m, int boxes, int cols, int col, int row0, int left)
+    {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            const uint8_t* p = buf + (slot - boxes) * kStageBytes;
+            for (int i = 0; i < boxes; ++i)
+                if (i * cols < left) bulk_store_2d(m, col + i * cols, row0, p + i * kStageBytes);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void bf16(const CUtensorMap* m, const float2 (&v)[16], int col, int row0, int left)
+    {
+        uint8_t* p = take(2);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < left) amax = max(amax, abs_bits(v[j]));
-}
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(p + (c >> 1) * kStageBytes + (c & 1) * 16) =
+                make_uint4(pack_bf16(v[4 * c]), pack_bf16(v[4 * c + 1]), pack_bf16(v[4 * c + 2]), pack_bf16(v[4 * c + 3]));
+        send(m, 2, 16, col, row0, left);
+    }
+    __device__ __forceinline__ void f32(const CUtensorMap* m, const float2 (&v)[16], int col, int row0, int left)
+    {
+        uint8_t* p = take(4);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(p + (c >> 1) * kStageBytes + (c & 1) * 16) =
+                make_float4(v[2 * c].x, v[2 * c].y, v[2 * c + 1].x, v[2 * c + 1].y);
+        send(m, 4, 8, col, row0, left);
+    }
+    __device__ __forceinline__ void codes(const CUtensorMap* m, const float2 (&v)[16], float mult, int fmt, int col,
+                                          int row0, int left)
+    {
+        uint32_t w[8];
+        codes32(w, v, mult, fmt);
+        uint8_t* p = take(1);
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        send(m, 1, 32, col, row0, left);
+    }
+};
+
+// 32 columns of a row of bf16 (64 bytes) or fp32 (128 bytes) into registers,
+// ahead of their use; zeros past `left`
 template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N])
+__device__ __forceinline__ void fetch_row(uint4* raw, const void* src, int bytes_left)
 {
-    static_assert(N == 4 || N == 8 || N == 16, "columns");
-    if constexpr (N == 4) tmem_ld_32x32b_x4(taddr, r);
-    else if constexpr (N == 8) tmem_ld_32x32b_x8(taddr, r);
-    else tmem_ld_32x32b_x16(taddr, r);
+    const uint4* s = static_cast<const uint4*>(src);
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = 16 * (i + 1) <= bytes_left ? __ldg(s + i) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ float2 raw_bf16(const uint4* raw, int j)     // columns 2 j, 2 j + 1
+{
+    const uint4 w = raw[j >> 2];
+    return unpack_bf16((j & 3) == 0 ? w.x : (j & 3) == 1 ? w.y : (j & 3) == 2 ? w.z : w.w);
+}
+__device__ __forceinline__ float2 raw_f32(const uint4* raw, int j)
+{
+    const uint4 w = raw[j >> 1];
+    return (j & 1) ? make_float2(__uint_as_float(w.z), __uint_as_float(w.w))
+                   : make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
 }
 __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 {
@@ -113,28 +194,13 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
     return old;
 }
-__device__ __forceinline__ void load32_bf16(const __nv_bfloat16* s, int left, float (&v)[32])
-{
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (8 * c + 8 <= left) w = __ldg(reinterpret_cast<const uint4*>(s + 8 * c));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[8 * c + 2 * j] = __uint_as_float(u[j] << 16);
-            v[8 * c + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
-    }
-}
-
 // ------------------------------------------------------------------ kernel
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     k_ffn_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FfnParams p,
-               uint32_t idesc, TileSched sched)
+               uint32_t idesc, TileSched sched, const __grid_constant__ CUtensorMap tmO0,
+               const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2)
 {
-    pdl_enter();
     constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = kFfnStages;
     constexpr bool b_mn = KIND == kEpiGluBwd;          // Wd [K][F]: MN-major
     using L = FfnSmem;
@@ -151,8 +217,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     const uint32_t rank = cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // what touches no global memory of the kernel before this one runs ahead
+    // of the wait on it
     if (threadIdx.x == 0) {
-        s_skip = rank == 0 ? *reinterpret_cast<volatile int*>(p.err) : 0;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -166,19 +233,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
     }
-    __syncthreads();
-    cluster_sync_all();
-    int skip = s_skip;
-    if (rank != 0) skip = (int)ld_shared_cluster_u32(cluster_map(smem_addr(&s_skip), 0));
-    cluster_sync_all();
-    if (skip) return;
     if (warp == 1) {
         tmem_alloc_pair(holder, TMEM_COLS);
         tmem_relinquish_pair();
     }
+    pdl_enter();
+    if (threadIdx.x == 0) s_skip = rank == 0 ? *reinterpret_cast<volatile int*>(p.err) : 0;
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();                        // both CTAs' barriers initialised, the leader's flag written
     tc_fence_after();
+    int skip = s_skip;
+    if (rank != 0) skip = (int)ld_shared_cluster_u32(cluster_map(smem_addr(&s_skip), 0));
     const uint32_t tmem_base = *holder;
 
     const int num_tiles = sched.num_m * sched.num_n;
@@ -186,7 +252,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err_cluster(bar, parity, p.err); };
 
-    if (warp == 0) {
+    if (skip) {
+        // a wait ran out earlier: compute nothing (the same decision in both CTAs)
+    } else if (warp == 0) {
         if (lane == 0) {
             constexpr uint32_t PAIR_TX = 2u * (uint32_t)L::STAGE;
             const uint32_t full0 = cluster_map(smem_addr(full), 0);
@@ -290,141 +358,142 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         const float qm = p.Q ? p.qstate[p.qH] : 1.0f;
         uint32_t amax = 0;
         const uint32_t aempty0 = cluster_map(smem_addr(aempty), 0);
+        Stager out{smem + L::STG_OFF + (warp - 2) * 4 * kStageBytes, lane, 0};
+        // columns of a tile in this warp's share; what its epilogue reads
+        // beside the sums (the residual, or g and u) is fetched one chunk of
+        // 32 columns ahead, the first chunk's before the tile's sums are done
+        constexpr int TN = KIND == kEpiGlu ? BH : BN;
+        const int c_begin = part * (TN / 2), c_end = c_begin + TN / 2;
+        uint4 pre[8];
+        auto fetch = [&](int row, int col) {
+            const int left = row < p.M ? min(p.N - col, 32) : 0;
+            if constexpr (KIND == kEpiAct) {
+                if (!p.res) return;
+                if (p.res_f32) fetch_row<8>(pre, static_cast<const float*>(p.res) + (int64_t)row * p.N + col, 4 * left);
+                else fetch_row<4>(pre, static_cast<const __nv_bfloat16*>(p.res) + (int64_t)row * p.N + col, 2 * left);
+            } else if constexpr (KIND == kEpiGluBwd) {
+                const __nv_bfloat16* s = p.gu + (int64_t)row * 2 * p.N + col;
+                fetch_row<4>(pre, s, 2 * left);
+                fetch_row<4>(pre + 4, s + p.N, 2 * left);
+            }
+        };
         int lt = 0;
         for (int t = cid; t < num_tiles; t += ncl, ++lt) {
             const int b = lt & 1;
             const uint32_t u = (uint32_t)(lt >> 1);
+            int mb, nb;
+            sched.coords(t, mb, nb);
+            const int row0 = mb * 2 * BM + (int)rank * BM + quarter * 32, row = row0 + lane;
+            const uint32_t keep = row < p.M ? 0xFFFFFFFFu : 0u;
+            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * BN);
+            fetch(row, nb * TN + c_begin);
+            // gemm_act: lane l holds the bias of columns 4 l .. 4 l + 3 of the share
+            [[maybe_unused]] float4 bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if constexpr (KIND == kEpiAct) {
+                const int bc = nb * TN + c_begin + 4 * lane;
+                if (p.bias && bc + 4 <= p.N) bias = __ldg(reinterpret_cast<const float4*>(p.bias + bc));
+            }
             const bool ok = wait(&afull[b], u & 1u);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
-            int mb, nb;
-            sched.coords(t, mb, nb);
-            const int row = mb * 2 * BM + (int)rank * BM + quarter * 32 + lane;
-            const bool live = row < p.M;
-            const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * BN);
-            if constexpr (KIND == kEpiGlu) {
 #pragma unroll 1
-                for (int c = part * (BH / 2); c < (part + 1) * (BH / 2); c += 32) {
+            for (int c = c_begin; c < c_end && row0 < p.M; c += 32) {
+                const int col = nb * TN + c, left = p.N - col;
+                if (left <= 0) break;
+                float2 v[16];
+                if constexpr (KIND == kEpiGlu) {
                     uint32_t rg[32], ru[32];
                     tmem_ld_32x32b_x32(taddr + (uint32_t)c, rg);
                     tmem_ld_32x32b_x32(taddr + (uint32_t)(BH + c), ru);
                     tmem_ld_wait();
-                    const int col = nb * BH + c, left = p.N - col;
-                    float g[32], v[32];
+                    float2 g[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        g[j] = __uint_as_float(rg[j]) * scale;
-                        v[j] = __uint_as_float(ru[j]) * scale;
+                    for (int j = 0; j < 16; ++j) {
+                        g[j] = __fmul2_rn(make_float2(__uint_as_float(rg[2 * j]), __uint_as_float(rg[2 * j + 1])), f2(scale));
+                        v[j] = __fmul2_rn(make_float2(__uint_as_float(ru[2 * j]), __uint_as_float(ru[2 * j + 1])), f2(scale));
                     }
-                    if (live && left > 0) {
-                        if (p.Z) {
-                            __nv_bfloat16* z = p.Z + (int64_t)row * 2 * p.N + col;
-                            store32_bf16(z, left, g);
-                            store32_bf16(z + p.N, left, v);
-                        }
-                        act_dispatch(p.act, [&](auto tag) {
+                    if (p.Z) {
+                        out.next_chunk();
+                        out.bf16(&tmO0, g, col, row0, left);
+                        out.bf16(&tmO1, v, col, row0, left);
+                    }
+                    act_dispatch(p.act, [&](auto tag) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const float2 h = __fmul2_rn(make_float2(v[j], v[j + 1]),
-                                                            act_f2<decltype(tag)::act>(make_float2(g[j], g[j + 1])));
-                                v[j] = h.x;
-                                v[j + 1] = h.y;
-                            }
-                        });
+                        for (int j = 0; j < 16; ++j) v[j] = __fmul2_rn(v[j], act_f2<decltype(tag)::act>(g[j]));
+                    });
+                    if (p.Q) max32(amax, v, left, keep);
+                    if (keep) {
                         if (p.D) store32_bf16(static_cast<__nv_bfloat16*>(p.D) + (int64_t)row * p.N + col, left, v);
-                        if (p.Q) {
-                            max32(amax, v, left);
-                            store32_codes(p.Q + (int64_t)row * p.N + col, left, v, qm, p.qfmt);
-                        }
+                        if (p.Q) store32_codes(p.Q + (int64_t)row * p.N + col, left, v, qm, p.qfmt);
                     }
                     __syncwarp();
-                }
-            } else {
-#pragma unroll 1
-                for (int c = part * BH; c < (part + 1) * BH; c += 32) {
+                } else {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
                     tmem_ld_wait();
-                    const int col = nb * BN + c, left = p.N - col;
-                    if (live && left > 0) {
-                        float v[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * scale;
-                        if constexpr (KIND == kEpiAct) {
-                            if (p.bias) {
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
+                    out.next_chunk();
+                    if constexpr (KIND == kEpiAct) {
+                        if (p.bias) {
+                            const int from = (c - c_begin) / 4;       // the lane that holds column c
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (j < left) v[j] += __ldg(p.bias + col + j);
+                            for (int j = 0; j < 16; j += 2) {
+                                const int s = from + j / 2;
+                                v[j] = __fadd2_rn(v[j], make_float2(__shfl_sync(0xFFFFFFFFu, bias.x, s),
+                                                                    __shfl_sync(0xFFFFFFFFu, bias.y, s)));
+                                v[j + 1] = __fadd2_rn(v[j + 1], make_float2(__shfl_sync(0xFFFFFFFFu, bias.z, s),
+                                                                            __shfl_sync(0xFFFFFFFFu, bias.w, s)));
                             }
-                            if (p.Z) store32_bf16(p.Z + (int64_t)row * p.N + col, left, v);
-                            act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    const float2 y = act_f2<decltype(tag)::act>(make_float2(v[j], v[j + 1]));
-                                    v[j] = y.x;
-                                    v[j + 1] = y.y;
-                                }
-                            });
-                            if (p.res) {
-                                if (p.res_f32) {
-                                    const float* s = static_cast<const float*>(p.res) + (int64_t)row * p.N + col;
-#pragma unroll
-                                    for (int j = 0; j < 32; j += 4)
-                                        if (j + 4 <= left) {
-                                            const float4 w = __ldg(reinterpret_cast<const float4*>(s + j));
-                                            v[j] += w.x;
-                                            v[j + 1] += w.y;
-                                            v[j + 2] += w.z;
-                                            v[j + 3] += w.w;
-                                        }
-                                } else {
-                                    float s[32];
-                                    load32_bf16(static_cast<const __nv_bfloat16*>(p.res) + (int64_t)row * p.N + col, left, s);
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] += s[j];
-                                }
-                            }
-                            if (p.D) {
-                                if (p.d_f32) store32_f32(static_cast<float*>(p.D) + (int64_t)row * p.N + col, left, v);
-                                else store32_bf16(static_cast<__nv_bfloat16*>(p.D) + (int64_t)row * p.N + col, left, v);
-                            }
-                            if (p.Q) {
-                                max32(amax, v, left);
-                                store32_codes(p.Q + (int64_t)row * p.N + col, left, v, qm, p.qfmt);
-                            }
-                        } else {
-                            float g[32], w[32];
-                            const __nv_bfloat16* s = p.gu + (int64_t)row * 2 * p.N + col;
-                            load32_bf16(s, left, g);
-                            load32_bf16(s + p.N, left, w);
-                            act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    float2 f, d;
-                                    act_fd2<decltype(tag)::act>(make_float2(g[j], g[j + 1]), f, d);
-                                    const float2 dh = make_float2(v[j], v[j + 1]);
-                                    const float2 dg = __fmul2_rn(__fmul2_rn(dh, make_float2(w[j], w[j + 1])), d);
-                                    const float2 du = __fmul2_rn(dh, f);
-                                    g[j] = dg.x;
-                                    g[j + 1] = dg.y;
-                                    w[j] = du.x;
-                                    w[j + 1] = du.y;
-                                }
-                            });
-                            max32(amax, g, left);
-                            max32(amax, w, left);
-                            uint8_t* q = p.Q + (int64_t)row * 2 * p.N + col;
-                            store32_codes(q, left, g, qm, p.qfmt);
-                            store32_codes(q + p.N, left, w, qm, p.qfmt);
                         }
+                        if (p.Z) out.bf16(&tmO0, v, col, row0, left);
+                        act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = act_f2<decltype(tag)::act>(v[j]);
+                        });
+                        if (p.res) {
+                            if (p.res_f32) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_f32(pre, j));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_bf16(pre, j));
+                            }
+                            if (c + 32 < c_end) fetch(row, col + 32);
+                        }
+                        if (p.D) {
+                            if (p.d_f32) out.f32(&tmO1, v, col, row0, left);
+                            else out.bf16(&tmO1, v, col, row0, left);
+                        }
+                        if (p.Q) {
+                            max32(amax, v, left, keep);
+                            out.codes(&tmO2, v, qm, p.qfmt, col, row0, left);
+                        }
+                    } else {
+                        float2 g[16];
+                        act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float2 f, d;
+                                act_fd2<decltype(tag)::act>(raw_bf16(pre, j), f, d);
+                                g[j] = __fmul2_rn(__fmul2_rn(v[j], raw_bf16(pre + 4, j)), d);
+                                v[j] = __fmul2_rn(v[j], f);
+                            }
+                        });
+                        if (c + 32 < c_end) fetch(row, col + 32);
+                        max32(amax, g, left, keep);
+                        max32(amax, v, left, keep);
+                        out.codes(&tmO0, g, qm, p.qfmt, col, row0, left);
+                        out.codes(&tmO1, v, qm, p.qfmt, col, row0, left);
                     }
-                    __syncwarp();
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(aempty0 + 8u * b);
         }
+        stage_store_drain(lane);
         if (p.Q) {
             amax = __reduce_max_sync(0xFFFFFFFFu, amax);
             if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(p.qstate), amax);
@@ -441,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
 // ================================================================== few rows
 // Products too small for 256 x 256 tiles on every SM: few rows (serving:
 // single tokens and small batches, where the time is the weights' bytes) or
-// few tiles.  The roles are swapped -- 128 weight rows are the M of the MMA
+// few tiles (rows_plan chooses).  The roles are swapped -- 128 weight rows are the M of the MMA
 // and NT tokens its N -- and the K loop is split over all SMs.  The work is
 // the list of (tile, 128-wide K block) pairs in tile order; CTA i of G takes
 // the i-th G-th of it, so every SM streams the same number of bytes whatever
@@ -478,7 +547,6 @@ struct RowsLayout {
     static constexpr int BYTES = BAR_OFF + 512 + 1024;
     static constexpr uint32_t TMEM_COLS = 2 * NT;
     static constexpr int SHARE = NT / 4;                                 // tokens of an epilogue warp
-    static constexpr int CH = SHARE < 8 ? SHARE : 8;                     // tokens of a chunk
     static_assert((2 * STAGES + 5) * 8 + 8 <= 512, "barriers");
     static_assert(TMEM_COLS >= 32 && TMEM_COLS <= 512, "tensor memory");
 };
@@ -503,23 +571,22 @@ __device__ __forceinline__ int rows_owner(const RowsParams& w, int u)
     return (int)((((int64_t)u + 1) * gridDim.x - 1) / ((int64_t)w.wtiles * w.mtiles * w.nkb));
 }
 
-// The residual of CH tokens of column n; the loads of a chunk are in flight
-// together, and a caller issues them ahead of its sums.
+// The residual of CH tokens of column n as stored bits: the loads of a chunk
+// are in flight together, and nothing here waits for them, so a caller fetches
+// ahead of its sums (converted at once, or fetched where it is added, the
+// latency was up to a third of a small product's time).
 template <int CH>
-__device__ __forceinline__ void rows_residual(const FfnParams& p, int m0, int n, float (&r)[CH])
+__device__ __forceinline__ void rows_residual(const FfnParams& p, int m0, int n, uint32_t (&r)[CH])
 {
     if (!p.res || n >= p.N) return;
     if (p.res_f32) {
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            if (m0 + j < p.M) r[j] = __ldg(static_cast<const float*>(p.res) + (int64_t)(m0 + j) * p.N + n);
+            if (m0 + j < p.M) r[j] = __ldg(static_cast<const uint32_t*>(p.res) + (int64_t)(m0 + j) * p.N + n);
     } else {
-        uint32_t b[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            if (m0 + j < p.M) b[j] = __ldg(static_cast<const uint16_t*>(p.res) + (int64_t)(m0 + j) * p.N + n);
-#pragma unroll
-        for (int j = 0; j < CH; ++j) r[j] = __uint_as_float(b[j] << 16);
+            if (m0 + j < p.M) r[j] = __ldg(static_cast<const uint16_t*>(p.res) + (int64_t)(m0 + j) * p.N + n);
     }
 }
 
@@ -527,7 +594,7 @@ __device__ __forceinline__ void rows_residual(const FfnParams& p, int m0, int n,
 // raw sums (glu: of the gate, up those of the up row), r the residual.
 template <int KIND, int CH>
 __device__ __forceinline__ void rows_epilogue(const FfnParams& p, float (&a)[CH], float (&up)[CH],
-                                              const float (&r)[CH], int m0, int n, float scale, float qm,
+                                              const uint32_t (&r)[CH], int m0, int n, float scale, float qm,
                                               uint32_t& amax)
 {
     const int live = p.M - m0;                   // tokens of the chunk inside the matrix
@@ -550,7 +617,7 @@ __device__ __forceinline__ void rows_epilogue(const FfnParams& p, float (&a)[CH]
         });
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            if (p.res) a[j] += r[j];
+            if (p.res) a[j] += __uint_as_float(p.res_f32 ? r[j] : r[j] << 16);
             if (p.D && j < live) {
                 const int64_t o = (int64_t)(m0 + j) * p.N + n;
                 if (p.d_f32) static_cast<float*>(p.D)[o] = a[j];
@@ -603,7 +670,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                RowsParams w, uint32_t idesc)
 {
     using L = RowsLayout<KIND, NT>;
-    constexpr int STAGES = L::STAGES, CH = L::CH;
+    constexpr int STAGES = L::STAGES;
     constexpr bool GLU = L::GLU;
     constexpr int BOX = L::COLS;                 // weight rows of a load (glu: gate rows, then up rows)
     extern __shared__ uint8_t smem_raw[];
@@ -795,7 +862,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                             up[3] += vu[s].w;
                         }
                 }
-                const float none[4] = {};
+                const uint32_t none[4] = {};
                 if (n < p.N) rows_epilogue<KIND, 4>(p, g, up, none, m_tile + 4 * i, n, scale, qm, amax);
             }
         };
@@ -810,29 +877,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             const int t0 = part * L::SHARE;                 // this warp's first token in the tile
             const int left = p.M - mt * NT;                 // tokens of the tile inside the matrix
             const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * NT);
+            uint32_t rs[L::SHARE];                          // the residual, fetched ahead of the sums
+            if (!GLU && whole) rows_residual<L::SHARE>(p, mt * NT + t0, n, rs);
             if (!bar_all(1, ETH, wait(&afull[b], (uint32_t)(seg >> 1) & 1u))) break;
             tc_fence_after();
             // this CTA's block of sums: in shared memory for a whole glu tile
             // (the barrier above says that the last one has been read)
             float* mine = GLU && whole ? sums : w.part + ((int64_t)blockIdx.x * 2 + (kb0 == 0 ? 1 : 0)) * (NT * BM);
-#pragma unroll 1
-            for (int c = t0; c < t0 + L::SHARE && c < left; c += CH) {
-                float rs[CH];
-                if (!GLU && whole) rows_residual<CH>(p, mt * NT + c, n, rs);
-                uint32_t r[CH];
-                tmem_ld_cols<CH>(taddr + c, r);
+#pragma unroll
+            for (int c = 0; c < L::SHARE; c += 4) {
+                if (t0 + c >= left) break;
+                uint32_t r[4];
+                tmem_ld_32x32b_x4(taddr + t0 + c, r);
                 tmem_ld_wait();
                 if (GLU || !whole) {
-#pragma unroll
-                    for (int j = 0; j < CH; j += 4)
-                        if (c + j < left)
-                            *reinterpret_cast<uint4*>(mine + (c + j) * BM + 4 * wr) =
-                                make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+                    *reinterpret_cast<uint4*>(mine + (t0 + c) * BM + 4 * wr) = make_uint4(r[0], r[1], r[2], r[3]);
                 } else if (n < p.N) {
-                    float a[CH];
+                    float a[4];
+                    uint32_t rj[4];
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) a[j] = __uint_as_float(r[j]);
-                    rows_epilogue<KIND, CH>(p, a, a, rs, mt * NT + c, n, scale, qm, amax);
+                    for (int j = 0; j < 4; ++j) {
+                        a[j] = __uint_as_float(r[j]);
+                        rj[j] = rs[c + j];
+                    }
+                    rows_epilogue<KIND, 4>(p, a, a, rj, mt * NT + t0 + c, n, scale, qm, amax);
                 }
                 __syncwarp();
             }
@@ -866,17 +934,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     // quads of tokens, up to eight loads a thread in flight
                     constexpr int SEG = 8;
                     const int parts = c1 - c0 + 1;
-#pragma unroll 1
-                    for (int c = t0; c < t0 + L::SHARE && c < left; c += 4) {
-                        float rs[4], a[4] = {};
-                        rows_residual<4>(p, mt * NT + c, n, rs);
+                    rows_residual<L::SHARE>(p, mt * NT + t0, n, rs);
+#pragma unroll
+                    for (int c = 0; c < L::SHARE; c += 4) {
+                        if (t0 + c >= left) break;
+                        float a[4] = {};
+                        uint32_t rj[4];
 #pragma unroll 1
                         for (int s0 = 0; s0 < parts; s0 += SEG) {
                             float4 v[SEG];
 #pragma unroll
                             for (int s = 0; s < SEG; ++s)
                                 if (s0 + s < parts)
-                                    v[s] = __ldcg(reinterpret_cast<const float4*>(block(s0 + s) + c * BM + 4 * wr));
+                                    v[s] = __ldcg(reinterpret_cast<const float4*>(block(s0 + s) + (t0 + c) * BM + 4 * wr));
 #pragma unroll
                             for (int s = 0; s < SEG; ++s)
                                 if (s0 + s < parts) {
@@ -886,7 +956,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                                     a[3] += v[s].w;
                                 }
                         }
-                        rows_epilogue<KIND, 4>(p, a, a, rs, mt * NT + c, n, scale, qm, amax);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) rj[j] = rs[c + j];
+                        rows_epilogue<KIND, 4>(p, a, a, rj, mt * NT + t0 + c, n, scale, qm, amax);
                     }
                 }
             }
@@ -943,33 +1015,56 @@ static cudaError_t ffn_clusters(const void* kern, int kind, int* clusters)
 }
 
 // Token columns of a few-rows tile.
-static int rows_nt(int kind, int64_t M)
-{
-    if (M <= 16) return 16;
-    if (M <= 32) return 32;
-    return M <= 64 || kind == kFfnGlu ? 64 : 128;
-}
-static int rows_cols(int kind) { return kind == kFfnGlu ? BM / 2 : BM; }
+static int rows_nt(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-// The few-rows kernel takes a product of at most 64 rows, and a larger one
-// whose tiles (128 weight rows x NT tokens) all run at once; `ctas` bounds
-// the SMs.
-static bool rows_applies(int kind, int64_t M, int64_t N, int64_t K, int64_t ctas)
+// Which kernel takes a product, and whether the few-rows one splits K, by an
+// estimate of each one's time from measurements on the GB300 (bf16 output with
+// residual, or gated codes; weights from DRAM; us):
+//   few rows  5.5, and the longest CTA's bytes at 80 KB a us (what an SM takes
+//             in); a split takes an equal share of the bytes and adds its
+//             join, as long as 128 KB + 4 KB per token column of that stream
+//   pair      8.5, what a tile's epilogue adds (pair_epi: the last tile's is
+//             not overlapped), and 0.27 per K block and wave of 256 x 256 tiles
+// Measured, few rows / pair: gemm_act N 4096, K 4096, 16 rows 9.8 / 15.8, 64
+// rows 15.1 / 16.4, 300 rows 21.3 / 18.3; N 4096, K 14336, 128 rows 25.7 / 39.1;
+// N 2064, K 1040, 300 rows 8.0 / 11.7; glu F 4096, K 4096, 64 rows 13.5 / 15.6,
+// 200 rows 23.6 / 16.0; F 14336, K 4096, 16 rows 25.0 / 31.1.
+struct RowsPlan {
+    bool use = false, split = false;
+    int grid = 0;
+};
+static RowsPlan rows_plan(int kind, int64_t M, int64_t N, int64_t K, int ctas, bool workspace, double pair_epi)
 {
-    const int64_t wt = (N + rows_cols(kind) - 1) / rows_cols(kind), nt = rows_nt(kind, M), mt = (M + nt - 1) / nt;
-    if (wt * mt > kRowsMaxTiles || wt * mt * ((K + BK - 1) / BK) >= ((int64_t)1 << 31)) return false;
-    return M <= 64 || wt * mt <= ctas;
+    RowsPlan r;
+    const int cols = kind == kFfnGlu ? BM / 2 : BM, nt = rows_nt(M);
+    const int64_t tiles = (N + cols - 1) / cols * ((M + nt - 1) / nt), nkb = (K + BK - 1) / BK, work = tiles * nkb;
+    if (tiles > kRowsMaxTiles || work >= ((int64_t)1 << 31)) return r;
+    if (ctas > kRowsMaxCtas) ctas = kRowsMaxCtas;
+    const double stage = A_BYTES + nt * BK, rate = 80e3, join = 128e3 + 4e3 * nt;
+    const int64_t most = (work + 3) / 4;                   // at least four K blocks a CTA
+    const int64_t g_split = ctas < most ? ctas : most, g_whole = ctas < tiles ? ctas : tiles;
+    const double whole = (double)((tiles + g_whole - 1) / g_whole * nkb) * stage;
+    const double share = (double)((work + g_split - 1) / g_split) * stage + join;
+    r.split = workspace && share < whole;
+    r.grid = (int)(r.split ? g_split : g_whole);
+    const int tile_n = kind == kFfnGlu ? kFfnBH : kFfnBN;
+    const int64_t pair_tiles = (M + 2 * BM - 1) / (2 * BM) * ((N + tile_n - 1) / tile_n), pairs = ctas / 2;
+    const double t_pair = 8.5 + pair_epi + 0.27 * (double)((pair_tiles + pairs - 1) / pairs * nkb);
+    r.use = 5.5 + (r.split ? share : whole) / rate < t_pair;
+    return r;
 }
 
 // bytes of the split's counters and partial sums, 0 where it never applies
 size_t ffn_workspace(int kind, int64_t M, int64_t N, int64_t K)
 {
-    if (!rows_applies(kind, M, N, K, kRowsMaxCtas)) return 0;
-    return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * rows_nt(kind, M) * BM * sizeof(float);
+    const RowsPlan r = rows_plan(kind, M, N, K, 152, true, 8.0);      // the costliest epilogue
+    if (!r.use || !r.split) return 0;
+    return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * rows_nt(M) * BM * sizeof(float);
 }
 
 template <int KIND, int NT>
-static cudaError_t launch_rows(const FfnArgs& a, const FfnParams& p, cudaStream_t st, int sms, const char** why)
+static cudaError_t launch_rows(const FfnArgs& a, const FfnParams& p, const RowsPlan& plan, cudaStream_t st,
+                               const char** why)
 {
     using L = RowsLayout<KIND, NT>;
     CUtensorMap tw, tx;
@@ -981,34 +1076,27 @@ static cudaError_t launch_rows(const FfnArgs& a, const FfnParams& p, cudaStream_
     w.wtiles = (int)((a.N + L::COLS - 1) / L::COLS);
     w.mtiles = (int)((a.M + NT - 1) / NT);
     w.nkb = (int)((a.K + BK - 1) / BK);
-    const int64_t tiles = (int64_t)w.wtiles * w.mtiles, work = tiles * w.nkb;
-    int64_t grid = sms < kRowsMaxCtas ? sms : kRowsMaxCtas;
-    // Splitting K shortens the longest CTA from whole tiles to an equal share
-    // and adds the join, about 3 us: what an SM streams of 128 KB in that time.
-    w.split = a.workspace != nullptr && ((tiles + grid - 1) / grid * w.nkb - work / grid) * L::STAGE > 128 * 1024;
-    if (w.split) {
+    w.split = plan.split;
+    if (plan.split) {
         w.counters = static_cast<uint32_t*>(a.workspace);
         w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kRowsCounterBytes);
-        const int64_t most = (work + 3) / 4;      // at least four K blocks a CTA
-        grid = grid < most ? grid : most;
-    } else {
-        grid = grid < tiles ? grid : tiles;
     }
     auto kern = k_ffn_rows<KIND, NT>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), L::BYTES);
     if (e != cudaSuccess) return e;
-    launch_k(kern, (unsigned)grid, kRowsThreads, L::BYTES, st, tw, tx, p, w, make_idesc(a.b_format, a.a_format, NT));
+    launch_k(kern, (unsigned)plan.grid, kRowsThreads, L::BYTES, st, tw, tx, p, w,
+             make_idesc(a.b_format, a.a_format, NT));
     return cudaGetLastError();
 }
 
 template <int KIND>
-static cudaError_t launch_rows_nt(const FfnArgs& a, const FfnParams& p, cudaStream_t st, int sms, const char** why)
+static cudaError_t launch_rows_nt(const FfnArgs& a, const FfnParams& p, const RowsPlan& plan, cudaStream_t st,
+                                  const char** why)
 {
-    switch (rows_nt(a.kind, a.M)) {
-    case 16: return launch_rows<KIND, 16>(a, p, st, sms, why);
-    case 32: return launch_rows<KIND, 32>(a, p, st, sms, why);
-    case 64: return launch_rows<KIND, 64>(a, p, st, sms, why);
-    default: return launch_rows<kEpiAct, 128>(a, p, st, sms, why);
+    switch (rows_nt(a.M)) {
+    case 16: return launch_rows<KIND, 16>(a, p, plan, st, why);
+    case 32: return launch_rows<KIND, 32>(a, p, plan, st, why);
+    default: return launch_rows<KIND, 64>(a, p, plan, st, why);
     }
 }
 
@@ -1037,8 +1125,14 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     cudaError_t e = device_error_word(&p.err);
     if (e != cudaSuccess) return e;
     const bool glu = a.kind == kFfnGlu, bwd = a.kind == kFfnGluBwd;
-    if (!bwd && rows_applies(a.kind, a.M, a.N, a.K, sms < kRowsMaxCtas ? sms : kRowsMaxCtas))
-        return glu ? launch_rows_nt<kEpiGlu>(a, p, st, sms, why) : launch_rows_nt<kEpiAct>(a, p, st, sms, why);
+    if (!bwd) {
+        const double epi = glu ? 0.0
+                               : (a.act != kActNone ? 1.5 : 0.0) + (a.residual ? (p.res_f32 ? 3.5 : 1.0) : 0.0) +
+                                     (a.D && p.d_f32 ? 1.5 : 0.0) + (a.Z ? 1.0 : 0.0);
+        const RowsPlan plan = rows_plan(a.kind, a.M, a.N, a.K, sms, a.workspace != nullptr, epi);
+        if (plan.use)
+            return glu ? launch_rows_nt<kEpiGlu>(a, p, plan, st, why) : launch_rows_nt<kEpiAct>(a, p, plan, st, why);
+    }
     CUtensorMap ta, tb;
     const bool ok_b = bwd ? make_tmap(&tb, a.B, a.N, a.K, BK) : make_tmap(&tb, a.B, a.K, glu ? 2 * a.N : a.N, kFfnBH);
     if (!make_tmap(&ta, a.A, a.K, a.M, BM) || !ok_b) {
@@ -1066,7 +1160,24 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     uint32_t idesc = make_idesc(a.a_format, a.b_format, kFfnBN);
     idesc = (idesc & ~(0x1Fu << 24)) | ((uint32_t)((2 * BM) >> 4) << 24);   // M = 256 over the pair
     if (bwd) idesc |= 1u << 16;                                              // B MN-major
-    launch_k(kern, grid, kFfnThreads, FfnSmem::BYTES, st, ta, tb, p, idesc, sched);
+    // outputs stored in bulk; a map that the epilogue does not use is a copy of A's
+    CUtensorMap o[3] = {ta, ta, ta};
+    bool ok = true;
+    if (bwd) {
+        ok = make_tmap_codes(&o[0], a.q_out, a.M, a.N, 2 * a.N) && make_tmap_codes(&o[1], a.q_out + a.N, a.M, a.N, 2 * a.N);
+    } else if (glu) {
+        __nv_bfloat16* z = p.Z;
+        if (z) ok = make_tmap_out(&o[0], z, a.M, a.N, true, 2 * a.N) && make_tmap_out(&o[1], z + a.N, a.M, a.N, true, 2 * a.N);
+    } else {
+        if (p.Z) ok = make_tmap_out(&o[0], p.Z, a.M, a.N, true);
+        if (p.D) ok = ok && make_tmap_out(&o[1], p.D, a.M, a.N, a.d_dtype == kBF16);
+        if (p.Q) ok = ok && make_tmap_codes(&o[2], p.Q, a.M, a.N);
+    }
+    if (!ok) {
+        *why = "cuTensorMapEncodeTiled failed (output)";
+        return cudaErrorInvalidValue;
+    }
+    launch_k(kern, grid, kFfnThreads, FfnSmem::BYTES, st, ta, tb, p, idesc, sched, o[0], o[1], o[2]);
     return cudaGetLastError();
 }
 
