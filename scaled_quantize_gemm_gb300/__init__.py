@@ -377,86 +377,84 @@ def fp8_linear_fwd_noalloc(x, w, y, bias=None, stream=None) -> None:
 
 
 # ------------------------------------------------- feed-forward sublayer
-def _nbytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
-
-
-def _matrix(t, name: str, rows: int, cols: int, dtype):
-    """an operand or output [rows][cols] whose shape the call's sizes come from"""
+# These calls serve single tokens, where the host's share counts: each buffer is
+# checked and its pointer taken in one step (a few attribute reads), and the
+# message is only put together when a check fails.
+def _mat(t, name: str, rows: int, cols: int, dtype) -> int:
+    """pointer of a contiguous [rows][cols] matrix of dtype"""
+    if t is not None and t.dtype is dtype and t.shape == (rows, cols) and t.is_contiguous():
+        return t.data_ptr()
     _need(t, name, dtype)
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
 
 
-def _vector(t, name: str, n: int, dtype=None):
-    _need(t, name, dtype if dtype is not None else _t().float32)
-    if t.numel() < n:
-        raise ValueError(f"{name}: {t.numel()} elements, needs {n}")
+def _vec(t, name: str, n: int) -> int:
+    """pointer of a contiguous fp32 vector of at least n elements"""
+    if t is not None and t.dtype is _torch.float32 and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, _torch.float32)
+    raise ValueError(f"{name}: {t.numel()} elements, needs {n}")
 
 
-def _cast_args(q, name: str, rows: int, cols: int, state, history_len: int):
+def _sized(t, name: str, dtypes) -> tuple:
+    """(pointer, rows, columns) of the contiguous matrix a call takes its sizes from"""
+    if t is None or t.dtype not in dtypes or not t.is_contiguous():
+        _need(t, name, dtypes[0] if len(dtypes) == 1 else None)
+        raise TypeError(f"{name}: dtype {t.dtype}, the library expects one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
+    r, c = t.shape
+    return t.data_ptr(), r, c
+
+
+def _cast(q, name: str, rows: int, cols: int, state, history_len: int) -> tuple:
+    """pointers of an output cast's codes and state"""
     if q is None:
-        return
-    _matrix(q, name, rows, cols, _t().uint8)
-    _vector(state, "q_state", history_len + 2)
+        return None, None
+    return _mat(q, name, rows, cols, _torch.uint8), _vec(state, "q_state", history_len + 2)
 
 
-def _gemm_operands(A, a_scale, B, b_scale, a_name: str, b_name: str):
-    T = _t()
-    for t, name in ((A, a_name), (B, b_name)):
-        _need(t, name, T.uint8)
-        if t.dim() != 2:
-            raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
-    _vector(a_scale, "a_scale", 1)
-    _vector(b_scale, "b_scale", 1)
+def _ws(t) -> tuple:
+    if t is None:
+        return None, 0
+    _need(t, "workspace", _torch.uint8)
+    return t.data_ptr(), t.numel()
 
 
 def fp8_layernorm_fwd(x, gamma, beta, eps: float, y, mu=None, rstd=None, residual=None, sum_out=None,
                       stream=None) -> None:
     """y = LayerNorm(x) gamma + beta; with a residual, of sum_out = x + residual."""
-    M, K = x.shape
-    code = _dtype_code(x)
-    _need(x, "x")
-    _matrix(y, "y", M, K, x.dtype)
-    _vector(gamma, "gamma", K)
-    if beta is not None:
-        _vector(beta, "beta", K)
+    T = _t()
+    px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
+    dt = x.dtype
     if (residual is None) != (sum_out is None):
         raise ValueError("residual and sum_out come together")
-    if residual is not None:
-        _matrix(residual, "residual", M, K, x.dtype)
-        _matrix(sum_out, "sum_out", M, K, x.dtype)
-    for t, name in ((mu, "mu"), (rstd, "rstd")):
-        if t is not None:
-            _vector(t, name, M)
-    _check(lib().fp8_layernorm_fwd(_ptr(x), _ptr(residual), code, _ptr(gamma), _ptr(beta), eps, M, K, _ptr(sum_out),
-                                   _ptr(y), _ptr(mu), _ptr(rstd), _stream(stream)))
+    _check(lib().fp8_layernorm_fwd(
+        px, None if residual is None else _mat(residual, "residual", M, K, dt), BF16 if dt is T.bfloat16 else F32,
+        _vec(gamma, "gamma", K), None if beta is None else _vec(beta, "beta", K), eps, M, K,
+        None if sum_out is None else _mat(sum_out, "sum_out", M, K, dt), _mat(y, "y", M, K, dt),
+        None if mu is None else _vec(mu, "mu", M), None if rstd is None else _vec(rstd, "rstd", M), _stream(stream)))
 
 
 def fp8_layernorm_bwd_workspace_bytes(M: int, K: int) -> int:
-    return int(lib().fp8_layernorm_bwd_workspace_bytes(M, K))
+    return lib().fp8_layernorm_bwd_workspace_bytes(M, K)
 
 
 def fp8_layernorm_bwd(dy, x, gamma, mu, rstd, dx, dgamma, dbeta, workspace, dres=None, stream=None) -> None:
     """dx (+ dres), dgamma and dbeta of a LayerNorm from its input x and saved mu, rstd."""
-    M, K = x.shape
-    code = _dtype_code(x)
-    _need(x, "x")
-    _matrix(dy, "dy", M, K, x.dtype)
-    _matrix(dx, "dx", M, K, x.dtype)
-    if dres is not None:
-        _matrix(dres, "dres", M, K, x.dtype)
-    for t, name, n in ((gamma, "gamma", K), (mu, "mu", M), (rstd, "rstd", M), (dgamma, "dgamma", K),
-                       (dbeta, "dbeta", K)):
-        _vector(t, name, n)
-    _need(workspace, "workspace", _t().uint8)
-    _check(lib().fp8_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(dres), code, _ptr(gamma), _ptr(mu), _ptr(rstd), M, K,
-                                   _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace),
-                                   _stream(stream)))
+    T = _t()
+    px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
+    dt = x.dtype
+    _need(workspace, "workspace", T.uint8)
+    _check(lib().fp8_layernorm_bwd(
+        _mat(dy, "dy", M, K, dt), px, None if dres is None else _mat(dres, "dres", M, K, dt),
+        BF16 if dt is T.bfloat16 else F32, _vec(gamma, "gamma", K), _vec(mu, "mu", M), _vec(rstd, "rstd", M), M, K,
+        _mat(dx, "dx", M, K, dt), _vec(dgamma, "dgamma", K), _vec(dbeta, "dbeta", K), *_ws(workspace),
+        _stream(stream)))
 
 
 def fp8_gemm_act_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(lib().fp8_gemm_act_workspace_bytes(M, N, K))
+    return lib().fp8_gemm_act_workspace_bytes(M, N, K)
 
 
 def fp8_gemm_act(A, a_format: int, a_scale, B, b_format: int, b_scale, act: int, D=None, bias=None, residual=None,
@@ -464,49 +462,40 @@ def fp8_gemm_act(A, a_format: int, a_scale, B, b_format: int, b_scale, act: int,
                  stream=None) -> None:
     """y = act(z) + residual, z = A B^T sA sB + bias, into D (bf16 / fp32) and / or FP8 codes q_out; z into z_out."""
     T = _t()
-    _gemm_operands(A, a_scale, B, b_scale, "A", "B")
-    M, K = A.shape
-    N = B.shape[0]
-    _matrix(B, "B", N, K, T.uint8)
-    if D is not None:
-        _matrix(D, "D", M, N, D.dtype)
-    if residual is not None:
-        _matrix(residual, "residual", M, N, residual.dtype)
-    if z_out is not None:
-        _matrix(z_out, "z_out", M, N, T.bfloat16)
-    if bias is not None:
-        _vector(bias, "bias", N)
-    _cast_args(q_out, "q_out", M, N, q_state, history_len)
-    _opt(workspace, "workspace", T.uint8)
-    _check(lib().fp8_gemm_act(_ptr(A), a_format, _ptr(a_scale), _ptr(B), b_format, _ptr(b_scale), M, N, K, act,
-                              _ptr(bias), _ptr(residual), BF16 if residual is None else _dtype_code(residual),
-                              _ptr(z_out), _ptr(D), BF16 if D is None else _dtype_code(D), _ptr(q_out), q_format,
-                              _ptr(q_state), history_len, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    u8 = (T.uint8,)
+    pa, M, K = _sized(A, "A", u8)
+    pb, N, kb = _sized(B, "B", u8)
+    if kb != K:
+        raise ValueError(f"B: shape {tuple(B.shape)}, expected {(N, K)}")
+    pq, ps = _cast(q_out, "q_out", M, N, q_state, history_len)
+    _check(lib().fp8_gemm_act(
+        pa, a_format, _vec(a_scale, "a_scale", 1), pb, b_format, _vec(b_scale, "b_scale", 1), M, N, K, act,
+        None if bias is None else _vec(bias, "bias", N),
+        None if residual is None else _mat(residual, "residual", M, N, residual.dtype),
+        BF16 if residual is None else _dtype_code(residual),
+        None if z_out is None else _mat(z_out, "z_out", M, N, T.bfloat16),
+        None if D is None else _mat(D, "D", M, N, D.dtype), BF16 if D is None else _dtype_code(D), pq, q_format, ps,
+        history_len, *_ws(workspace), _stream(stream)))
 
 
 def fp8_act_bwd_workspace_bytes(M: int, N: int) -> int:
-    return int(lib().fp8_act_bwd_workspace_bytes(M, N))
+    return lib().fp8_act_bwd_workspace_bytes(M, N)
 
 
 def fp8_act_bwd(dy, z, act: int, dbias=None, dz=None, q_out=None, q_format: int = E5M2, q_state=None,
                 history_len: int = 0, workspace=None, stream=None) -> None:
     """dz = dy act'(z): FP8 codes q_out, bf16 dz, and dbias = the column sums of dz."""
     T = _t()
-    M, N = z.shape
-    _need(z, "z", T.bfloat16)
-    _matrix(dy, "dy", M, N, T.bfloat16)
-    if dbias is not None:
-        _vector(dbias, "dbias", N)
-    if dz is not None:
-        _matrix(dz, "dz", M, N, T.bfloat16)
-    _cast_args(q_out, "q_out", M, N, q_state, history_len)
-    _opt(workspace, "workspace", T.uint8)
-    _check(lib().fp8_act_bwd(_ptr(dy), _ptr(z), M, N, act, _ptr(dbias), _ptr(dz), _ptr(q_out), q_format,
-                             _ptr(q_state), history_len, _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    pz, M, N = _sized(z, "z", (T.bfloat16,))
+    pq, ps = _cast(q_out, "q_out", M, N, q_state, history_len)
+    _check(lib().fp8_act_bwd(
+        _mat(dy, "dy", M, N, T.bfloat16), pz, M, N, act, None if dbias is None else _vec(dbias, "dbias", N),
+        None if dz is None else _mat(dz, "dz", M, N, T.bfloat16), pq, q_format, ps, history_len, *_ws(workspace),
+        _stream(stream)))
 
 
 def fp8_glu_fwd_workspace_bytes(M: int, F: int, K: int) -> int:
-    return int(lib().fp8_glu_fwd_workspace_bytes(M, F, K))
+    return lib().fp8_glu_fwd_workspace_bytes(M, F, K)
 
 
 def fp8_glu_fwd(A, a_format: int, a_scale, W, w_format: int, w_scale, act: int, h_out=None, gu_out=None, q_out=None,
@@ -514,19 +503,18 @@ def fp8_glu_fwd(A, a_format: int, a_scale, W, w_format: int, w_scale, act: int, 
     """h = act(g) u with [g | u] = A W^T sA sW, W = [W_gate; W_up]: into h_out (bf16) and / or FP8 codes q_out;
     [g | u] into gu_out."""
     T = _t()
-    _gemm_operands(A, a_scale, W, w_scale, "A", "W")
-    M, K = A.shape
-    F = W.shape[0] // 2
-    _matrix(W, "W", 2 * F, K, T.uint8)
-    if h_out is not None:
-        _matrix(h_out, "h_out", M, F, T.bfloat16)
-    if gu_out is not None:
-        _matrix(gu_out, "gu_out", M, 2 * F, T.bfloat16)
-    _cast_args(q_out, "q_out", M, F, q_state, history_len)
-    _opt(workspace, "workspace", T.uint8)
-    _check(lib().fp8_glu_fwd(_ptr(A), a_format, _ptr(a_scale), _ptr(W), w_format, _ptr(w_scale), M, F, K, act,
-                             _ptr(gu_out), _ptr(h_out), _ptr(q_out), q_format, _ptr(q_state), history_len,
-                             _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    u8 = (T.uint8,)
+    pa, M, K = _sized(A, "A", u8)
+    pw, F2, kw = _sized(W, "W", u8)
+    F = F2 // 2
+    if kw != K or F2 != 2 * F:
+        raise ValueError(f"W: shape {tuple(W.shape)}, expected {(2 * F, K)}")
+    pq, ps = _cast(q_out, "q_out", M, F, q_state, history_len)
+    _check(lib().fp8_glu_fwd(
+        pa, a_format, _vec(a_scale, "a_scale", 1), pw, w_format, _vec(w_scale, "w_scale", 1), M, F, K, act,
+        None if gu_out is None else _mat(gu_out, "gu_out", M, F2, T.bfloat16),
+        None if h_out is None else _mat(h_out, "h_out", M, F, T.bfloat16), pq, q_format, ps, history_len,
+        *_ws(workspace), _stream(stream)))
 
 
 def fp8_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scale, gu, act: int, q_dgu, q_format: int,
@@ -534,16 +522,17 @@ def fp8_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scale, gu, ac
     """codes of [dg | du] from the block's output gradient dY [M][K], the down projection Wd [K][F] and the
     forward's [g | u]."""
     T = _t()
-    _gemm_operands(dY, dy_scale, Wd, w_scale, "dY", "Wd")
-    M, K = dY.shape
-    F = Wd.shape[1]
-    _matrix(Wd, "Wd", K, F, T.uint8)
-    _matrix(gu, "gu", M, 2 * F, T.bfloat16)
+    u8 = (T.uint8,)
+    py, M, K = _sized(dY, "dY", u8)
+    pw, kw, F = _sized(Wd, "Wd", u8)
+    if kw != K:
+        raise ValueError(f"Wd: shape {tuple(Wd.shape)}, expected {(K, F)}")
     if q_dgu is None:
         raise ValueError("q_dgu is required")
-    _cast_args(q_dgu, "q_dgu", M, 2 * F, q_state, history_len)
-    _check(lib().fp8_glu_bwd(_ptr(dY), dy_format, _ptr(dy_scale), _ptr(Wd), w_format, _ptr(w_scale), M, F, K,
-                             _ptr(gu), act, _ptr(q_dgu), q_format, _ptr(q_state), history_len, _stream(stream)))
+    pg = _mat(gu, "gu", M, 2 * F, T.bfloat16)
+    pq, ps = _cast(q_dgu, "q_dgu", M, 2 * F, q_state, history_len)
+    _check(lib().fp8_glu_bwd(py, dy_format, _vec(dy_scale, "dy_scale", 1), pw, w_format, _vec(w_scale, "w_scale", 1),
+                             M, F, K, pg, act, pq, q_format, ps, history_len, _stream(stream)))
 
 
 def fp8_selftest_wait_timeout(limit_us: int, waited_out, stream=None) -> None:

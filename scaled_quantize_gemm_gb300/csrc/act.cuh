@@ -72,6 +72,12 @@ __device__ __forceinline__ float min_nan(float a, float b)
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float2 max2_nan(float2 a, float b) { return make_float2(max_nan(a.x, b), max_nan(a.y, b)); }
 __device__ __forceinline__ float2 min2_nan(float2 a, float b) { return make_float2(min_nan(a.x, b), min_nan(a.y, b)); }
 

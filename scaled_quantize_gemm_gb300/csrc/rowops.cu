@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "act.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -208,18 +210,34 @@ struct RawVec<2> { using type = uint16_t; };
 template <typename T, int VEC>
 struct Pack {
     using Raw = typename RawVec<sizeof(T) * VEC>::type;
+    static constexpr bool PAIRS = sizeof(T) == 2 && VEC % 2 == 0;    // bf16 pairs in 32-bit words
     static __device__ __forceinline__ void to_floats(const Raw& raw, float (&v)[VEC])
     {
-        const T* e = reinterpret_cast<const T*>(&raw);
+        if constexpr (PAIRS) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[j] = to_f(e[j]);
+            for (int j = 0; j < VEC; j += 2) {
+                v[j] = __uint_as_float(w[j / 2] << 16);
+                v[j + 1] = __uint_as_float(w[j / 2] & 0xFFFF0000u);
+            }
+        } else {
+            const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[j] = to_f(e[j]);
+        }
     }
     static __device__ __forceinline__ Raw from_floats(const float (&v)[VEC])
     {
         Raw raw;
-        T* e = reinterpret_cast<T*>(&raw);
+        if constexpr (PAIRS) {
+            __nv_bfloat162* w = reinterpret_cast<__nv_bfloat162*>(&raw);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) e[j] = from_f<T>(v[j]);
+            for (int j = 0; j < VEC; j += 2) w[j / 2] = __floats2bfloat162_rn(v[j], v[j + 1]);
+        } else {
+            T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) e[j] = from_f<T>(v[j]);
+        }
         return raw;
     }
 };
@@ -241,91 +259,125 @@ __device__ __forceinline__ void load_param(const float* __restrict__ p, int c, f
         for (int j = 0; j < VEC; ++j) v[j] = __ldg(p + c + j);
     }
 }
-// Sum over the warps of a CTA, the same bits in every thread; `red` holds one
-// float a warp and is not written again before another barrier.
-__device__ __forceinline__ float block_total(const float* red, int warps)
+// Sum of `red`, one float a warp, zeros up to the power of two `span` >= warps:
+// every lane reads one entry and log2(span) shuffles leave the same total in
+// all of them.  `red` is not written again before another barrier.
+__device__ __forceinline__ int pow2_span(int warps) { return warps <= 1 ? 1 : 1 << (32 - __clz(warps - 1)); }
+__device__ __forceinline__ float block_total(const float* red, int span)
 {
-    const int lane = threadIdx.x & 31;
-    return warp_sum(lane < warps ? red[lane] : 0.0f);
+    float v = red[threadIdx.x & (span - 1)];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        if (o < span) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+// Two sums at once: lanes 0-15 end with the first's total, lanes 16-31 with the
+// second's (one exchange, then four shuffles instead of ten).
+__device__ __forceinline__ float warp_sum2(float a, float b)
+{
+    const bool hi = threadIdx.x & 16;
+    float v = hi ? b : a;
+    v += __shfl_xor_sync(0xFFFFFFFFu, hi ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+// Two sums of one float a warp each (red[0], red[1]) over up to 32 warps, in
+// every lane: the halves of a warp take one each.
+__device__ __forceinline__ float2 block_total2(const float (*red)[32], int span)
+{
+    const float* r = red[(threadIdx.x >> 4) & 1];
+    float v = r[threadIdx.x & 15 & (span - 1)];
+    if (span == 32) v += r[16 + (threadIdx.x & 15)];
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1)
+        if (o < span) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
 }
 
 // ------------------------------------------------------------------ LayerNorm forward
 // A CTA takes one row at a time and holds it in registers (16 columns a
-// thread) from the sum to the output, so x and the residual are read once and
-// y (and the sum) written once; no row is prefetched, the loads of a CTA's
-// row overlap the reductions of the others on its SM.
+// thread, as stored) from the sum to the output, so x and the residual are
+// read once and y (and the sum) written once; no row is prefetched, the loads
+// of a CTA's row overlap the reductions of the others on its SM: MINB CTAs of
+// at most MAXT threads, 1536 threads (six CTAs at 4096 columns: 82 us for 16384
+// rows in bf16 with residual, 96 % of the copy rate; four 93, eight 105).
 constexpr int kLnCols = 16;         // columns a thread holds
-template <typename T, int VEC>
-__global__ void __launch_bounds__(1024) k_ln_fwd(const T* __restrict__ x, const T* __restrict__ res,
-                                                 const float* __restrict__ gamma, const float* __restrict__ beta,
-                                                 float eps, int64_t R, int K, T* __restrict__ sum, T* __restrict__ y,
-                                                 float* __restrict__ mu, float* __restrict__ rstd)
+template <typename T, int VEC, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
+    k_ln_fwd(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ gamma,
+             const float* __restrict__ beta, float eps, int64_t R, int K, T* __restrict__ sum, T* __restrict__ y,
+             float* __restrict__ mu, float* __restrict__ rstd)
 {
-    pdl_enter();
     constexpr int NV = kLnCols / VEC;
     using P = Pack<T, VEC>;
     using Raw = typename P::Raw;
     __shared__ float red[2][32];
     const int t = threadIdx.x, nt = blockDim.x, warp = t >> 5, warps = nt >> 5;
+    const int span = pow2_span(warps);
+    if (t < 64) red[t >> 5][t & 31] = 0.0f;
+    if (nt < 64 && t < 32) red[1][t] = 0.0f;
+    __syncthreads();
+    pdl_enter();
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         const int64_t base = r * K;
-        float v[NV][VEC];
         Raw raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + t) * VEC;
-            if (c < K) raw[i] = *reinterpret_cast<const Raw*>(x + base + c);
-            else raw[i] = Raw{};
+            raw[i] = c < K ? *reinterpret_cast<const Raw*>(x + base + c) : Raw{};
         }
         if (res) {
             Raw rr[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * nt + t) * VEC;
-                if (c < K) rr[i] = *reinterpret_cast<const Raw*>(res + base + c);
-                else rr[i] = Raw{};
+                rr[i] = c < K ? *reinterpret_cast<const Raw*>(res + base + c) : Raw{};
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * nt + t) * VEC;
-                float w[VEC];
-                P::to_floats(raw[i], v[i]);
+                float v[VEC], w[VEC];
+                P::to_floats(raw[i], v);
                 P::to_floats(rr[i], w);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) v[i][j] += w[j];
-                raw[i] = P::from_floats(v[i]);          // the sum as stored
+                for (int j = 0; j < VEC; ++j) v[j] += w[j];
+                raw[i] = P::from_floats(v);             // the sum as stored
                 if (c < K) *reinterpret_cast<Raw*>(sum + base + c) = raw[i];
             }
         }
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            P::to_floats(raw[i], v[i]);
+            float v[VEC];
+            P::to_floats(raw[i], v);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) s += v[i][j];
+            for (int j = 0; j < VEC; ++j) s += v[j];
         }
         s = warp_sum(s);
         if (warps > 1) {
             if ((t & 31) == 0) red[0][warp] = s;
             __syncthreads();
-            s = block_total(red[0], warps);
+            s = block_total(red[0], span);
         }
         const float mean = s / (float)K;
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = (i * nt + t) * VEC < K;
+            if ((i * nt + t) * VEC >= K) continue;
+            float v[VEC];
+            P::to_floats(raw[i], v);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                v[i][j] -= mean;
-                if (in) s = fmaf(v[i][j], v[i][j], s);
+                v[j] -= mean;
+                s = fmaf(v[j], v[j], s);
             }
         }
         s = warp_sum(s);
         if (warps > 1) {
             if ((t & 31) == 0) red[1][warp] = s;
             __syncthreads();
-            s = block_total(red[1], warps);
+            s = block_total(red[1], span);
         }
         const float rs = 1.0f / sqrtf(s / (float)K + eps);
         if (t == 0) {
@@ -336,25 +388,33 @@ __global__ void __launch_bounds__(1024) k_ln_fwd(const T* __restrict__ x, const 
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + t) * VEC;
             if (c >= K) continue;
-            float g[VEC], b[VEC] = {};
+            float v[VEC], g[VEC], b[VEC] = {};
+            P::to_floats(raw[i], v);
             load_param<VEC>(gamma, c, g);
             if (beta) load_param<VEC>(beta, c, b);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) g[j] = fmaf(v[i][j] * rs, g[j], b[j]);
-            *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(g);
+            for (int j = 0; j < VEC; ++j) v[j] = fmaf((v[j] - mean) * rs, g[j], b[j]);
+            *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(v);
         }
     }
 }
 
 // ------------------------------------------------------------------ LayerNorm backward
-// A CTA takes rows r = blockIdx.x, + gridDim.x, ... and each thread the same
-// C columns of every row, so dgamma and dbeta accumulate in its registers and
-// go to the workspace once per CTA.  x, dy and dres of the next STAGES - 1 rows
-// are in flight (cp.async) while a row is worked on: a thread copies exactly
-// the elements that it will read, so the ring needs no barrier and no wait on
-// another thread, and a row costs one barrier, for its two sums.  C = 8 keeps
-// the row's normalised values and dy gamma in registers across that barrier;
-// C = 16 (rows over 8192) reads them from the ring again.
+// A group of threads takes a row at a time and each thread the same C columns
+// of every row, so dgamma and dbeta accumulate in its registers; a CTA holds
+// one group, or several for short rows, whose sums meet in shared memory at the
+// end, and writes one partial row to the workspace.  x, dy and dres of the next
+// STAGES - 1 rows are in flight (cp.async) while a row is worked on: a thread
+// copies exactly the elements that it will read, so the ring needs no barrier
+// and no wait on another thread, and a row costs one barrier of its group, for
+// its two sums.
+// The time goes with the instructions a row costs beside its elements (ncu at
+// 16384 x 4096 with 8 columns a thread: 40 instructions an element, issue slots
+// 59 % busy, DRAM 53 %), so a thread takes 16 columns: 119 -> 93 us.  KEEP holds
+// the row's normalised values and dy gamma in registers across the barrier
+// (rows of up to 8192; longer ones read the ring again).  Rows that move one
+// element at a time (odd bf16 or fp32 lengths) take 8 columns (4096 x 1001
+// bf16: 45 us against 75 with 16).
 __device__ __forceinline__ void cp_async4(void* s, const void* g)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s)), "l"(g) : "memory");
@@ -364,41 +424,67 @@ __device__ __forceinline__ void cp_async_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <typename Raw>
-__device__ __forceinline__ void stage_vec(Raw* s, const void* g)
+__device__ __forceinline__ void bar_group(int id, int threads)
 {
-    if constexpr (sizeof(Raw) == 16) cp_async16(s, g);
-    else if constexpr (sizeof(Raw) == 4) cp_async4(s, g);
-    else *s = *static_cast<const Raw*>(g);       // 2 bytes: below cp.async's smallest size
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+constexpr int kLnGroups = 8;        // groups of a CTA, at most
 
-template <typename T, int VEC, int C, int STAGES>
-__global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const T* __restrict__ x,
-                                                 const T* __restrict__ dres, const float* __restrict__ gamma,
-                                                 const float* __restrict__ mu, const float* __restrict__ rstd,
-                                                 int64_t R, int K, T* __restrict__ dx, float* __restrict__ part)
+template <typename T, int VEC, int C, int STAGES, int MAXT, int MINB, bool KEEP, bool GROUPED>
+__global__ void __launch_bounds__(MAXT, MINB)
+    k_ln_bwd(const T* __restrict__ dy, const T* __restrict__ x, const T* __restrict__ dres,
+             const float* __restrict__ gamma, const float* __restrict__ mu, const float* __restrict__ rstd, int64_t R,
+             int K, int group_threads, T* __restrict__ dx, float* __restrict__ part)
 {
-    pdl_enter();
     constexpr int NV = C / VEC;
-    constexpr bool KEEP = C == 8;
     using P = Pack<T, VEC>;
     using Raw = typename P::Raw;
     extern __shared__ __align__(16) uint8_t ln_ring[];
-    __shared__ float red[2][2][32];
-    const int t = threadIdx.x, nt = blockDim.x, warp = t >> 5, warps = nt >> 5;
+    constexpr int RG = GROUPED ? kLnGroups : 1;
+    __shared__ float red[RG][2][2][32];
+    const int nt = GROUPED ? group_threads : blockDim.x, g = GROUPED ? threadIdx.x / nt : 0, t = threadIdx.x - g * nt;
+    const int groups = GROUPED ? blockDim.x / nt : 1, warp = t >> 5, warps = nt >> 5;
+    const int span = pow2_span(warps);
+    for (int i = threadIdx.x; i < RG * 128; i += blockDim.x) (&red[0][0][0][0])[i] = 0.0f;
+    __syncthreads();
+    pdl_enter();
     const int narr = dres ? 3 : 2;
     // [stage][array][vector i][thread]
-    Raw* ring = reinterpret_cast<Raw*>(ln_ring);
-    auto slot = [&](int st, int arr, int i) -> Raw* { return ring + ((st * narr + arr) * NV + i) * nt + t; };
+    Raw* ring = reinterpret_cast<Raw*>(ln_ring) + threadIdx.x;
+    auto slot = [&](int st, int arr, int i) -> Raw* { return ring + ((st * narr + arr) * NV + i) * blockDim.x; };
     auto stage = [&](int st, int64_t r) {
         if (r < R) {
+            if constexpr (sizeof(Raw) >= 4) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + t) * VEC;
-                if (c < K) {
-                    stage_vec(slot(st, 0, i), x + r * K + c);
-                    stage_vec(slot(st, 1, i), dy + r * K + c);
-                    if (dres) stage_vec(slot(st, 2, i), dres + r * K + c);
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * nt + t) * VEC;
+                    if (c < K) {
+                        auto copy = [&](int arr, const T* src) {
+                            if constexpr (sizeof(Raw) == 16) cp_async16(slot(st, arr, i), src + r * K + c);
+                            else cp_async4(slot(st, arr, i), src + r * K + c);
+                        };
+                        copy(0, x);
+                        copy(1, dy);
+                        if (dres) copy(2, dres);
+                    }
+                }
+            } else {
+                // 2 bytes: below cp.async's smallest size, through registers
+                Raw v[3][NV];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * nt + t) * VEC;
+                    if (c < K) {
+                        v[0][i] = *reinterpret_cast<const Raw*>(x + r * K + c);
+                        v[1][i] = *reinterpret_cast<const Raw*>(dy + r * K + c);
+                        if (dres) v[2][i] = *reinterpret_cast<const Raw*>(dres + r * K + c);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    *slot(st, 0, i) = v[0][i];
+                    *slot(st, 1, i) = v[1][i];
+                    if (dres) *slot(st, 2, i) = v[2][i];
                 }
             }
         }
@@ -422,29 +508,31 @@ __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const
         for (int j = 0; j < C / 2; ++j)
             v[j] = make_float2(f[(2 * j) / VEC][(2 * j) % VEC], f[(2 * j + 1) / VEC][(2 * j + 1) % VEC]);
     };
+    constexpr bool GREG = KEEP && MAXT <= 512;      // gamma in registers as well
     float2 ag[C / 2] = {}, ab[C / 2] = {}, gam[C / 2];
-    if constexpr (KEEP) params(gam);
+    if constexpr (GREG) params(gam);
+    const int64_t first = (int64_t)blockIdx.x * groups + g, step = (int64_t)gridDim.x * groups;
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) stage(s, blockIdx.x + (int64_t)s * gridDim.x);
+    for (int s = 0; s < STAGES - 1; ++s) stage(s, first + s * step);
     int st = 0, par = 0;
     const float inv = 1.0f / (float)K;
     float mean = 0.0f, rs = 0.0f;
-    if (blockIdx.x < R) {
-        mean = __ldg(mu + blockIdx.x);
-        rs = __ldg(rstd + blockIdx.x);
+    if (first < R) {
+        mean = __ldg(mu + first);
+        rs = __ldg(rstd + first);
     }
-    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+    for (int64_t r = first; r < R; r += step) {
         int ahead = st + STAGES - 1;
         if (ahead >= STAGES) ahead -= STAGES;
-        stage(ahead, r + (int64_t)(STAGES - 1) * gridDim.x);
-        const int64_t rn = r + gridDim.x < R ? r + gridDim.x : r;
+        stage(ahead, r + (STAGES - 1) * step);
+        const int64_t rn = r + step < R ? r + step : r;
         const float mean_n = __ldg(mu + rn), rs_n = __ldg(rstd + rn);
         cp_async_wait<STAGES - 1>();
         float2 xh[C / 2], w[C / 2];
         auto load_row = [&]() {
             fetch(st, 0, xh);
             fetch(st, 1, w);
-            if constexpr (!KEEP) params(gam);
+            if constexpr (!GREG) params(gam);
 #pragma unroll
             for (int j = 0; j < C / 2; ++j) xh[j] = __fmul2_rn(__fadd2_rn(xh[j], f2(-mean)), f2(rs));
         };
@@ -458,17 +546,17 @@ __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const
             t1 = __fadd2_rn(t1, w[j]);
             t2 = __ffma2_rn(w[j], xh[j], t2);
         }
-        float s1 = warp_sum(t1.x + t1.y), s2 = warp_sum(t2.x + t2.y);
+        const float s = warp_sum2(t1.x + t1.y, t2.x + t2.y);
+        float2 c12;
         if (warps > 1) {
-            if ((t & 31) == 0) {
-                red[par][0][warp] = s1;
-                red[par][1][warp] = s2;
-            }
-            __syncthreads();
-            s1 = block_total(red[par][0], warps);
-            s2 = block_total(red[par][1], warps);
+            if ((t & 15) == 0) red[g][par][(t >> 4) & 1][warp] = s;
+            if constexpr (GROUPED) bar_group(1 + g, nt);
+            else __syncthreads();
+            c12 = block_total2(red[g][par], span);
+        } else {
+            c12 = make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
         }
-        const float c1 = s1 * inv, c2 = s2 * inv;
+        const float c1 = c12.x * inv, c2 = c12.y * inv;
         if constexpr (!KEEP) {
             load_row();
 #pragma unroll
@@ -498,6 +586,26 @@ __global__ void __launch_bounds__(1024) k_ln_bwd(const T* __restrict__ dy, const
         par ^= 1;
         if (++st == STAGES) st = 0;
     }
+    if constexpr (GROUPED) {
+        // the groups' sums, added in group order by the first (the ring is idle)
+        float2* sums = reinterpret_cast<float2*>(ln_ring);
+        cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < C / 2; ++j) {
+            sums[(2 * j) * blockDim.x + threadIdx.x] = ag[j];
+            sums[(2 * j + 1) * blockDim.x + threadIdx.x] = ab[j];
+        }
+        __syncthreads();
+        if (g > 0) return;
+        for (int o = 1; o < groups; ++o) {
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) {
+                ag[j] = __fadd2_rn(ag[j], sums[(2 * j) * blockDim.x + o * nt + t]);
+                ab[j] = __fadd2_rn(ab[j], sums[(2 * j + 1) * blockDim.x + o * nt + t]);
+            }
+        }
+    }
     float* pg = part + (int64_t)blockIdx.x * 2 * K;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -520,7 +628,7 @@ constexpr int kActCols = 256;
 template <int ACT>
 __device__ __forceinline__ void act_bwd_rows(const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ z,
                                              int64_t r0, int64_t r1, int64_t N, int64_t c, __nv_bfloat16* __restrict__ dz,
-                                             uint8_t* __restrict__ q, int fmt, float m, float2 (&sum)[4], uint32_t& amax)
+                                             uint8_t* __restrict__ q, int fmt, float m, float2 (&sum)[4], float& amax)
 {
     // the loads run two of the warp's rows ahead of the arithmetic
     constexpr int AHEAD = 2;
@@ -564,7 +672,7 @@ __device__ __forceinline__ void act_bwd_rows(const __nv_bfloat16* __restrict__ d
             uint32_t w[2];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                amax = max(amax, max(__float_as_uint(v[j].x) & 0x7FFFFFFFu, __float_as_uint(v[j].y) & 0x7FFFFFFFu));
+                amax = max3_nan(amax, fabsf(v[j].x), fabsf(v[j].y));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float2 a = __fmul2_rn(v[2 * j], f2(m)), b = __fmul2_rn(v[2 * j + 1], f2(m));
@@ -576,7 +684,7 @@ __device__ __forceinline__ void act_bwd_rows(const __nv_bfloat16* __restrict__ d
     }
 }
 
-__global__ void __launch_bounds__(256, 4) k_act_bwd(const __nv_bfloat16* __restrict__ dy,
+__global__ void __launch_bounds__(256, 5) k_act_bwd(const __nv_bfloat16* __restrict__ dy,
                                                     const __nv_bfloat16* __restrict__ z, int act, int64_t R, int64_t N,
                                                     int64_t slab, __nv_bfloat16* __restrict__ dz,
                                                     uint8_t* __restrict__ q, int fmt, float* qstate, int H,
@@ -591,15 +699,16 @@ __global__ void __launch_bounds__(256, 4) k_act_bwd(const __nv_bfloat16* __restr
     const int64_t r1 = r0 + slab < R ? r0 + slab : R;
     const float m = q ? qstate[H] : 1.0f;
     float2 sum[4] = {};
-    uint32_t amax = 0;
+    float amax_f = 0.0f;
     if (c < N)
         act_dispatch(act, [&](auto tag) {
-            act_bwd_rows<decltype(tag)::act>(dy, z, r0 + warp, r1, N, c, dz, q, fmt, m, sum, amax);
+            act_bwd_rows<decltype(tag)::act>(dy, z, r0 + warp, r1, N, c, dz, q, fmt, m, sum, amax_f);
         });
     if (part) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) cols[warp][j][lane] = sum[j];
     }
+    uint32_t amax = __float_as_uint(amax_f);     // not negative: ordered as integers, a NaN above all
     if (q) {
         amax = __reduce_max_sync(0xFFFFFFFFu, amax);
         if (lane == 0) red[warp] = amax;
@@ -621,27 +730,51 @@ __global__ void __launch_bounds__(256, 4) k_act_bwd(const __nv_bfloat16* __restr
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t parts_for(int64_t rows) { return rows < kMaxParts ? rows : kMaxParts; }
 
-// CTAs of a kernel that are resident at once
+// CTAs of a kernel that are resident at once.  The answers are kept: the query
+// took over a microsecond of every call.
 int resident(const void* kern, int threads, int smem, int sms)
 {
+    struct Entry {
+        const void* kern;
+        int threads, smem, dev, per_sm;
+    };
+    static std::mutex mu;
+    static Entry known[256];
+    static int n = 0;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n; ++i)
+        if (known[i].kern == kern && known[i].threads == threads && known[i].smem == smem && known[i].dev == dev)
+            return known[i].per_sm * sms;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1) {
         cudaGetLastError();
-        per_sm = 1;
+        return sms;
     }
+    if (n < 256) known[n++] = {kern, threads, smem, dev, per_sm};
     return per_sm * sms;
+}
+
+template <typename T, int VEC, int MAXT, int MINB>
+cudaError_t ln_fwd_cta(const LnArgs& a, cudaStream_t st, int sms, int threads)
+{
+    auto kern = k_ln_fwd<T, VEC, MAXT, MINB>;
+    const int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, 0, sms);
+    launch_k(kern, (unsigned)(a.M < cap ? a.M : cap), threads, 0, st, static_cast<const T*>(a.x),
+             static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, (int)a.K, static_cast<T*>(a.sum),
+             static_cast<T*>(a.y), a.mu, a.rstd);
+    return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t ln_fwd_rows(const LnArgs& a, cudaStream_t st, int sms)
 {
     const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
-    auto kern = k_ln_fwd<T, VEC>;
-    const int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, 0, sms);
-    launch_k(kern, (unsigned)(a.M < cap ? a.M : cap), threads, 0, st, static_cast<const T*>(a.x),
-             static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, (int)a.K, static_cast<T*>(a.sum),
-             static_cast<T*>(a.y), a.mu, a.rstd);
-    return cudaGetLastError();
+    if (threads <= 256) return ln_fwd_cta<T, VEC, 256, 6>(a, st, sms, threads);
+    if (threads <= 512) return ln_fwd_cta<T, VEC, 512, 3>(a, st, sms, threads);
+    if (threads <= 768) return ln_fwd_cta<T, VEC, 768, 2>(a, st, sms, threads);
+    return ln_fwd_cta<T, VEC, 1024, 1>(a, st, sms, threads);
 }
 
 template <typename T>
@@ -660,40 +793,55 @@ cudaError_t ln_fwd(const LnArgs& a, cudaStream_t st, int sms)
     return cudaGetLastError();
 }
 
-constexpr int kSmemCta = 227 * 1024;
+constexpr int kLnRoom = 227 * 1024 - 6 * 1024;      // shared memory of a LayerNorm ring (beside the reduction's)
 
-template <typename T, int VEC, int C, int STAGES>
-cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int threads, int smem, int* parts)
+template <typename T, int VEC, int C, int STAGES, int MAXT, int MINB, bool KEEP, bool GROUPED>
+cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int group, int groups, int smem, int* parts)
 {
-    auto kern = k_ln_bwd<T, VEC, C, STAGES>;
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), kSmemCta - 2048);
+    auto kern = k_ln_bwd<T, VEC, C, STAGES, MAXT, MINB, KEEP, GROUPED>;
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), kLnRoom);
     if (e != cudaSuccess) return e;
+    const int threads = group * groups;
     int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, smem, sms);
-    cap = cap < parts_for(a.M) ? cap : parts_for(a.M);
+    const int64_t most = parts_for(cdiv(a.M, groups));
+    cap = cap < most ? cap : most;
     *parts = (int)cap;
     launch_k(kern, (unsigned)cap, threads, smem, st, static_cast<const T*>(a.dy), static_cast<const T*>(a.x),
-             static_cast<const T*>(a.dres), a.gamma, (const float*)a.mu, (const float*)a.rstd, a.M, (int)a.K,
+             static_cast<const T*>(a.dres), a.gamma, (const float*)a.mu, (const float*)a.rstd, a.M, (int)a.K, group,
              static_cast<T*>(a.dx), static_cast<float*>(a.workspace));
     return cudaGetLastError();
 }
 
-// three stages of the ring where they fit, else two or one
-template <typename T, int VEC, int C>
+// Three stages of the ring where they fit, else two or one.  Short rows share a
+// CTA of MAXT threads where there are rows for all of its groups on every SM.
+template <typename T, int VEC, int C, int MAXT, int MINB, bool KEEP>
 cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
 {
-    const int threads = 32 * (int)cdiv(a.K, 32 * C);
-    const int stage = threads * C * (int)sizeof(T) * (a.dres ? 3 : 2);
-    const int room = kSmemCta - 2048;
-    if (3 * stage <= room) return ln_bwd_rows<T, VEC, C, 3>(a, st, sms, threads, 3 * stage, parts);
-    if (2 * stage <= room) return ln_bwd_rows<T, VEC, C, 2>(a, st, sms, threads, 2 * stage, parts);
-    return ln_bwd_rows<T, VEC, C, 1>(a, st, sms, threads, stage, parts);
+    const int group = 32 * (int)cdiv(a.K, 32 * C);
+    int groups = MAXT <= 256 ? MAXT / group : 1;
+    groups = groups < kLnGroups ? groups : kLnGroups;
+    while (groups > 1 && a.M < (int64_t)groups * sms) --groups;
+    const int stage = group * groups * C * (int)sizeof(T) * (a.dres ? 3 : 2);
+    if constexpr (MAXT <= 256) {
+        if (groups > 1) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, true>(a, st, sms, group, groups, 3 * stage, parts);
+    }
+    if (3 * stage <= kLnRoom) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, 3 * stage, parts);
+    if (2 * stage <= kLnRoom) return ln_bwd_rows<T, VEC, C, 2, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, 2 * stage, parts);
+    return ln_bwd_rows<T, VEC, C, 1, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, stage, parts);
 }
 
 template <typename T, int VEC>
 cudaError_t ln_bwd_vec(const LnArgs& a, cudaStream_t st, int sms, int* parts)
 {
-    if (a.K <= 1024 * 8) return ln_bwd_cols<T, VEC, 8>(a, st, sms, parts);
-    return ln_bwd_cols<T, VEC, 16>(a, st, sms, parts);
+    if constexpr (VEC == 1) {
+        if (a.K <= 256 * 8) return ln_bwd_cols<T, VEC, 8, 256, 4, true>(a, st, sms, parts);
+        if (a.K <= 1024 * 8) return ln_bwd_cols<T, VEC, 8, 1024, 1, true>(a, st, sms, parts);
+    } else {
+        if (a.K <= 256 * 16) return ln_bwd_cols<T, VEC, 16, 256, 2, true>(a, st, sms, parts);
+        if (a.K <= 512 * 16) return ln_bwd_cols<T, VEC, 16, 512, 1, true>(a, st, sms, parts);
+        if (a.K <= 768 * 16) return ln_bwd_cols<T, VEC, 16, 768, 1, true>(a, st, sms, parts);
+    }
+    return ln_bwd_cols<T, VEC, 16, 1024, 1, false>(a, st, sms, parts);
 }
 
 template <typename T>
