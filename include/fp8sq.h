@@ -428,6 +428,10 @@ FP8SQ_API int fp8_linear_fwd_noalloc(const void* x, const void* w, int64_t M, in
  *     dtype         of x, residual, sum_out, y [M][K]: BF16 or F32
  *     residual, sum_out  both or neither; beta may be NULL (zero)
  *     mu_out, rstd_out   f32 [M] or NULL (the backward pass needs them)
+ *     q_out         u8 [M][K] or NULL: the codes sat_RNE_fp8(y * m) of the
+ *                   fp32 y in q_format under the delayed state q_state (as
+ *                   fp8_layernorm_quantize, for any M and K); y may then be
+ *                   NULL
  *   Any M >= 0 and K >= 1; x, residual, sum_out, y, gamma, beta 16-byte
  *   aligned.
  * fp8_layernorm_bwd: with xh = (x - mu) rstd and w = dy gamma,
@@ -443,7 +447,7 @@ FP8SQ_API int fp8_linear_fwd_noalloc(const void* x, const void* w, int64_t M, in
  */
 FP8SQ_API int fp8_layernorm_fwd(const void* x, const void* residual, int dtype, const float* gamma, const float* beta,
                                 float eps, int64_t M, int64_t K, void* sum_out, void* y, float* mu_out, float* rstd_out,
-                                void* stream);
+                                uint8_t* q_out, int q_format, float* q_state, int q_history_len, void* stream);
 FP8SQ_API size_t fp8_layernorm_bwd_workspace_bytes(int64_t M, int64_t K);
 FP8SQ_API int fp8_layernorm_bwd(const void* dy, const void* x, const void* dres, int dtype, const float* gamma,
                                 const float* mu, const float* rstd, int64_t M, int64_t K, void* dx, float* dgamma,

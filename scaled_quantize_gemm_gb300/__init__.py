@@ -73,7 +73,7 @@ def lib() -> ctypes.CDLL:
                 "fp8_layernorm_quantize": (I, [P, P, P, c.c_float, I64, I64, I, P, I, P, P, P, P, P]),
                 "fp8_layernorm_linear_fwd": (I, [P, P, P, c.c_float, P, I64, I64, I64, P, P, I, P, Z, P, P, P, P,
                                                  I, P]),
-                "fp8_layernorm_fwd": (I, [P, P, I, P, P, c.c_float, I64, I64, P, P, P, P, P]),
+                "fp8_layernorm_fwd": (I, [P, P, I, P, P, c.c_float, I64, I64, P, P, P, P, P, I, P, I, P]),
                 "fp8_layernorm_bwd_workspace_bytes": (Z, [I64, I64]),
                 "fp8_layernorm_bwd": (I, [P, P, P, I, P, P, P, I64, I64, P, P, P, P, Z, P]),
                 "fp8_gemm_act_workspace_bytes": (Z, [I64, I64, I64]),
@@ -421,19 +421,22 @@ def _ws(t) -> tuple:
     return t.data_ptr(), t.numel()
 
 
-def fp8_layernorm_fwd(x, gamma, beta, eps: float, y, mu=None, rstd=None, residual=None, sum_out=None,
-                      stream=None) -> None:
-    """y = LayerNorm(x) gamma + beta; with a residual, of sum_out = x + residual."""
+def fp8_layernorm_fwd(x, gamma, beta, eps: float, y, mu=None, rstd=None, residual=None, sum_out=None, q_out=None,
+                      q_format: int = E4M3, q_state=None, history_len: int = 0, stream=None) -> None:
+    """y = LayerNorm(x) gamma + beta; with a residual, of sum_out = x + residual; with q_out, y's FP8 codes under
+    the delayed state q_state (y may then be None)."""
     T = _t()
     px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
     dt = x.dtype
     if (residual is None) != (sum_out is None):
         raise ValueError("residual and sum_out come together")
+    pq, ps = _cast(q_out, "q_out", M, K, q_state, history_len)
     _check(lib().fp8_layernorm_fwd(
         px, None if residual is None else _mat(residual, "residual", M, K, dt), BF16 if dt is T.bfloat16 else F32,
         _vec(gamma, "gamma", K), None if beta is None else _vec(beta, "beta", K), eps, M, K,
-        None if sum_out is None else _mat(sum_out, "sum_out", M, K, dt), _mat(y, "y", M, K, dt),
-        None if mu is None else _vec(mu, "mu", M), None if rstd is None else _vec(rstd, "rstd", M), _stream(stream)))
+        None if sum_out is None else _mat(sum_out, "sum_out", M, K, dt),
+        None if y is None and pq is not None else _mat(y, "y", M, K, dt), None if mu is None else _vec(mu, "mu", M),
+        None if rstd is None else _vec(rstd, "rstd", M), pq, q_format, ps, history_len, _stream(stream)))
 
 
 def fp8_layernorm_bwd_workspace_bytes(M: int, K: int) -> int:

@@ -66,14 +66,15 @@ extern "C" {
 
 FP8SQ_API int fp8_layernorm_fwd(const void* x, const void* residual, int dtype, const float* gamma, const float* beta,
                                 float eps, int64_t M, int64_t K, void* sum_out, void* y, float* mu_out, float* rstd_out,
-                                void* stream)
+                                uint8_t* q_out, int q_format, float* q_state, int q_history_len, void* stream)
 {
     const char* fn = "fp8_layernorm_fwd";
     if (M < 0 || K < 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: negative size", fn);
     if (M >= kMaxDim || K >= kMaxDim) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: dimension too large", fn);
     if (!valid_dtype(dtype)) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: bad dtype", fn);
     if (K == 0 && M != 0) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: a row needs at least one element", fn);
-    if ((!x || !y || !gamma) && M != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: null x, gamma or y", fn);
+    if ((!x || !gamma) && M != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: null x or gamma", fn);
+    if (!y && !q_out && M != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: neither y nor codes asked for", fn);
     if ((residual != nullptr) != (sum_out != nullptr) && M != 0)
         return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: residual and sum_out come together", fn);
     if (!(eps >= 0.0f)) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
@@ -82,6 +83,7 @@ FP8SQ_API int fp8_layernorm_fwd(const void* x, const void* residual, int dtype, 
         return api_fail(FP8SQ_ERR_MISALIGNED, "%s: x, residual, sum, y, gamma, beta must be 16-byte aligned", fn);
     if (!aligned(mu_out, 4) || !aligned(rstd_out, 4)) return api_fail(FP8SQ_ERR_MISALIGNED, "%s: mu, rstd must be 4-byte aligned", fn);
     int sms, r;
+    if ((r = check_cast(fn, q_out, q_format, q_state, q_history_len))) return r;
     if ((r = fp8sq::api_check_device(&sms))) return r;
     fp8sq::LnArgs a;
     a.M = M;
@@ -96,6 +98,10 @@ FP8SQ_API int fp8_layernorm_fwd(const void* x, const void* residual, int dtype, 
     a.y = y;
     a.mu = mu_out;
     a.rstd = rstd_out;
+    a.q = q_out;
+    a.q_format = q_format;
+    a.q_state = q_state;
+    a.q_history_len = q_history_len;
     return cuda_status(fp8sq::launch_layernorm_fwd(a, static_cast<cudaStream_t>(stream), sms), "fp8_layernorm_fwd launch");
 }
 

@@ -123,6 +123,10 @@ struct LnArgs {
     const void* residual = nullptr;  // forward: added to x
     void* sum = nullptr;             // forward: x + residual as rounded
     void* y = nullptr;
+    uint8_t* q = nullptr;            // forward: codes of y under a delayed state, or null
+    int q_format = kE4M3;
+    float* q_state = nullptr;
+    int q_history_len = 0;
     float* mu = nullptr;
     float* rstd = nullptr;
     const void* dy = nullptr;        // backward

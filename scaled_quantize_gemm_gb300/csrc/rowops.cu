@@ -51,15 +51,30 @@ __device__ __forceinline__ float cta_sum(float v, float* red)
     return ((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7]));
 }
 
+__device__ __forceinline__ uint8_t code1(float v, int fmt)
+{
+    return (uint8_t)(fmt == kE4M3 ? cvt_e4m3x2(v, 0.0f) : cvt_e5m2x2(v, 0.0f));
+}
+// a warp's largest |value| into a state's newest amax: not negative, so ordered
+// as integers, a NaN above everything
+__device__ __forceinline__ void record_amax(float amax, float* state)
+{
+    const uint32_t a = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
+    if ((threadIdx.x & 31) == 0) atomicMax(reinterpret_cast<unsigned int*>(state), a);
+}
+
 // ------------------------------------------------------------------ any row length
 template <typename T>
 __global__ void __launch_bounds__(256) k_ln_fwd_any(const T* x, const T* __restrict__ res,
                                                     const float* __restrict__ gamma, const float* __restrict__ beta,
                                                     float eps, int64_t R, int64_t K, T* sum, T* __restrict__ y,
-                                                    float* __restrict__ mu, float* __restrict__ rstd)
+                                                    float* __restrict__ mu, float* __restrict__ rstd,
+                                                    uint8_t* __restrict__ q, int fmt, float* qstate, int H)
 {
     pdl_enter();
     __shared__ float red[8];
+    const float m = q ? qstate[H] : 1.0f;
+    float amax = 0.0f;
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         const T* xr = x + r * K;
         float s = 0.0f;
@@ -84,9 +99,16 @@ __global__ void __launch_bounds__(256) k_ln_fwd_any(const T* x, const T* __restr
             if (mu) mu[r] = mean;
             if (rstd) rstd[r] = rs;
         }
-        for (int64_t c = threadIdx.x; c < K; c += 256)
-            y[r * K + c] = from_f<T>(fmaf((to_f(xr[c]) - mean) * rs, gamma[c], beta ? beta[c] : 0.0f));
+        for (int64_t c = threadIdx.x; c < K; c += 256) {
+            const float v = fmaf((to_f(xr[c]) - mean) * rs, gamma[c], beta ? beta[c] : 0.0f);
+            if (y) y[r * K + c] = from_f<T>(v);
+            if (q) {
+                amax = max_nan(amax, fabsf(v));
+                q[r * K + c] = code1(__fmul_rn(v, m), fmt);
+            }
+        }
     }
+    if (q) record_amax(amax, qstate);
 }
 
 template <typename T>
@@ -182,7 +204,7 @@ __global__ void __launch_bounds__(256) k_act_bwd_any(const __nv_bfloat16* __rest
                 if (q) {
                     amax = max(amax, __float_as_uint(d) & 0x7FFFFFFFu);
                     const float v = __fmul_rn(d, m);
-                    q[r * N + c] = (uint8_t)(fmt == kE4M3 ? cvt_e4m3x2(v, 0.0f) : cvt_e5m2x2(v, 0.0f));
+                    q[r * N + c] = code1(v, fmt);
                 }
             }
         });
@@ -303,11 +325,17 @@ __device__ __forceinline__ float2 block_total2(const float (*red)[32], int span)
 // at most MAXT threads, 1536 threads (six CTAs at 4096 columns: 82 us for 16384
 // rows in bf16 with residual, 96 % of the copy rate; four 93, eight 105).
 constexpr int kLnCols = 16;         // columns a thread holds
-template <typename T, int VEC, int MAXT, int MINB>
+// CODES: y also (or only) as FP8 codes under a delayed state, cast from fp32.
+struct LnCast {
+    uint8_t* q;
+    int fmt, H;
+    float* state;
+};
+template <typename T, int VEC, int MAXT, int MINB, bool CODES>
 __global__ void __launch_bounds__(MAXT, MINB)
     k_ln_fwd(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ gamma,
              const float* __restrict__ beta, float eps, int64_t R, int K, T* __restrict__ sum, T* __restrict__ y,
-             float* __restrict__ mu, float* __restrict__ rstd)
+             float* __restrict__ mu, float* __restrict__ rstd, LnCast cast)
 {
     constexpr int NV = kLnCols / VEC;
     using P = Pack<T, VEC>;
@@ -319,6 +347,8 @@ __global__ void __launch_bounds__(MAXT, MINB)
     if (nt < 64 && t < 32) red[1][t] = 0.0f;
     __syncthreads();
     pdl_enter();
+    const float m = CODES ? cast.state[cast.H] : 1.0f;
+    float amax = 0.0f;
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         const int64_t base = r * K;
         Raw raw[NV];
@@ -394,9 +424,30 @@ __global__ void __launch_bounds__(MAXT, MINB)
             if (beta) load_param<VEC>(beta, c, b);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) v[j] = fmaf((v[j] - mean) * rs, g[j], b[j]);
-            *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(v);
+            if (!CODES || y) *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(v);
+            if constexpr (CODES) {
+                uint8_t* q = cast.q + base + c;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    amax = max_nan(amax, fabsf(v[j]));
+                    v[j] = __fmul_rn(v[j], m);
+                }
+                if constexpr (VEC >= 2) {
+                    uint16_t h[VEC / 2];
+#pragma unroll
+                    for (int j = 0; j < VEC; j += 2)
+                        h[j / 2] = (uint16_t)(cast.fmt == kE4M3 ? cvt_e4m3x2(v[j], v[j + 1]) : cvt_e5m2x2(v[j], v[j + 1]));
+                    if constexpr (VEC == 8)
+                        *reinterpret_cast<uint2*>(q) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+                    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(q) = h[0] | (uint32_t)h[1] << 16;
+                    else *reinterpret_cast<uint16_t*>(q) = h[0];
+                } else {
+                    *q = code1(v[0], cast.fmt);
+                }
+            }
         }
     }
+    if constexpr (CODES) record_amax(amax, cast.state);
 }
 
 // ------------------------------------------------------------------ LayerNorm backward
@@ -756,40 +807,44 @@ int resident(const void* kern, int threads, int smem, int sms)
     return per_sm * sms;
 }
 
-template <typename T, int VEC, int MAXT, int MINB>
+template <typename T, int VEC, int MAXT, int MINB, bool CODES>
 cudaError_t ln_fwd_cta(const LnArgs& a, cudaStream_t st, int sms, int threads)
 {
-    auto kern = k_ln_fwd<T, VEC, MAXT, MINB>;
+    auto kern = k_ln_fwd<T, VEC, MAXT, MINB, CODES>;
     const int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, 0, sms);
     launch_k(kern, (unsigned)(a.M < cap ? a.M : cap), threads, 0, st, static_cast<const T*>(a.x),
              static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, (int)a.K, static_cast<T*>(a.sum),
-             static_cast<T*>(a.y), a.mu, a.rstd);
+             static_cast<T*>(a.y), a.mu, a.rstd, LnCast{a.q, a.q_format, a.q_history_len, a.q_state});
     return cudaGetLastError();
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool CODES>
 cudaError_t ln_fwd_rows(const LnArgs& a, cudaStream_t st, int sms)
 {
     const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
-    if (threads <= 256) return ln_fwd_cta<T, VEC, 256, 6>(a, st, sms, threads);
-    if (threads <= 512) return ln_fwd_cta<T, VEC, 512, 3>(a, st, sms, threads);
-    if (threads <= 768) return ln_fwd_cta<T, VEC, 768, 2>(a, st, sms, threads);
-    return ln_fwd_cta<T, VEC, 1024, 1>(a, st, sms, threads);
+    if (threads <= 256) return ln_fwd_cta<T, VEC, 256, 6, CODES>(a, st, sms, threads);
+    if (threads <= 512) return ln_fwd_cta<T, VEC, 512, 3, CODES>(a, st, sms, threads);
+    if (threads <= 768) return ln_fwd_cta<T, VEC, 768, 2, CODES>(a, st, sms, threads);
+    return ln_fwd_cta<T, VEC, 1024, 1, CODES>(a, st, sms, threads);
+}
+
+template <typename T, bool CODES>
+cudaError_t ln_fwd_vec(const LnArgs& a, cudaStream_t st, int sms)
+{
+    constexpr int WIDE = 16 / (int)sizeof(T), NARROW = WIDE / 4;     // 16 and 4 bytes
+    if (a.K % WIDE == 0) return ln_fwd_rows<T, WIDE, CODES>(a, st, sms);
+    if (a.K % NARROW == 0) return ln_fwd_rows<T, NARROW, CODES>(a, st, sms);
+    return ln_fwd_rows<T, 1, CODES>(a, st, sms);
 }
 
 template <typename T>
 cudaError_t ln_fwd(const LnArgs& a, cudaStream_t st, int sms)
 {
-    constexpr int WIDE = 16 / (int)sizeof(T), NARROW = WIDE / 4;     // 16 and 4 bytes
-    if (a.K <= 1024 * kLnCols) {
-        if (a.K % WIDE == 0) return ln_fwd_rows<T, WIDE>(a, st, sms);
-        if (a.K % NARROW == 0) return ln_fwd_rows<T, NARROW>(a, st, sms);
-        return ln_fwd_rows<T, 1>(a, st, sms);
-    }
+    if (a.K <= 1024 * kLnCols) return a.q ? ln_fwd_vec<T, true>(a, st, sms) : ln_fwd_vec<T, false>(a, st, sms);
     const int64_t cap = (int64_t)sms * 8;
     launch_k(k_ln_fwd_any<T>, (unsigned)(a.M < cap ? a.M : cap), 256, 0, st, static_cast<const T*>(a.x),
              static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, a.K, static_cast<T*>(a.sum),
-             static_cast<T*>(a.y), a.mu, a.rstd);
+             static_cast<T*>(a.y), a.mu, a.rstd, a.q, a.q_format, a.q_state, a.q_history_len);
     return cudaGetLastError();
 }
 

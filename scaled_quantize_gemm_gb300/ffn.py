@@ -1,0 +1,152 @@
+"""A pre-norm gated feed-forward sublayer on the FP8 path (te.LayerNormMLP's
+parts, gated):
+
+    n = LayerNorm(x) gamma + beta            cast to E4M3 in the same kernel
+    [g | u] = n [W_gate; W_up]^T             one product; h = act(g) u is formed
+    h = act(g) u                             and cast in its epilogue
+    y = x + h W_down^T                       the residual added in the epilogue
+
+with per-tensor delayed scaling for every cast.  ``forward`` and ``backward``
+are a training step (weights cast from bf16 every step, as they change);
+``freeze`` casts the weights once and ``decode`` runs a few tokens at a time
+with the scales as they stand: three kernels, each streaming its weights once.
+
+The backward pass takes dY in E5M2 (HYBRID) and never writes the gradient of
+h: its product's epilogue turns it into the codes of [dg | du], which feed the
+data and weight gradients as they are.
+"""
+from __future__ import annotations
+
+import torch
+
+import scaled_quantize_gemm_gb300 as sq
+
+# delayed-scaling states, in the order of GatedFFN.states
+N, W_GU, H_, W_DOWN, DY, DGU = range(6)
+FORMATS = [sq.E4M3, sq.E4M3, sq.E4M3, sq.E4M3, sq.E5M2, sq.E5M2]
+
+
+class GatedFFN:
+    """One sublayer's weights, scaling states and buffers.
+
+    gamma [K] fp32, beta [K] fp32 or None, w_gate_up [2F][K] bf16 (the gate's
+    rows, then the up projection's), w_down [K][F] bf16; K, F multiples of 16.
+    A training step takes a number of tokens that is a multiple of 16 (the
+    weight gradients contract over them); ``decode`` takes any number.
+    """
+
+    def __init__(self, gamma, beta, w_gate_up, w_down, act: int = sq.ACT_SILU, eps: float = 1e-5,
+                 history_len: int = 16):
+        F2, K = w_gate_up.shape
+        if F2 % 32 or K % 16 or tuple(w_down.shape) != (K, F2 // 2):
+            raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not make a "
+                             "gated block of sizes that are multiples of 16")
+        self.gamma, self.beta, self.w_gate_up, self.w_down = gamma, beta, w_gate_up, w_down
+        self.K, self.F, self.act, self.eps, self.H = K, F2 // 2, act, eps, history_len
+        dev = w_gate_up.device
+        self.states = torch.empty(6 * sq.state_floats(history_len), device=dev)
+        sq.fp8_scale_init(self.states, 6, history_len)
+        self.q_gate_up = torch.empty((F2, K), dtype=torch.uint8, device=dev)
+        self.q_down = torch.empty((K, self.F), dtype=torch.uint8, device=dev)
+        self._buffers = {}
+        self._saved = None
+
+    # ------------------------------------------------------------ states and scratch
+    def _state(self, i):
+        n = sq.state_floats(self.H)
+        return self.states[i * n:(i + 1) * n]
+
+    def _scale(self, i):
+        """the dequantisation step of a state's codes (one element)"""
+        j = (i + 1) * sq.state_floats(self.H) - 1
+        return self.states[j:j + 1]
+
+    def _get(self, name, shape, dtype):
+        """a buffer that lives as long as its shape is asked for"""
+        t = self._buffers.get(name)
+        if t is None or t.shape != torch.Size(shape) or t.dtype != dtype:
+            t = self._buffers[name] = torch.empty(shape, dtype=dtype, device=self.states.device)
+        return t
+
+    def _workspace(self, name, nbytes):
+        """scratch of the split products (zeroed when made, left so by every call)"""
+        if nbytes == 0:
+            return None
+        t = self._buffers.get(name)
+        if t is None or t.numel() < nbytes:
+            t = self._buffers[name] = torch.zeros(nbytes, dtype=torch.uint8, device=self.states.device)
+        return t
+
+    def calibrate(self, x):
+        """One forward pass that sets the activations' and weights' scales from what it records."""
+        for _ in range(2):
+            self.forward(x)
+            self.update_scales()
+
+    def update_scales(self):
+        """The end-of-step update of all states (history maximum)."""
+        sq.fp8_update_scale(self.states, 6, self.H, FORMATS)
+
+    def freeze(self):
+        """Casts both weights with their current scales, for ``decode``."""
+        for w, q, i in ((self.w_gate_up, self.q_gate_up, W_GU), (self.w_down, self.q_down, W_DOWN)):
+            sq.fp8_quantize(w, FORMATS[i], sq.TENSOR, q, delayed_state=self._state(i), history_len=self.H)
+
+    # ------------------------------------------------------------ one pass
+    def _run(self, x, gu, mu, rstd, y):
+        M, K, F, H = x.shape[0], self.K, self.F, self.H
+        qn, qh = self._get("qn", (M, K), torch.uint8), self._get("qh", (M, F), torch.uint8)
+        sq.fp8_layernorm_fwd(x, self.gamma, self.beta, self.eps, None, mu=mu, rstd=rstd, q_out=qn, q_format=sq.E4M3,
+                             q_state=self._state(N), history_len=H)
+        sq.fp8_glu_fwd(qn, sq.E4M3, self._scale(N), self.q_gate_up, sq.E4M3, self._scale(W_GU), self.act, gu_out=gu,
+                       q_out=qh, q_format=sq.E4M3, q_state=self._state(H_), history_len=H,
+                       workspace=self._workspace("ws_gu", sq.fp8_glu_fwd_workspace_bytes(M, F, K)))
+        sq.fp8_gemm_act(qh, sq.E4M3, self._scale(H_), self.q_down, sq.E4M3, self._scale(W_DOWN), sq.ACT_NONE, D=y,
+                        residual=x, workspace=self._workspace("ws_down", sq.fp8_gemm_act_workspace_bytes(M, K, F)))
+        return qn, qh
+
+    def decode(self, x, y=None):
+        """y for any number of tokens, on the frozen weights; keeps nothing for a backward pass."""
+        y = torch.empty_like(x) if y is None else y
+        self._run(x, None, None, None, y)
+        return y
+
+    def forward(self, x):
+        """y [M][K] bf16 of x [M][K] bf16; keeps what ``backward`` needs."""
+        M = x.shape[0]
+        self.freeze()
+        gu = self._get("gu", (M, 2 * self.F), torch.bfloat16)
+        mu, rstd = self._get("mu", (M,), torch.float32), self._get("rstd", (M,), torch.float32)
+        y = torch.empty_like(x)
+        qn, qh = self._run(x, gu, mu, rstd, y)
+        self._saved = (x, gu, mu, rstd, qn, qh)
+        return y
+
+    def backward(self, dy):
+        """-> (dx bf16, dgamma, dbeta, dw_gate_up, dw_down, all fp32) of the last forward."""
+        if self._saved is None:
+            raise RuntimeError("backward without a forward")
+        x, gu, mu, rstd, qn, qh = self._saved
+        self._saved = None
+        M, K, F, H = x.shape[0], self.K, self.F, self.H
+        if M % 16:
+            raise ValueError(f"a training step takes a multiple of 16 tokens, got {M}")
+        dev = x.device
+        qdy, qdgu = self._get("qdy", (M, K), torch.uint8), self._get("qdgu", (M, 2 * F), torch.uint8)
+        sq.fp8_quantize(dy, sq.E5M2, sq.TENSOR, qdy, delayed_state=self._state(DY), history_len=H)
+        sq.fp8_glu_bwd(qdy, sq.E5M2, self._scale(DY), self.q_down, sq.E4M3, self._scale(W_DOWN), gu, self.act, qdgu,
+                       sq.E5M2, self._state(DGU), H)
+        dn = self._get("dn", (M, K), torch.bfloat16)
+        dw_gu = torch.empty((2 * F, K), device=dev)
+        dw_down = torch.empty((K, F), device=dev)
+        s_dy, s_dgu = self._scale(DY), self._scale(DGU)
+        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.K_MAJOR, self.q_gate_up, sq.E4M3, self._scale(W_GU), sq.MN_MAJOR,
+                           dn, M, K, 2 * F)
+        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.MN_MAJOR, qn, sq.E4M3, self._scale(N), sq.MN_MAJOR, dw_gu, 2 * F,
+                           K, M)
+        sq.fp8_gemm_layout(qdy, sq.E5M2, s_dy, sq.MN_MAJOR, qh, sq.E4M3, self._scale(H_), sq.MN_MAJOR, dw_down, K, F,
+                           M)
+        dx, dgamma, dbeta = torch.empty_like(x), torch.empty(K, device=dev), torch.empty(K, device=dev)
+        ws = self._get("ws_ln", (max(16, sq.fp8_layernorm_bwd_workspace_bytes(M, K)),), torch.uint8)
+        sq.fp8_layernorm_bwd(dn, x, self.gamma, mu, rstd, dx, dgamma, dbeta, ws, dres=dy)
+        return dx, dgamma, dbeta, dw_gu, dw_down

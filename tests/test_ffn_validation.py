@@ -20,11 +20,13 @@ def L():
 
 
 def test_layernorm_fwd(L):
-    def call(x=F, res=None, dtype=0, gamma=F, beta=F, eps=1e-5, M=4, K=10, total=None, y=F, mu=F, rstd=F):
-        return L.fp8_layernorm_fwd(x, res, dtype, gamma, beta, c.c_float(eps), M, K, total, y, mu, rstd, None)
+    def call(x=F, res=None, dtype=0, gamma=F, beta=F, eps=1e-5, M=4, K=10, total=None, y=F, mu=F, rstd=F, q=None, qf=0,
+             st=None, H=0):
+        return L.fp8_layernorm_fwd(x, res, dtype, gamma, beta, c.c_float(eps), M, K, total, y, mu, rstd, q, qf, st, H, None)
 
     for bad in (dict(x=None), dict(gamma=None), dict(y=None), dict(dtype=2), dict(M=-1), dict(K=-1), dict(res=F),
-                dict(total=F), dict(eps=-1.0), dict(eps=float("nan"))):
+                dict(total=F), dict(eps=-1.0), dict(eps=float("nan")), dict(q=F), dict(q=F, st=F, H=0),
+                dict(q=F, st=F, H=4, qf=5)):
         assert call(**bad) == sq.ERR_INVALID_ARG, bad
     for bad in (dict(x=P(4104)), dict(gamma=P(4100)), dict(beta=P(4100)), dict(y=P(4098)), dict(mu=P(4098)),
                 dict(res=P(4104), total=F)):
@@ -120,7 +122,7 @@ def test_act_bwd(L):
 def test_no_gpu_is_an_error(L):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
-    assert L.fp8_layernorm_fwd(F, None, 0, F, F, c.c_float(1e-5), 4, 16, None, F, F, F, None) == sq.ERR_CUDA
+    assert L.fp8_layernorm_fwd(F, None, 0, F, F, c.c_float(1e-5), 4, 16, None, F, F, F, None, 0, None, 0, None) == sq.ERR_CUDA
     assert L.fp8_glu_bwd(F, 1, F, F, 0, F, 4, 32, 64, F, 4, F, 1, F, 4, None) == sq.ERR_CUDA
 
 
@@ -137,6 +139,10 @@ def test_binding_checks_shapes_and_types():
         sq.fp8_layernorm_fwd(z(10, 4, dtype=bf16).t(), g, None, 1e-5, z(4, 10, dtype=bf16))
     with pytest.raises(ValueError, match="residual"):
         sq.fp8_layernorm_fwd(x, g, None, 1e-5, z(4, 10, dtype=bf16), residual=x)
+    with pytest.raises(ValueError, match="y is required"):
+        sq.fp8_layernorm_fwd(x, g, None, 1e-5, None)
+    with pytest.raises(ValueError, match="q_state"):
+        sq.fp8_layernorm_fwd(x, g, None, 1e-5, None, q_out=z(4, 10, dtype=u8), q_state=z(5), history_len=4)
     with pytest.raises(ValueError, match="rstd"):
         sq.fp8_layernorm_bwd(x, x, g, z(4), z(3), z(4, 10, dtype=bf16), g, g, z(1, dtype=u8))
     A, B, one = z(4, 32, dtype=u8), z(16, 32, dtype=u8), z(1)

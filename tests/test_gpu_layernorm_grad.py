@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import scaled_quantize_gemm_gb300 as sq
-from _ffn_ref import U, assert_within, gen, randn
+from _ffn_ref import U, assert_amax, assert_codes, assert_within, gen, new_state, randn
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -67,6 +67,33 @@ def test_forward(M, K, dtype):
         y2 = torch.empty_like(y)
         sq.fp8_layernorm_fwd(x, gamma, b, EPS, y2, residual=res, sum_out=total)
         assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt,m", [(sq.E4M3, 60.0), (sq.E5M2, 5000.0)])
+@pytest.mark.parametrize("M,K", [(1, 4096), (3, 7), (17, 1002), (33, 1535), (300, 264), (5, 12288), (2, 20000)])
+def test_forward_codes(M, K, fmt, m, dtype):
+    """The codes of y, with and without y itself, and the newest amax."""
+    g = gen(M * 139 + K)
+    x = (randn(g, M, K) * 2 + randn(g, M, 1)).to(dtype)
+    gamma, beta = randn(g, K) * 0.2 + 1, randn(g, K) * 0.1
+    m64, r64, y64 = _fwd64(x.double(), gamma.double(), beta.double())
+    c = (K / 32 + 16) * U
+    e_mu = c * x.double().abs().mean(1) + U * m64.abs()
+    e_r = 0.5 * (2 * c + 8 * U + (2 * e_mu * r64 + (e_mu * r64) ** 2)) + 8 * U
+    d = (x.double() - m64[:, None]).abs()
+    e = gamma.double().abs() * r64[:, None] * (e_mu[:, None] + 2 * U * d + d * e_r[:, None]) + 8 * U * (
+        gamma.double().abs() * d * r64[:, None] + beta.double().abs())
+    y, mu, rstd = torch.empty_like(x), torch.empty(M, device=DEV), torch.empty(M, device=DEV)
+    seen = []
+    for out in (y, None):
+        q, st = torch.full((M, K), 0x55, dtype=torch.uint8, device=DEV), new_state(16, m, 0.5)
+        sq.fp8_layernorm_fwd(x, gamma, beta, EPS, out, mu=mu, rstd=rstd, q_out=q, q_format=fmt, q_state=st, history_len=16)
+        assert_codes(q, y64, e, m, fmt, "codes")
+        assert_amax(st, 0.5, y64, e, "amax")
+        seen.append(q)
+    assert torch.equal(*seen)
+    _check_fwd(x, gamma, beta, y, mu, rstd)
 
 
 def _bwd64(dy, x, gamma, mu, rstd, dres):
