@@ -33,7 +33,10 @@ __device__ __forceinline__ void pdl_enter()
 
 // Lets the next kernel on the stream launch before this grid has ended (its
 // pdl_enter still waits for the end).  Only for grids that are resident as a
-// whole, once they have issued their loads: k_ffn_rows.
+// whole, so that no CTA of theirs waits for a place that a dependent has taken:
+// k_ffn_rows once it has issued its loads, and the LayerNorm forward, whose
+// dependents then prepare (and prefetch weights) under it.  A decoded token's
+// three kernels (4096 -> 14336 -> 4096): 45.3 us without, 42.4 with.
 __device__ __forceinline__ void pdl_trigger()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

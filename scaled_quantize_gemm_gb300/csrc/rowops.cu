@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     if (t < 64) red[t >> 5][t & 31] = 0.0f;
     if (nt < 64 && t < 32) red[1][t] = 0.0f;
     __syncthreads();
+    pdl_trigger();
     pdl_enter();
     const float m = CODES ? cast.state[cast.H] : 1.0f;
     float amax = 0.0f;
