@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
 // the row's normalised values and dy gamma in registers across the barrier
 // (rows of up to 8192; longer ones read the ring again).  Rows that move one
 // element at a time (odd bf16 or fp32 lengths) take 8 columns (4096 x 1001
-// bf16: 45 us against 75 with 16).
+// bf16: 45 us against 75 with 16, before their copies were asynchronous).
 __device__ __forceinline__ void cp_async4(void* s, const void* g)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s)), "l"(g) : "memory");
@@ -501,52 +501,48 @@ __global__ void __launch_bounds__(MAXT, MINB)
     __syncthreads();
     pdl_enter();
     const int narr = dres ? 3 : 2;
-    // [stage][array][vector i][thread]
-    Raw* ring = reinterpret_cast<Raw*>(ln_ring) + threadIdx.x;
-    auto slot = [&](int st, int arr, int i) -> Raw* { return ring + ((st * narr + arr) * NV + i) * blockDim.x; };
+    // [stage][array][vector i][thread].  A 2-byte element travels as the aligned
+    // 32-bit word it is part of (cp.async's smallest copy), HALF.
+    constexpr bool HALF = sizeof(Raw) == 2;
+    using Slot = typename RawVec<HALF ? 4 : (int)sizeof(Raw)>::type;
+    Slot* ring = reinterpret_cast<Slot*>(ln_ring) + threadIdx.x;
+    auto slot = [&](int st, int arr, int i) -> Slot* { return ring + ((st * narr + arr) * NV + i) * blockDim.x; };
     auto stage = [&](int st, int64_t r) {
         if (r < R) {
-            if constexpr (sizeof(Raw) >= 4) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (i * nt + t) * VEC;
-                    if (c < K) {
-                        auto copy = [&](int arr, const T* src) {
-                            if constexpr (sizeof(Raw) == 16) cp_async16(slot(st, arr, i), src + r * K + c);
-                            else cp_async4(slot(st, arr, i), src + r * K + c);
-                        };
-                        copy(0, x);
-                        copy(1, dy);
-                        if (dres) copy(2, dres);
-                    }
-                }
-            } else {
-                // 2 bytes: below cp.async's smallest size, through registers
-                Raw v[3][NV];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (i * nt + t) * VEC;
-                    if (c < K) {
-                        v[0][i] = *reinterpret_cast<const Raw*>(x + r * K + c);
-                        v[1][i] = *reinterpret_cast<const Raw*>(dy + r * K + c);
-                        if (dres) v[2][i] = *reinterpret_cast<const Raw*>(dres + r * K + c);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    *slot(st, 0, i) = v[0][i];
-                    *slot(st, 1, i) = v[1][i];
-                    if (dres) *slot(st, 2, i) = v[2][i];
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + t) * VEC;
+                if (c < K) {
+                    const int64_t at = r * K + c;
+                    auto copy = [&](int arr, const T* src) {
+                        if constexpr (sizeof(Raw) == 16) {
+                            cp_async16(slot(st, arr, i), src + at);
+                        } else if constexpr (sizeof(Raw) == 4) {
+                            cp_async4(slot(st, arr, i), src + at);
+                        } else {
+                            // the last element of an odd count has no partner
+                            if ((at | 1) < R * K) cp_async4(slot(st, arr, i), src + (at & ~(int64_t)1));
+                            else *slot(st, arr, i) = *reinterpret_cast<const uint16_t*>(src + at);
+                        }
+                    };
+                    copy(0, x);
+                    copy(1, dy);
+                    if (dres) copy(2, dres);
                 }
             }
         }
         cp_async_commit();
     };
     // columns past K hold zeros in every array, so they add nothing
-    auto fetch = [&](int st, int arr, float2 (&v)[C / 2]) {
+    auto fetch = [&](int st, int arr, int64_t r, float2 (&v)[C / 2]) {
         float f[NV][VEC];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) P::to_floats((i * nt + t) * VEC < K ? *slot(st, arr, i) : Raw{}, f[i]);
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * nt + t) * VEC;
+            const Slot raw = c < K ? *slot(st, arr, i) : Slot{};
+            if constexpr (HALF) f[i][0] = __uint_as_float(((r * K + c) & 1) ? raw & 0xFFFF0000u : raw << 16);
+            else P::to_floats(raw, f[i]);
+        }
 #pragma unroll
         for (int j = 0; j < C / 2; ++j)
             v[j] = make_float2(f[(2 * j) / VEC][(2 * j) % VEC], f[(2 * j + 1) / VEC][(2 * j + 1) % VEC]);
@@ -582,8 +578,8 @@ __global__ void __launch_bounds__(MAXT, MINB)
         cp_async_wait<STAGES - 1>();
         float2 xh[C / 2], w[C / 2];
         auto load_row = [&]() {
-            fetch(st, 0, xh);
-            fetch(st, 1, w);
+            fetch(st, 0, r, xh);
+            fetch(st, 1, r, w);
             if constexpr (!GREG) params(gam);
 #pragma unroll
             for (int j = 0; j < C / 2; ++j) xh[j] = __fmul2_rn(__fadd2_rn(xh[j], f2(-mean)), f2(rs));
@@ -618,7 +614,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
         for (int j = 0; j < C / 2; ++j)
             w[j] = __fmul2_rn(__ffma2_rn(xh[j], f2(-c2), __fadd2_rn(w[j], f2(-c1))), f2(rs));
         if (dres) {
-            fetch(st, 2, xh);
+            fetch(st, 2, r, xh);
 #pragma unroll
             for (int j = 0; j < C / 2; ++j) w[j] = __fadd2_rn(w[j], xh[j]);
         }
@@ -663,11 +659,25 @@ __global__ void __launch_bounds__(MAXT, MINB)
     for (int i = 0; i < NV; ++i) {
         const int c = (i * nt + t) * VEC;
         if (c >= K) continue;
+        // (sixteen-byte stores: with single floats, 32 bytes apart in a warp,
+        // 16384 x 4096 took 92 us instead of 84 and 512 x 4096 16 instead of 8)
+        if constexpr (VEC % 4 == 0) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int e = i * VEC + j;
-            pg[c + j] = (e & 1) ? ag[e / 2].y : ag[e / 2].x;
-            pg[K + c + j] = (e & 1) ? ab[e / 2].y : ab[e / 2].x;
+            for (int j = 0; j < VEC; j += 4) {
+                const int e = (i * VEC + j) / 2;
+                *reinterpret_cast<float4*>(pg + c + j) = make_float4(ag[e].x, ag[e].y, ag[e + 1].x, ag[e + 1].y);
+                *reinterpret_cast<float4*>(pg + K + c + j) = make_float4(ab[e].x, ab[e].y, ab[e + 1].x, ab[e + 1].y);
+            }
+        } else if constexpr (VEC == 2) {
+            *reinterpret_cast<float2*>(pg + c) = ag[i];
+            *reinterpret_cast<float2*>(pg + K + c) = ab[i];
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int e = i * VEC + j;
+                pg[c + j] = (e & 1) ? ag[e / 2].y : ag[e / 2].x;
+                pg[K + c + j] = (e & 1) ? ab[e / 2].y : ab[e / 2].x;
+            }
         }
     }
 }
@@ -882,7 +892,8 @@ cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
     int groups = MAXT <= 256 ? MAXT / group : 1;
     groups = groups < kLnGroups ? groups : kLnGroups;
     while (groups > 1 && a.M < (int64_t)groups * sms) --groups;
-    const int stage = group * groups * C * (int)sizeof(T) * (a.dres ? 3 : 2);
+    const int bytes = sizeof(T) * VEC == 2 ? 4 : (int)sizeof(T);          // an element in the ring
+    const int stage = group * groups * C * bytes * (a.dres ? 3 : 2);
     if constexpr (MAXT <= 256) {
         if (groups > 1) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, true>(a, st, sms, group, groups, 3 * stage, parts);
     }
