@@ -71,21 +71,29 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // the first `left` of 32 columns, nothing where keep is 0
 __device__ __forceinline__ void max32(uint32_t& amax, const float2 (&v)[16], int left, uint32_t keep)
 {
-    uint32_t m = 0;
+    float m = 0.0f;
+    if (left >= 32) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if (2 * j < left) m = max(m, max(abs_bits(v[j].x), abs_bits(v[j].y)));
-    amax = max(amax, m & keep);
+        for (int j = 0; j < 16; ++j) m = max3_nan(m, fabsf(v[j].x), fabsf(v[j].y));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (2 * j < left) m = max3_nan(m, fabsf(v[j].x), fabsf(v[j].y));
+    }
+    amax = max(amax, __float_as_uint(m) & keep);       // not negative: ordered as integers, a NaN above all
 }
 // 32 codes of one row
 __device__ __forceinline__ void codes32(uint32_t (&w)[8], const float2 (&v)[16], float m, int fmt)
 {
+    auto all = [&](auto cvt) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 a = __fmul2_rn(v[2 * j], f2(m)), b = __fmul2_rn(v[2 * j + 1], f2(m));
-        w[j] = fmt == kE4M3 ? (cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16))
-                            : (cvt_e5m2x2(a.x, a.y) | (cvt_e5m2x2(b.x, b.y) << 16));
-    }
+        for (int j = 0; j < 8; ++j) {
+            const float2 a = __fmul2_rn(v[2 * j], f2(m)), b = __fmul2_rn(v[2 * j + 1], f2(m));
+            w[j] = cvt(a.x, a.y) | (cvt(b.x, b.y) << 16);
+        }
+    };
+    if (fmt == kE4M3) all([](float a, float b) { return cvt_e4m3x2(a, b); });
+    else all([](float a, float b) { return cvt_e5m2x2(a, b); });
 }
 __device__ __forceinline__ void store32_bf16(__nv_bfloat16* d, int left, const float2 (&v)[16])
 {
@@ -168,14 +176,27 @@ struct Stager {
     }
 };
 
+// a whole 32-byte sector in one load (16-byte loads by row take each twice)
+__device__ __forceinline__ void ldg32(uint4& a, uint4& b, const void* p)
+{
+    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+        : "l"(p));
+}
 // 32 columns of a row of bf16 (64 bytes) or fp32 (128 bytes) into registers,
-// ahead of their use; zeros past `left`
+// ahead of their use; zeros past `bytes_left`
 template <int N>
 __device__ __forceinline__ void fetch_row(uint4* raw, const void* src, int bytes_left)
 {
     const uint4* s = static_cast<const uint4*>(src);
 #pragma unroll
-    for (int i = 0; i < N; ++i) raw[i] = 16 * (i + 1) <= bytes_left ? __ldg(s + i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < N; i += 2) {
+        if (16 * (i + 2) <= bytes_left && (reinterpret_cast<uintptr_t>(src) & 31) == 0) ldg32(raw[i], raw[i + 1], s + i);
+        else {
+            raw[i] = 16 * (i + 1) <= bytes_left ? __ldg(s + i) : make_uint4(0, 0, 0, 0);
+            raw[i + 1] = 16 * (i + 2) <= bytes_left ? __ldg(s + i + 1) : make_uint4(0, 0, 0, 0);
+        }
+    }
 }
 __device__ __forceinline__ float2 raw_bf16(const uint4* raw, int j)     // columns 2 j, 2 j + 1
 {

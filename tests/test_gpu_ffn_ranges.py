@@ -27,6 +27,53 @@ def test_random_sizes(seed):
     _glu_bwd_case(M, N, K, act, seed)
 
 
+# ---------------------------------------------------------------- buffers on 16-byte boundaries only
+def _shifted(t):
+    """a copy of t that starts 16 bytes past a 256-byte boundary"""
+    n = 16 // t.element_size()
+    flat = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    out = flat[n:].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 32 == 16
+    return out
+
+
+@pytest.mark.parametrize("M", [5, 64, 203])
+def test_buffers_on_16_byte_boundaries_give_the_same(M):
+    N, K = 272, 528
+    g = gen(M)
+    A, sa = to_codes(randn(g, M, K), 0)
+    B, sb = to_codes(randn(g, 2 * N, K), 0)
+    Wd, swd = to_codes(randn(g, K, N), 0)
+    bias, gamma, beta = randn(g, N), randn(g, N), randn(g, N)
+    x, dy, gu = randn(g, M, N).to(BF), randn(g, M, N).to(BF), randn(g, M, 2 * N).to(BF)
+    res32 = randn(g, M, N)
+    outs = []
+    for f in (lambda t: t, _shifted):
+        e = lambda *s, dtype=BF: f(torch.zeros(s, dtype=dtype, device=DEV))                      # noqa: E731
+        st = [new_state(H, 3.0) for _ in range(4)]
+        a, b, w = f(A), f(B), f(Wd)
+        D, Z, Q, D32 = e(M, N), e(M, N), e(M, N, dtype=torch.uint8), e(M, N, dtype=F32)
+        sq.fp8_gemm_act(a, 0, sa, b[:N].contiguous() if f is not _shifted else _shifted(B[:N]), 0, sb, SILU, D=D,
+                        bias=f(bias), residual=f(x), z_out=Z, q_out=Q, q_state=st[0], history_len=H)
+        sq.fp8_gemm_act(a, 0, sa, f(B[:N].contiguous()), 0, sb, GELU, D=D32, residual=f(res32))
+        G, Hh, Qh = e(M, 2 * N), e(M, N), e(M, N, dtype=torch.uint8)
+        sq.fp8_glu_fwd(a, 0, sa, b, 0, sb, SILU, gu_out=G, h_out=Hh, q_out=Qh, q_state=st[1], history_len=H)
+        dq = e(M, 2 * N, dtype=torch.uint8)
+        sq.fp8_glu_bwd(a, 0, sa, w, 0, swd, f(gu), SILU, dq, sq.E5M2, st[2], H)
+        y, mu, rstd, s = e(M, N), torch.empty(M, device=DEV), torch.empty(M, device=DEV), e(M, N)
+        sq.fp8_layernorm_fwd(f(x), f(gamma), f(beta), 1e-5, y, mu=mu, rstd=rstd, residual=f(dy), sum_out=s)
+        dx, dg, db = e(M, N), torch.empty(N, device=DEV), torch.empty(N, device=DEV)
+        ws = torch.empty(sq.fp8_layernorm_bwd_workspace_bytes(M, N), dtype=torch.uint8, device=DEV)
+        sq.fp8_layernorm_bwd(f(dy), s, f(gamma), mu, rstd, dx, dg, db, ws, dres=f(x))
+        dz, qz, dbias = e(M, N), e(M, N, dtype=torch.uint8), torch.empty(N, device=DEV)
+        wb = torch.empty(sq.fp8_act_bwd_workspace_bytes(M, N), dtype=torch.uint8, device=DEV)
+        sq.fp8_act_bwd(f(dy), f(x), GELU, dbias=dbias, dz=dz, q_out=qz, q_state=st[3], history_len=H, workspace=wb)
+        torch.cuda.synchronize()
+        outs.append([D, Z, Q, D32, G, Hh, Qh, dq, y, mu, rstd, s, dx, dg, db, dz, qz, dbias, *st])
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
+
+
 # ---------------------------------------------------------------- more than 2^31 elements
 ROWS = 160000                     # x 14336 columns: 2.29e9
 
