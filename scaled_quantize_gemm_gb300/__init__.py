@@ -417,7 +417,8 @@ def _cast(q, name: str, rows: int, cols: int, state, history_len: int) -> tuple:
 def _ws(t) -> tuple:
     if t is None:
         return None, 0
-    _need(t, "workspace", _torch.uint8)
+    if t.dtype is not _torch.uint8 or not t.is_contiguous():
+        _need(t, "workspace", _torch.uint8)
     return t.data_ptr(), t.numel()
 
 
@@ -428,15 +429,25 @@ def fp8_layernorm_fwd(x, gamma, beta, eps: float, y, mu=None, rstd=None, residua
     T = _t()
     px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
     dt = x.dtype
-    if (residual is None) != (sum_out is None):
-        raise ValueError("residual and sum_out come together")
-    pq, ps = _cast(q_out, "q_out", M, K, q_state, history_len)
-    _check(lib().fp8_layernorm_fwd(
-        px, None if residual is None else _mat(residual, "residual", M, K, dt), BF16 if dt is T.bfloat16 else F32,
-        _vec(gamma, "gamma", K), None if beta is None else _vec(beta, "beta", K), eps, M, K,
-        None if sum_out is None else _mat(sum_out, "sum_out", M, K, dt),
-        None if y is None and pq is not None else _mat(y, "y", M, K, dt), None if mu is None else _vec(mu, "mu", M),
-        None if rstd is None else _vec(rstd, "rstd", M), pq, q_format, ps, history_len, _stream(stream)))
+    pr = psum = py = pmu = prs = pq = ps = None
+    if residual is not None or sum_out is not None:
+        if residual is None or sum_out is None:
+            raise ValueError("residual and sum_out come together")
+        pr, psum = _mat(residual, "residual", M, K, dt), _mat(sum_out, "sum_out", M, K, dt)
+    if q_out is not None:
+        pq, ps = _cast(q_out, "q_out", M, K, q_state, history_len)
+    if y is not None or pq is None:
+        py = _mat(y, "y", M, K, dt)
+    if mu is not None:
+        pmu = _vec(mu, "mu", M)
+    if rstd is not None:
+        prs = _vec(rstd, "rstd", M)
+    r = (_lib or lib()).fp8_layernorm_fwd(
+        px, pr, BF16 if dt is T.bfloat16 else F32, _vec(gamma, "gamma", K),
+        None if beta is None else _vec(beta, "beta", K), eps, M, K, psum, py, pmu, prs, pq, q_format, ps, history_len,
+        _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
 
 
 def fp8_layernorm_bwd_workspace_bytes(M: int, K: int) -> int:
@@ -460,25 +471,50 @@ def fp8_gemm_act_workspace_bytes(M: int, N: int, K: int) -> int:
     return lib().fp8_gemm_act_workspace_bytes(M, N, K)
 
 
+def _operands(A, a_scale, B, b_scale, names) -> tuple:
+    """(pA, M, K, p a_scale, pB, rows of B, columns of B, p b_scale) of two matrices of codes"""
+    u8, f32 = _torch.uint8, _torch.float32
+    if (A is not None and B is not None and A.dtype is u8 and B.dtype is u8 and A.dim() == 2 and B.dim() == 2 and
+            A.is_contiguous() and B.is_contiguous() and a_scale is not None and a_scale.dtype is f32 and
+            b_scale is not None and b_scale.dtype is f32 and a_scale.numel() >= 1 and b_scale.numel() >= 1):
+        M, K = A.shape
+        N, kb = B.shape
+        return A.data_ptr(), M, K, a_scale.data_ptr(), B.data_ptr(), N, kb, b_scale.data_ptr()
+    pa, M, K = _sized(A, names[0], (u8,))
+    pb, N, kb = _sized(B, names[1], (u8,))
+    return pa, M, K, _vec(a_scale, "a_scale", 1), pb, N, kb, _vec(b_scale, "b_scale", 1)
+
+
 def fp8_gemm_act(A, a_format: int, a_scale, B, b_format: int, b_scale, act: int, D=None, bias=None, residual=None,
                  z_out=None, q_out=None, q_format: int = E4M3, q_state=None, history_len: int = 0, workspace=None,
                  stream=None) -> None:
     """y = act(z) + residual, z = A B^T sA sB + bias, into D (bf16 / fp32) and / or FP8 codes q_out; z into z_out."""
     T = _t()
-    u8 = (T.uint8,)
-    pa, M, K = _sized(A, "A", u8)
-    pb, N, kb = _sized(B, "B", u8)
+    pa, M, K, sa, pb, N, kb, sb = _operands(A, a_scale, B, b_scale, ("A", "B"))
     if kb != K:
         raise ValueError(f"B: shape {tuple(B.shape)}, expected {(N, K)}")
-    pq, ps = _cast(q_out, "q_out", M, N, q_state, history_len)
-    _check(lib().fp8_gemm_act(
-        pa, a_format, _vec(a_scale, "a_scale", 1), pb, b_format, _vec(b_scale, "b_scale", 1), M, N, K, act,
-        None if bias is None else _vec(bias, "bias", N),
-        None if residual is None else _mat(residual, "residual", M, N, residual.dtype),
-        BF16 if residual is None else _dtype_code(residual),
-        None if z_out is None else _mat(z_out, "z_out", M, N, T.bfloat16),
-        None if D is None else _mat(D, "D", M, N, D.dtype), BF16 if D is None else _dtype_code(D), pq, q_format, ps,
-        history_len, *_ws(workspace), _stream(stream)))
+    pd = pr = pz = pq = ps = pbias = pw = None
+    rdt = ddt = BF16
+    nw = 0
+    if D is not None:
+        ddt = BF16 if D.dtype is T.bfloat16 else _dtype_code(D)
+        pd = _mat(D, "D", M, N, D.dtype)
+    if residual is not None:
+        rdt = BF16 if residual.dtype is T.bfloat16 else _dtype_code(residual)
+        pr = _mat(residual, "residual", M, N, residual.dtype)
+    if bias is not None:
+        pbias = _vec(bias, "bias", N)
+    if z_out is not None:
+        pz = _mat(z_out, "z_out", M, N, T.bfloat16)
+    if q_out is not None:
+        pq, ps = _cast(q_out, "q_out", M, N, q_state, history_len)
+    if workspace is not None:
+        pw, nw = _ws(workspace)
+    r = (_lib or lib()).fp8_gemm_act(pa, a_format, sa, pb, b_format, sb, M, N, K, act, pbias, pr, rdt, pz, pd, ddt, pq,
+                                     q_format, ps, history_len, pw, nw,
+                                     _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
 
 
 def fp8_act_bwd_workspace_bytes(M: int, N: int) -> int:
@@ -506,18 +542,24 @@ def fp8_glu_fwd(A, a_format: int, a_scale, W, w_format: int, w_scale, act: int, 
     """h = act(g) u with [g | u] = A W^T sA sW, W = [W_gate; W_up]: into h_out (bf16) and / or FP8 codes q_out;
     [g | u] into gu_out."""
     T = _t()
-    u8 = (T.uint8,)
-    pa, M, K = _sized(A, "A", u8)
-    pw, F2, kw = _sized(W, "W", u8)
+    pa, M, K, sa, pb, F2, kw, sw = _operands(A, a_scale, W, w_scale, ("A", "W"))
     F = F2 // 2
     if kw != K or F2 != 2 * F:
         raise ValueError(f"W: shape {tuple(W.shape)}, expected {(2 * F, K)}")
-    pq, ps = _cast(q_out, "q_out", M, F, q_state, history_len)
-    _check(lib().fp8_glu_fwd(
-        pa, a_format, _vec(a_scale, "a_scale", 1), pw, w_format, _vec(w_scale, "w_scale", 1), M, F, K, act,
-        None if gu_out is None else _mat(gu_out, "gu_out", M, F2, T.bfloat16),
-        None if h_out is None else _mat(h_out, "h_out", M, F, T.bfloat16), pq, q_format, ps, history_len,
-        *_ws(workspace), _stream(stream)))
+    ph = pg = pq = ps = pw = None
+    nw = 0
+    if gu_out is not None:
+        pg = _mat(gu_out, "gu_out", M, F2, T.bfloat16)
+    if h_out is not None:
+        ph = _mat(h_out, "h_out", M, F, T.bfloat16)
+    if q_out is not None:
+        pq, ps = _cast(q_out, "q_out", M, F, q_state, history_len)
+    if workspace is not None:
+        pw, nw = _ws(workspace)
+    r = (_lib or lib()).fp8_glu_fwd(pa, a_format, sa, pb, w_format, sw, M, F, K, act, pg, ph, pq, q_format, ps,
+                                    history_len, pw, nw, _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
 
 
 def fp8_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scale, gu, act: int, q_dgu, q_format: int,
@@ -525,17 +567,15 @@ def fp8_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scale, gu, ac
     """codes of [dg | du] from the block's output gradient dY [M][K], the down projection Wd [K][F] and the
     forward's [g | u]."""
     T = _t()
-    u8 = (T.uint8,)
-    py, M, K = _sized(dY, "dY", u8)
-    pw, kw, F = _sized(Wd, "Wd", u8)
+    pa, M, K, sa, pb, kw, F, sw = _operands(dY, dy_scale, Wd, w_scale, ("dY", "Wd"))
     if kw != K:
         raise ValueError(f"Wd: shape {tuple(Wd.shape)}, expected {(K, F)}")
     if q_dgu is None:
         raise ValueError("q_dgu is required")
     pg = _mat(gu, "gu", M, 2 * F, T.bfloat16)
     pq, ps = _cast(q_dgu, "q_dgu", M, 2 * F, q_state, history_len)
-    _check(lib().fp8_glu_bwd(py, dy_format, _vec(dy_scale, "dy_scale", 1), pw, w_format, _vec(w_scale, "w_scale", 1),
-                             M, F, K, pg, act, pq, q_format, ps, history_len, _stream(stream)))
+    _check(lib().fp8_glu_bwd(pa, dy_format, sa, pb, w_format, sw, M, F, K, pg, act, pq, q_format, ps, history_len,
+                             _stream(stream)))
 
 
 def fp8_selftest_wait_timeout(limit_us: int, waited_out, stream=None) -> None:
