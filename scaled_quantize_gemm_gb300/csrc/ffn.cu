@@ -51,10 +51,15 @@ struct FfnParams {
 };
 
 constexpr int kFfnStages = 6;
-constexpr int kFfnEpiWarps = 8;                  // two per TMEM lane quarter
-constexpr int kFfnThreads = 32 * (2 + kFfnEpiWarps);
+// Epilogue warps: two per TMEM lane quarter; four for glu_bwd, whose epilogue is
+// the longest (an exponential and a reciprocal an element, two outputs) and has
+// more latency to cover than two warps of an SM quarter do.
+template <int KIND>
+constexpr int kFfnEpiWarps = KIND == kEpiGluBwd ? 16 : 8;
+template <int KIND>
+constexpr int kFfnThreads = 32 * (2 + kFfnEpiWarps<KIND>);
 constexpr int kFfnBN = 256, kFfnBH = 128;
-using FfnSmem = Smem<kFfnBH, kFfnStages, 2, 4 * kFfnEpiWarps>;   // per epilogue warp: four 1 KB staging boxes
+using FfnSmem = Smem<kFfnBH, kFfnStages, 2, 32>;      // 32 staging boxes of 1 KB, shared out among the epilogue warps
 
 // ------------------------------------------------------------------ epilogue pieces
 __device__ __forceinline__ uint32_t pack_bf16(float2 v)
@@ -82,18 +87,20 @@ __device__ __forceinline__ void max32(uint32_t& amax, const float2 (&v)[16], int
     }
     amax = max(amax, __float_as_uint(m) & keep);       // not negative: ordered as integers, a NaN above all
 }
-// 32 codes of one row
-__device__ __forceinline__ void codes32(uint32_t (&w)[8], const float2 (&v)[16], float m, int fmt)
+// 16 and 32 codes of one row
+__device__ __forceinline__ uint4 codes16(const float2* v, float m, int fmt)
 {
+    uint32_t w[4];
     auto all = [&](auto cvt) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             const float2 a = __fmul2_rn(v[2 * j], f2(m)), b = __fmul2_rn(v[2 * j + 1], f2(m));
             w[j] = cvt(a.x, a.y) | (cvt(b.x, b.y) << 16);
         }
     };
     if (fmt == kE4M3) all([](float a, float b) { return cvt_e4m3x2(a, b); });
     else all([](float a, float b) { return cvt_e5m2x2(a, b); });
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void store32_bf16(__nv_bfloat16* d, int left, const float2 (&v)[16])
 {
@@ -105,10 +112,8 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* d, int left, const f
 }
 __device__ __forceinline__ void store32_codes(uint8_t* q, int left, const float2 (&v)[16], float m, int fmt)
 {
-    uint32_t w[8];
-    codes32(w, v, m, fmt);
-    if (16 <= left) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (32 <= left) *reinterpret_cast<uint4*>(q + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    if (16 <= left) *reinterpret_cast<uint4*>(q) = codes16(v, m, fmt);
+    if (32 <= left) *reinterpret_cast<uint4*>(q + 16) = codes16(v + 8, m, fmt);
 }
 
 // Staged bulk stores of one epilogue warp: 4 KB, four boxes of 32 rows x 32
@@ -167,11 +172,10 @@ struct Stager {
     __device__ __forceinline__ void codes(const CUtensorMap* m, const float2 (&v)[16], float mult, int fmt, int col,
                                           int row0, int left)
     {
-        uint32_t w[8];
-        codes32(w, v, mult, fmt);
+        const uint4 lo = codes16(v, mult, fmt), hi = codes16(v + 8, mult, fmt);
         uint8_t* p = take(1);
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(p) = lo;
+        *reinterpret_cast<uint4*>(p + 16) = hi;
         send(m, 1, 32, col, row0, left);
     }
 };
@@ -217,7 +221,7 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 }
 // ------------------------------------------------------------------ kernel
 template <int KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1)
     k_ffn_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FfnParams p,
                uint32_t idesc, TileSched sched, const __grid_constant__ CUtensorMap tmO0,
                const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2)
@@ -247,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&afull[b], 1);
-            mbar_init(&aempty[b], 2 * kFfnEpiWarps);
+            mbar_init(&aempty[b], 2 * kFfnEpiWarps<KIND>);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -374,18 +378,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         }
     } else {
         const int quarter = warp & 3;       // the TMEM lane quarter this warp may read
-        const int part = (warp - 2) >> 2;   // column half
+        const int part = (warp - 2) >> 2;   // share of the columns
+        constexpr int PARTS = kFfnEpiWarps<KIND> / 4, BOXES = 32 / kFfnEpiWarps<KIND>;
         const float scale = __ldg(p.sA) * __ldg(p.sB);
         const float qm = p.Q ? p.qstate[p.qH] : 1.0f;
         uint32_t amax = 0;
         const uint32_t aempty0 = cluster_map(smem_addr(aempty), 0);
-        Stager out{smem + L::STG_OFF + (warp - 2) * 4 * kStageBytes, lane, 0};
+        Stager out{smem + L::STG_OFF + (warp - 2) * BOXES * kStageBytes, lane, 0};
         // columns of a tile in this warp's share; what its epilogue reads
         // beside the sums (the residual, or g and u) is fetched one chunk of
-        // 32 columns ahead, the first chunk's before the tile's sums are done
+        // 32 columns (16 of g and u) ahead, the first chunk's before the tile's
+        // sums are done
         constexpr int TN = KIND == kEpiGlu ? BH : BN;
-        const int c_begin = part * (TN / 2), c_end = c_begin + TN / 2;
-        uint4 pre[8];
+        const int c_begin = part * (TN / PARTS), c_end = c_begin + TN / PARTS;
+        uint4 pre[KIND == kEpiGluBwd ? 4 : 8];
         auto fetch = [&](int row, int col) {
             const int left = row < p.M ? min(p.N - col, 32) : 0;
             if constexpr (KIND == kEpiAct) {
@@ -393,9 +399,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                 if (p.res_f32) fetch_row<8>(pre, static_cast<const float*>(p.res) + (int64_t)row * p.N + col, 4 * left);
                 else fetch_row<4>(pre, static_cast<const __nv_bfloat16*>(p.res) + (int64_t)row * p.N + col, 2 * left);
             } else if constexpr (KIND == kEpiGluBwd) {
+                // 16 columns of g, then of u
                 const __nv_bfloat16* s = p.gu + (int64_t)row * 2 * p.N + col;
-                fetch_row<4>(pre, s, 2 * left);
-                fetch_row<4>(pre + 4, s + p.N, 2 * left);
+                fetch_row<2>(pre, s, 2 * left);
+                fetch_row<2>(pre + 2, s + p.N, 2 * left);
             }
         };
         int lt = 0;
@@ -448,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                         if (p.Q) store32_codes(p.Q + (int64_t)row * p.N + col, left, v, qm, p.qfmt);
                     }
                     __syncwarp();
-                } else {
+                } else if constexpr (KIND == kEpiAct) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
                     tmem_ld_wait();
@@ -456,57 +463,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                     for (int j = 0; j < 16; ++j)
                         v[j] = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
                     out.next_chunk();
-                    if constexpr (KIND == kEpiAct) {
-                        if (p.bias) {
-                            const int from = (c - c_begin) / 4;       // the lane that holds column c
+                    if (p.bias) {
+                        const int from = (c - c_begin) / 4;       // the lane that holds column c
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                const int s = from + j / 2;
-                                v[j] = __fadd2_rn(v[j], make_float2(__shfl_sync(0xFFFFFFFFu, bias.x, s),
-                                                                    __shfl_sync(0xFFFFFFFFu, bias.y, s)));
-                                v[j + 1] = __fadd2_rn(v[j + 1], make_float2(__shfl_sync(0xFFFFFFFFu, bias.z, s),
-                                                                            __shfl_sync(0xFFFFFFFFu, bias.w, s)));
-                            }
+                        for (int j = 0; j < 16; j += 2) {
+                            const int s = from + j / 2;
+                            v[j] = __fadd2_rn(v[j], make_float2(__shfl_sync(0xFFFFFFFFu, bias.x, s),
+                                                                __shfl_sync(0xFFFFFFFFu, bias.y, s)));
+                            v[j + 1] = __fadd2_rn(v[j + 1], make_float2(__shfl_sync(0xFFFFFFFFu, bias.z, s),
+                                                                        __shfl_sync(0xFFFFFFFFu, bias.w, s)));
                         }
-                        if (p.Z) out.bf16(&tmO0, v, col, row0, left);
+                    }
+                    if (p.Z) out.bf16(&tmO0, v, col, row0, left);
+                    act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = act_f2<decltype(tag)::act>(v[j]);
+                    });
+                    if (p.res) {
+                        if (p.res_f32) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_f32(pre, j));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_bf16(pre, j));
+                        }
+                        if (c + 32 < c_end) fetch(row, col + 32);
+                    }
+                    if (p.D) {
+                        if (p.d_f32) out.f32(&tmO1, v, col, row0, left);
+                        else out.bf16(&tmO1, v, col, row0, left);
+                    }
+                    if (p.Q) {
+                        max32(amax, v, left, keep);
+                        out.codes(&tmO2, v, qm, p.qfmt, col, row0, left);
+                    }
+                } else {
+                    // two halves of 16 columns, each 16 bytes of the two boxes' rows
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(taddr + (uint32_t)(c + 16 * h), r);
+                        tmem_ld_wait();
+                        float2 dg[8], du[8];
                         act_dispatch(p.act, [&](auto tag) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = act_f2<decltype(tag)::act>(v[j]);
-                        });
-                        if (p.res) {
-                            if (p.res_f32) {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_f32(pre, j));
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_bf16(pre, j));
-                            }
-                            if (c + 32 < c_end) fetch(row, col + 32);
-                        }
-                        if (p.D) {
-                            if (p.d_f32) out.f32(&tmO1, v, col, row0, left);
-                            else out.bf16(&tmO1, v, col, row0, left);
-                        }
-                        if (p.Q) {
-                            max32(amax, v, left, keep);
-                            out.codes(&tmO2, v, qm, p.qfmt, col, row0, left);
-                        }
-                    } else {
-                        float2 g[16];
-                        act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 dh = __fmul2_rn(
+                                    make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
                                 float2 f, d;
                                 act_fd2<decltype(tag)::act>(raw_bf16(pre, j), f, d);
-                                g[j] = __fmul2_rn(__fmul2_rn(v[j], raw_bf16(pre + 4, j)), d);
-                                v[j] = __fmul2_rn(v[j], f);
+                                dg[j] = __fmul2_rn(__fmul2_rn(dh, raw_bf16(pre + 2, j)), d);
+                                du[j] = __fmul2_rn(dh, f);
                             }
                         });
-                        if (c + 32 < c_end) fetch(row, col + 32);
-                        max32(amax, g, left, keep);
-                        max32(amax, v, left, keep);
-                        out.codes(&tmO0, g, qm, p.qfmt, col, row0, left);
-                        out.codes(&tmO1, v, qm, p.qfmt, col, row0, left);
+                        const int cn = c + 16 * (h + 1);
+                        if (cn < c_end) fetch(row, nb * TN + cn);
+                        float m = 0.0f;
+                        if (left > 16 * h) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                m = max3_nan(m, fabsf(dg[j].x), fabsf(dg[j].y));
+                                m = max3_nan(m, fabsf(du[j].x), fabsf(du[j].y));
+                            }
+                        }
+                        amax = max(amax, __float_as_uint(m) & keep);
+                        const uint4 qg = codes16(dg, qm, p.qfmt), qu = codes16(du, qm, p.qfmt);
+                        if (h == 0) out.reset();        // the previous chunk's boxes have been read
+                        uint8_t* q = out.buf + 32 * lane + 16 * h;
+                        *reinterpret_cast<uint4*>(q) = qg;
+                        *reinterpret_cast<uint4*>(q + kStageBytes) = qu;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bulk_store_2d(&tmO0, col, row0, out.buf);
+                        bulk_store_2d(&tmO1, col, row0, out.buf + kStageBytes);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
             }
@@ -1013,7 +1045,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 // Co-resident CTA pairs of a kernel on the current device, queried once per
 // kernel and device (the entries are atomics: concurrent first calls store
 // the same value).
-static cudaError_t ffn_clusters(const void* kern, int kind, int* clusters)
+static cudaError_t ffn_clusters(const void* kern, int kind, int threads, int* clusters)
 {
     static std::atomic<int> cache[3][64];
     int dev = 0;
@@ -1030,7 +1062,7 @@ static cudaError_t ffn_clusters(const void* kern, int kind, int* clusters)
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(kFfnThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = FfnSmem::BYTES;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1176,7 +1208,8 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     static const Kern kerns[3] = {k_ffn_pair<kEpiAct>, k_ffn_pair<kEpiGlu>, k_ffn_pair<kEpiGluBwd>};
     Kern kern = kerns[a.kind];
     int clusters = 0;
-    e = ffn_clusters(reinterpret_cast<const void*>(kern), a.kind, &clusters);
+    const int threads = bwd ? kFfnThreads<kEpiGluBwd> : kFfnThreads<kEpiAct>;
+    e = ffn_clusters(reinterpret_cast<const void*>(kern), a.kind, threads, &clusters);
     if (e != cudaSuccess) {
         *why = "cluster occupancy query failed";
         return e;
@@ -1210,7 +1243,7 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
         *why = "cuTensorMapEncodeTiled failed (output)";
         return cudaErrorInvalidValue;
     }
-    launch_k(kern, grid, kFfnThreads, FfnSmem::BYTES, st, ta, tb, p, idesc, sched, o[0], o[1], o[2]);
+    launch_k(kern, grid, threads, FfnSmem::BYTES, st, ta, tb, p, idesc, sched, o[0], o[1], o[2]);
     return cudaGetLastError();
 }
 
