@@ -50,7 +50,13 @@ struct FfnParams {
     int* err;
 };
 
-constexpr int kFfnStages = 6;
+// Ring stages of 32 KB.  Where the epilogue reads rows beside the sums, the
+// lines in flight need room in the L1 that shares the SM's memory with the ring:
+// five stages, not six (2000 x 1616 -> 5440 with an fp32 residual 40.0 -> 36.8 us;
+// gated backward of 1056 tokens, 928 -> 7776, 109 -> 106).  Without such reads
+// six are as fast or faster (256 tokens, 4096 -> 2 x 14336: 29.9 against 30.9).
+template <int KIND>
+constexpr int kFfnStages = KIND == kEpiGlu ? 6 : 5;
 // Epilogue warps: two per TMEM lane quarter; four for glu_bwd, whose epilogue is
 // the longest (an exponential and a reciprocal an element, two outputs) and has
 // more latency to cover than two warps of an SM quarter do.
@@ -59,7 +65,8 @@ constexpr int kFfnEpiWarps = KIND == kEpiGluBwd ? 16 : 8;
 template <int KIND>
 constexpr int kFfnThreads = 32 * (2 + kFfnEpiWarps<KIND>);
 constexpr int kFfnBN = 256, kFfnBH = 128;
-using FfnSmem = Smem<kFfnBH, kFfnStages, 2, 32>;      // 32 staging boxes of 1 KB, shared out among the epilogue warps
+template <int KIND>
+using FfnSmem = Smem<kFfnBH, kFfnStages<KIND>, 2, 32>;      // 32 staging boxes of 1 KB, shared out among the epilogue warps
 
 // ------------------------------------------------------------------ epilogue pieces
 __device__ __forceinline__ uint32_t pack_bf16(float2 v)
@@ -219,16 +226,24 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
     return old;
 }
-// ------------------------------------------------------------------ kernel
+// ------------------------------------------------------------------ tiles of 256 x 256
+// Bound by the tensor cores where K is long (ncu, 2048 tokens, K 4096: tensor
+// pipe active 85 % glu_fwd, 73 % gemm_act with gelu, z and codes, 68 % glu_bwd),
+// by the epilogue where it is short: an accumulator's 128 x 256 values a CTA take
+// about 8 us through eight warps (gelu, z and codes), which the MMAs of the next
+// tile cover from K of about 3000 on.
+// One GB300, us: glu_fwd 16384 x 4096 -> 2 x 14336 with g, u and codes 1075
+// (3580 TFLOP/s); gemm_act 16384 x 4096 -> 14336 with bias, gelu_tanh, z and codes
+// 580-600; glu_bwd 2048 x 4096 -> 14336 86.
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1)
     k_ffn_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FfnParams p,
                uint32_t idesc, TileSched sched, const __grid_constant__ CUtensorMap tmO0,
                const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2)
 {
-    constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = kFfnStages;
+    constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = kFfnStages<KIND>;
     constexpr bool b_mn = KIND == kEpiGluBwd;          // Wd [K][F]: MN-major
-    using L = FfnSmem;
+    using L = FfnSmem<KIND>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -1045,7 +1060,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 // Co-resident CTA pairs of a kernel on the current device, queried once per
 // kernel and device (the entries are atomics: concurrent first calls store
 // the same value).
-static cudaError_t ffn_clusters(const void* kern, int kind, int threads, int* clusters)
+static cudaError_t ffn_clusters(const void* kern, int kind, int threads, int smem, int* clusters)
 {
     static std::atomic<int> cache[3][64];
     int dev = 0;
@@ -1058,12 +1073,12 @@ static cudaError_t ffn_clusters(const void* kern, int kind, int threads, int* cl
             return cudaSuccess;
         }
     }
-    e = smem_attr_once(kern, FfnSmem::BYTES);
+    e = smem_attr_once(kern, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = FfnSmem::BYTES;
+    cfg.dynamicSmemBytes = (size_t)smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1208,8 +1223,10 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     static const Kern kerns[3] = {k_ffn_pair<kEpiAct>, k_ffn_pair<kEpiGlu>, k_ffn_pair<kEpiGluBwd>};
     Kern kern = kerns[a.kind];
     int clusters = 0;
+    static_assert((int)FfnSmem<kEpiAct>::BYTES == (int)FfnSmem<kEpiGluBwd>::BYTES, "one size for both");
     const int threads = bwd ? kFfnThreads<kEpiGluBwd> : kFfnThreads<kEpiAct>;
-    e = ffn_clusters(reinterpret_cast<const void*>(kern), a.kind, threads, &clusters);
+    const int smem = glu ? FfnSmem<kEpiGlu>::BYTES : FfnSmem<kEpiAct>::BYTES;
+    e = ffn_clusters(reinterpret_cast<const void*>(kern), a.kind, threads, smem, &clusters);
     if (e != cudaSuccess) {
         *why = "cluster occupancy query failed";
         return e;
@@ -1243,7 +1260,7 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
         *why = "cuTensorMapEncodeTiled failed (output)";
         return cudaErrorInvalidValue;
     }
-    launch_k(kern, grid, threads, FfnSmem::BYTES, st, ta, tb, p, idesc, sched, o[0], o[1], o[2]);
+    launch_k(kern, grid, threads, (size_t)smem, st, ta, tb, p, idesc, sched, o[0], o[1], o[2]);
     return cudaGetLastError();
 }
 
