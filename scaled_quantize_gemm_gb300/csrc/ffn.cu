@@ -9,7 +9,8 @@
 //   glu_bwd   dh = (dY Wd) s; dg = dh u act'(g), du = dh act(g) from the
 //             forward's [g | u]; the codes of [dg | du] under one delayed state
 //
-// All three run on CTA pairs (tcgen05 .cta_group::2, M = 256, N = 256): the
+// All three run on CTA pairs (tcgen05 .cta_group::2, M = 256, N = 256; products
+// of few rows or few tiles on k_ffn_rows, further down): the
 // even CTA issues the MMAs over both CTAs' shared memory and each CTA's TMEM
 // holds its 128 rows, two accumulators of 256 columns.  In glu_fwd the even
 // CTA loads 128 rows of W_gate and the odd one the same 128 rows of W_up, so

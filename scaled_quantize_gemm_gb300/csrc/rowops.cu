@@ -267,7 +267,11 @@ struct Pack {
 template <int VEC>
 __device__ __forceinline__ void load_param(const float* __restrict__ p, int c, float (&v)[VEC])
 {
-    if constexpr (VEC % 4 == 0) {
+    if constexpr (VEC == 2) {
+        const float2 w = __ldg(reinterpret_cast<const float2*>(p + c));
+        v[0] = w.x;
+        v[1] = w.y;
+    } else if constexpr (VEC % 4 == 0) {
 #pragma unroll
         for (int j = 0; j < VEC; j += 4) {
             const float4 w = __ldg(reinterpret_cast<const float4*>(p + c + j));
@@ -467,6 +471,10 @@ __global__ void __launch_bounds__(MAXT, MINB)
 // (rows of up to 8192; longer ones read the ring again).  Rows that move one
 // element at a time (odd bf16 or fp32 lengths) take 8 columns (4096 x 1001
 // bf16: 45 us against 75 with 16, before their copies were asynchronous).
+__device__ __forceinline__ void cp_async8(void* s, const void* g)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(s)), "l"(g) : "memory");
+}
 __device__ __forceinline__ void cp_async4(void* s, const void* g)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s)), "l"(g) : "memory");
@@ -517,6 +525,8 @@ __global__ void __launch_bounds__(MAXT, MINB)
                     auto copy = [&](int arr, const T* src) {
                         if constexpr (sizeof(Raw) == 16) {
                             cp_async16(slot(st, arr, i), src + at);
+                        } else if constexpr (sizeof(Raw) == 8) {
+                            cp_async8(slot(st, arr, i), src + at);
                         } else if constexpr (sizeof(Raw) == 4) {
                             cp_async4(slot(st, arr, i), src + at);
                         } else {
@@ -847,9 +857,10 @@ cudaError_t ln_fwd_rows(const LnArgs& a, cudaStream_t st, int sms)
 template <typename T, bool CODES>
 cudaError_t ln_fwd_vec(const LnArgs& a, cudaStream_t st, int sms)
 {
-    constexpr int WIDE = 16 / (int)sizeof(T), NARROW = WIDE / 4;     // 16 and 4 bytes
+    constexpr int WIDE = 16 / (int)sizeof(T);        // the widest vector of 16, 8 or 4 bytes that divides a row
     if (a.K % WIDE == 0) return ln_fwd_rows<T, WIDE, CODES>(a, st, sms);
-    if (a.K % NARROW == 0) return ln_fwd_rows<T, NARROW, CODES>(a, st, sms);
+    if (a.K % (WIDE / 2) == 0) return ln_fwd_rows<T, WIDE / 2, CODES>(a, st, sms);
+    if (a.K % (WIDE / 4) == 0) return ln_fwd_rows<T, WIDE / 4, CODES>(a, st, sms);
     return ln_fwd_rows<T, 1, CODES>(a, st, sms);
 }
 
@@ -883,7 +894,9 @@ cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int group, in
     return cudaGetLastError();
 }
 
-// Three stages of the ring where they fit, else two or one.  Short rows share a
+// Three stages of the ring where they fit, else two or one.  Rows take the widest
+// vector of 16, 8 or 4 bytes that divides them (7400 x 1862 fp32: 45 us with 8
+// bytes, 65 with 4).  Short rows share a
 // CTA of MAXT threads where there are rows for all of its groups on every SM.
 template <typename T, int VEC, int C, int MAXT, int MINB, bool KEEP>
 cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
@@ -897,7 +910,9 @@ cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
     if constexpr (MAXT <= 256) {
         if (groups > 1) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, true>(a, st, sms, group, groups, 3 * stage, parts);
     }
-    if (3 * stage <= kLnRoom) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, 3 * stage, parts);
+    // (two CTAs with two stages each before one with three: 2048 x 4096 fp32 35.1 -> 27.5 us)
+    const bool two = MINB >= 2 && 6 * stage > kLnRoom && 4 * stage <= kLnRoom;
+    if (3 * stage <= kLnRoom && !two) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, 3 * stage, parts);
     if (2 * stage <= kLnRoom) return ln_bwd_rows<T, VEC, C, 2, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, 2 * stage, parts);
     return ln_bwd_rows<T, VEC, C, 1, MAXT, MINB, KEEP, false>(a, st, sms, group, 1, stage, parts);
 }
@@ -919,15 +934,16 @@ cudaError_t ln_bwd_vec(const LnArgs& a, cudaStream_t st, int sms, int* parts)
 template <typename T>
 cudaError_t ln_bwd(const LnArgs& a, cudaStream_t st, int sms)
 {
-    constexpr int WIDE = 16 / (int)sizeof(T), NARROW = WIDE / 4;
+    constexpr int WIDE = 16 / (int)sizeof(T);
     float* part = static_cast<float*>(a.workspace);
     int parts = 0;
     if (a.M > 0) {
         cudaError_t e = cudaSuccess;
         if (a.K <= 1024 * kLnCols) {
-            e = a.K % WIDE == 0     ? ln_bwd_vec<T, WIDE>(a, st, sms, &parts)
-                : a.K % NARROW == 0 ? ln_bwd_vec<T, NARROW>(a, st, sms, &parts)
-                                    : ln_bwd_vec<T, 1>(a, st, sms, &parts);
+            e = a.K % WIDE == 0         ? ln_bwd_vec<T, WIDE>(a, st, sms, &parts)
+                : a.K % (WIDE / 2) == 0 ? ln_bwd_vec<T, WIDE / 2>(a, st, sms, &parts)
+                : a.K % (WIDE / 4) == 0 ? ln_bwd_vec<T, WIDE / 4>(a, st, sms, &parts)
+                                        : ln_bwd_vec<T, 1>(a, st, sms, &parts);
             if (e != cudaSuccess) return e;
         } else {
             const int64_t cap = (int64_t)sms * 8;

@@ -18,7 +18,7 @@ DEV = "cuda"
 EPS = 1e-5
 DTYPES = [torch.bfloat16, torch.float32]
 SIZES = [(1, 1), (1, 4096), (3, 7), (5, 16), (17, 1000), (33, 1535), (2, 8192), (64, 12288), (7, 16384), (3, 20000),
-         (1500, 264), (700, 2048), (9, 12000), (4, 65552)]
+         (1500, 264), (700, 2048), (9, 12000), (4, 65552), (400, 1862), (130, 1004), (6, 9998), (20, 4094)]
 
 
 def _fwd64(s, gamma, beta):
