@@ -560,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(aempty0 + 8u * b);
+            if (lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
         }
         stage_store_drain(lane);
         if (p.Q) {

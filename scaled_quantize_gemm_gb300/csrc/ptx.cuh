@@ -336,6 +336,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_addr)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
+// The same without release semantics, for a barrier that hands over tensor
+// memory only: tcgen05.wait::ld has completed the reads and
+// tcgen05.fence::before_thread_sync orders them before the arrival, so the
+// thread's global stores need not be waited for (a release at cluster scope
+// puts a memory barrier behind them).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cl_addr)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
