@@ -325,6 +325,15 @@ __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t cl_addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cl_addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cl_addr)
 {
     uint32_t v;
