@@ -460,25 +460,20 @@ __global__ void __launch_bounds__(MAXT, MINB)
 // of every row, so dgamma and dbeta accumulate in its registers; a CTA holds
 // one group, or several for short rows, whose sums meet in shared memory at the
 // end, and writes one partial row to the workspace.  x, dy and dres of the next
-// STAGES - 1 rows are in flight (cp.async) while a row is worked on: a thread
-// copies exactly the elements that it will read, so the ring needs no barrier
-// and no wait on another thread, and a row costs one barrier of its group, for
-// its two sums.
+// STAGES - 1 rows are in flight while a row is worked on, and a row costs one
+// barrier of its group, for its two sums.  Rows of whole 16-byte vectors: a
+// thread copies (cp.async) exactly the elements that it will read, so the ring
+// needs no barrier.  Other rows (BULK): one thread copies each whole, with the
+// 16-byte blocks it begins and ends in, and a stage is free again after the
+// next row's barrier (16-byte copies whatever the rows' alignment; one element
+// or vector at a time by cp.async, and 8 columns a thread: 2051 x 1535 fp32 17.0
+// -> 12.8 us, 3000 x 5001 bf16 80.5 -> 36.8, 1198 x 9849 bf16 148 -> 42, 3000 x 5002
+// 39.7 -> 31.8).
 // The time goes with the instructions a row costs beside its elements (ncu at
 // 16384 x 4096 with 8 columns a thread: 40 instructions an element, issue slots
 // 59 % busy, DRAM 53 %), so a thread takes 16 columns: 119 -> 93 us.  KEEP holds
 // the row's normalised values and dy gamma in registers across the barrier
-// (rows of up to 8192; longer ones read the ring again).  Rows that move one
-// element at a time (odd bf16 or fp32 lengths) take 8 columns (4096 x 1001
-// bf16: 45 us against 75 with 16, before their copies were asynchronous).
-__device__ __forceinline__ void cp_async8(void* s, const void* g)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(s)), "l"(g) : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* s, const void* g)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(s)), "l"(g) : "memory");
-}
+// (rows of up to 12288; longer ones read the ring again).
 template <int N>
 __device__ __forceinline__ void cp_async_wait()
 {
@@ -489,69 +484,102 @@ __device__ __forceinline__ void bar_group(int id, int threads)
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 constexpr int kLnGroups = 8;        // groups of a CTA, at most
+// room of a row in the ring with the 16-byte blocks it begins and ends in
+__host__ __device__ constexpr int ln_row_bytes(int K, int size) { return (K * size + 30) & ~15; }
 
 template <typename T, int VEC, int C, int STAGES, int MAXT, int MINB, bool KEEP, bool GROUPED>
 __global__ void __launch_bounds__(MAXT, MINB)
     k_ln_bwd(const T* __restrict__ dy, const T* __restrict__ x, const T* __restrict__ dres,
              const float* __restrict__ gamma, const float* __restrict__ mu, const float* __restrict__ rstd, int64_t R,
-             int K, int group_threads, T* __restrict__ dx, float* __restrict__ part)
+             int K, int group_threads, T* __restrict__ dx, float* __restrict__ part, int* err)
 {
     constexpr int NV = C / VEC;
+    constexpr bool BULK = VEC * sizeof(T) < 16;
     using P = Pack<T, VEC>;
     using Raw = typename P::Raw;
     extern __shared__ __align__(16) uint8_t ln_ring[];
     constexpr int RG = GROUPED ? kLnGroups : 1;
     __shared__ float red[RG][2][2][32];
+    __shared__ uint64_t full[RG][STAGES];               // BULK: a stage's rows have arrived
     const int nt = GROUPED ? group_threads : blockDim.x, g = GROUPED ? threadIdx.x / nt : 0, t = threadIdx.x - g * nt;
     const int groups = GROUPED ? blockDim.x / nt : 1, warp = t >> 5, warps = nt >> 5;
     const int span = pow2_span(warps);
     for (int i = threadIdx.x; i < RG * 128; i += blockDim.x) (&red[0][0][0][0])[i] = 0.0f;
+    if (BULK && threadIdx.x == 0) {
+        for (int i = 0; i < RG * STAGES; ++i) mbar_init(&full[0][0] + i, 1);
+        fence_mbar_init();
+    }
     __syncthreads();
     pdl_enter();
     const int narr = dres ? 3 : 2;
-    // [stage][array][vector i][thread].  A 2-byte element travels as the aligned
-    // 32-bit word it is part of (cp.async's smallest copy), HALF.
-    constexpr bool HALF = sizeof(Raw) == 2;
-    using Slot = typename RawVec<HALF ? 4 : (int)sizeof(Raw)>::type;
-    Slot* ring = reinterpret_cast<Slot*>(ln_ring) + threadIdx.x;
-    auto slot = [&](int st, int arr, int i) -> Slot* { return ring + ((st * narr + arr) * NV + i) * blockDim.x; };
+    // [stage][array][vector i][thread]
+    Raw* ring = reinterpret_cast<Raw*>(ln_ring) + threadIdx.x;
+    auto slot = [&](int st, int arr, int i) -> Raw* { return ring + ((st * narr + arr) * NV + i) * blockDim.x; };
+    // BULK: [group][stage][array][row_bytes], a row with the 16-byte blocks it
+    // begins and ends in; of the last rows only the blocks inside the array,
+    // the elements after those one by one
+    const int row_bytes = ln_row_bytes(K, sizeof(T));
+    const int64_t whole = (R * K * (int)sizeof(T)) & ~(int64_t)15;
+    auto row = [&](int st, int arr) { return ln_ring + ((g * STAGES + st) * narr + arr) * row_bytes; };
     auto stage = [&](int st, int64_t r) {
-        if (r < R) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * nt + t) * VEC;
-                if (c < K) {
-                    const int64_t at = r * K + c;
-                    auto copy = [&](int arr, const T* src) {
-                        if constexpr (sizeof(Raw) == 16) {
-                            cp_async16(slot(st, arr, i), src + at);
-                        } else if constexpr (sizeof(Raw) == 8) {
-                            cp_async8(slot(st, arr, i), src + at);
-                        } else if constexpr (sizeof(Raw) == 4) {
-                            cp_async4(slot(st, arr, i), src + at);
-                        } else {
-                            // the last element of an odd count has no partner
-                            if ((at | 1) < R * K) cp_async4(slot(st, arr, i), src + (at & ~(int64_t)1));
-                            else *slot(st, arr, i) = *reinterpret_cast<const uint16_t*>(src + at);
-                        }
-                    };
-                    copy(0, x);
-                    copy(1, dy);
-                    if (dres) copy(2, dres);
+        if constexpr (BULK) {
+            if (t == 0 && r < R) {
+                const int64_t from = r * K * (int)sizeof(T), a0 = from & ~(int64_t)15;
+                int64_t a1 = (from + K * (int)sizeof(T) + 15) & ~(int64_t)15;
+                if (a1 > whole) a1 = whole;
+                const uint32_t n = a1 > a0 ? (uint32_t)(a1 - a0) : 0u;
+                int c = (int)((a0 + n - from) / (int)sizeof(T));
+                for (c = c > 0 ? c : 0; c < K; ++c) {
+                    const int to = (int)(from - a0) + c * (int)sizeof(T);
+                    *reinterpret_cast<T*>(row(st, 0) + to) = x[r * K + c];
+                    *reinterpret_cast<T*>(row(st, 1) + to) = dy[r * K + c];
+                    if (dres) *reinterpret_cast<T*>(row(st, 2) + to) = dres[r * K + c];
+                }
+                mbar_arrive_expect_tx(&full[g][st], n * narr);
+                if (n) {
+                    bulk_load_1d(row(st, 0), reinterpret_cast<const char*>(x) + a0, n, &full[g][st]);
+                    bulk_load_1d(row(st, 1), reinterpret_cast<const char*>(dy) + a0, n, &full[g][st]);
+                    if (dres) bulk_load_1d(row(st, 2), reinterpret_cast<const char*>(dres) + a0, n, &full[g][st]);
                 }
             }
+        } else {
+            if (r < R) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = (i * nt + t) * VEC;
+                    if (c < K) {
+                        const int64_t at = r * K + c;
+                        cp_async16(slot(st, 0, i), x + at);
+                        cp_async16(slot(st, 1, i), dy + at);
+                        if (dres) cp_async16(slot(st, 2, i), dres + at);
+                    }
+                }
+            }
+            cp_async_commit();
         }
-        cp_async_commit();
     };
+    // BULK: the thread's columns are t, t + nt, ...: the first `own` of C are in the row
+    const int own = K / VEC > t ? (K / VEC - t + nt - 1) / nt : 0;
     // columns past K hold zeros in every array, so they add nothing
     auto fetch = [&](int st, int arr, int64_t r, float2 (&v)[C / 2]) {
         float f[NV][VEC];
+        if constexpr (BULK) {
+            const int64_t from = r * K * (int)sizeof(T);
+            const uint8_t* p = row(st, arr) + ((int)from & 15) + t * (int)sizeof(Raw);
+            const int hop = nt * (int)sizeof(Raw);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + t) * VEC;
-            const Slot raw = c < K ? *slot(st, arr, i) : Slot{};
-            if constexpr (HALF) f[i][0] = __uint_as_float(((r * K + c) & 1) ? raw & 0xFFFF0000u : raw << 16);
-            else P::to_floats(raw, f[i]);
+            for (int i = 0; i < NV; ++i) {
+                Raw raw{};
+                if (i < own) raw = *reinterpret_cast<const Raw*>(p);
+                p += hop;
+                P::to_floats(raw, f[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + t) * VEC;
+                P::to_floats(c < K ? *slot(st, arr, i) : Raw{}, f[i]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < C / 2; ++j)
@@ -570,9 +598,11 @@ __global__ void __launch_bounds__(MAXT, MINB)
     float2 ag[C / 2] = {}, ab[C / 2] = {}, gam[C / 2];
     if constexpr (GREG) params(gam);
     const int64_t first = (int64_t)blockIdx.x * groups + g, step = (int64_t)gridDim.x * groups;
+    constexpr int AHEAD = BULK && STAGES == 1 ? 1 : STAGES - 1;          // rows in flight before the first
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) stage(s, first + s * step);
+    for (int s = 0; s < AHEAD; ++s) stage(s, first + s * step);
     int st = 0, par = 0;
+    uint32_t phase = 0;
     const float inv = 1.0f / (float)K;
     float mean = 0.0f, rs = 0.0f;
     if (first < R) {
@@ -582,10 +612,15 @@ __global__ void __launch_bounds__(MAXT, MINB)
     for (int64_t r = first; r < R; r += step) {
         int ahead = st + STAGES - 1;
         if (ahead >= STAGES) ahead -= STAGES;
-        stage(ahead, r + (STAGES - 1) * step);
+        if constexpr (!BULK) stage(ahead, r + (STAGES - 1) * step);
         const int64_t rn = r + step < R ? r + step : r;
         const float mean_n = __ldg(mu + rn), rs_n = __ldg(rstd + rn);
-        cp_async_wait<STAGES - 1>();
+        if constexpr (BULK) {
+            // (an error word that is set already does not end the wait for the copies)
+            if (!wait_bounded_err(&full[g][st], phase, err)) wait_drain(&full[g][st], phase);
+        } else {
+            cp_async_wait<STAGES - 1>();
+        }
         float2 xh[C / 2], w[C / 2];
         auto load_row = [&]() {
             fetch(st, 0, r, xh);
@@ -614,6 +649,8 @@ __global__ void __launch_bounds__(MAXT, MINB)
         } else {
             c12 = make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
         }
+        // the group is past its reads of the row before, whose stage is free
+        if constexpr (BULK && STAGES > 1) stage(ahead, r + (STAGES - 1) * step);
         const float c1 = c12.x * inv, c2 = c12.y * inv;
         if constexpr (!KEEP) {
             load_row();
@@ -628,21 +665,43 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
             for (int j = 0; j < C / 2; ++j) w[j] = __fadd2_rn(w[j], xh[j]);
         }
+        if constexpr (BULK) {
+            T* o = dx + r * K + t * VEC;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * nt + t) * VEC;
-            float v[VEC];
+            for (int i = 0; i < NV; ++i) {
+                float v[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int e = i * VEC + j;
-                v[j] = (e & 1) ? w[e / 2].y : w[e / 2].x;
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = i * VEC + j;
+                    v[j] = (e & 1) ? w[e / 2].y : w[e / 2].x;
+                }
+                if (i < own) *reinterpret_cast<Raw*>(o) = P::from_floats(v);
+                o += nt * VEC;
             }
-            if (c < K) *reinterpret_cast<Raw*>(dx + r * K + c) = P::from_floats(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * nt + t) * VEC;
+                float v[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = i * VEC + j;
+                    v[j] = (e & 1) ? w[e / 2].y : w[e / 2].x;
+                }
+                if (c < K) *reinterpret_cast<Raw*>(dx + r * K + c) = P::from_floats(v);
+            }
+        }
+        if constexpr (BULK && STAGES == 1) {
+            __syncthreads();
+            stage(0, r + step);
         }
         mean = mean_n;
         rs = rs_n;
         par ^= 1;
-        if (++st == STAGES) st = 0;
+        if (++st == STAGES) {
+            st = 0;
+            phase ^= 1u;
+        }
     }
     if constexpr (GROUPED) {
         // the groups' sums, added in group order by the first (the ring is idle)
@@ -883,6 +942,8 @@ cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int group, in
     auto kern = k_ln_bwd<T, VEC, C, STAGES, MAXT, MINB, KEEP, GROUPED>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), kLnRoom);
     if (e != cudaSuccess) return e;
+    int* err = nullptr;
+    if (VEC * sizeof(T) < 16 && (e = device_error_word(&err)) != cudaSuccess) return e;
     const int threads = group * groups;
     int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, smem, sms);
     const int64_t most = parts_for(cdiv(a.M, groups));
@@ -890,13 +951,12 @@ cudaError_t ln_bwd_rows(const LnArgs& a, cudaStream_t st, int sms, int group, in
     *parts = (int)cap;
     launch_k(kern, (unsigned)cap, threads, smem, st, static_cast<const T*>(a.dy), static_cast<const T*>(a.x),
              static_cast<const T*>(a.dres), a.gamma, (const float*)a.mu, (const float*)a.rstd, a.M, (int)a.K, group,
-             static_cast<T*>(a.dx), static_cast<float*>(a.workspace));
+             static_cast<T*>(a.dx), static_cast<float*>(a.workspace), err);
     return cudaGetLastError();
 }
 
 // Three stages of the ring where they fit, else two or one.  Rows take the widest
-// vector of 16, 8 or 4 bytes that divides them (7400 x 1862 fp32: 45 us with 8
-// bytes, 65 with 4).  Short rows share a
+// vector of 16, 8, 4 or 2 bytes that divides them.  Short rows share a
 // CTA of MAXT threads where there are rows for all of its groups on every SM.
 template <typename T, int VEC, int C, int MAXT, int MINB, bool KEEP>
 cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
@@ -905,10 +965,13 @@ cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
     int groups = MAXT <= 256 ? MAXT / group : 1;
     groups = groups < kLnGroups ? groups : kLnGroups;
     while (groups > 1 && a.M < (int64_t)groups * sms) --groups;
-    const int bytes = sizeof(T) * VEC == 2 ? 4 : (int)sizeof(T);          // an element in the ring
-    const int stage = group * groups * C * bytes * (a.dres ? 3 : 2);
+    const int row = VEC * sizeof(T) < 16 ? ln_row_bytes((int)a.K, sizeof(T)) : group * C * (int)sizeof(T);
+    const int stage = groups * row * (a.dres ? 3 : 2);
     if constexpr (MAXT <= 256) {
-        if (groups > 1) return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, true>(a, st, sms, group, groups, 3 * stage, parts);
+        const int sums = group * groups * C * (int)sizeof(float2), ring = 3 * stage;
+        if (groups > 1)
+            return ln_bwd_rows<T, VEC, C, 3, MAXT, MINB, KEEP, true>(
+                a, st, sms, group, groups, ring > sums ? ring : sums, parts);
     }
     // (two CTAs with two stages each before one with three: 2048 x 4096 fp32 35.1 -> 27.5 us)
     const bool two = MINB >= 2 && 6 * stage > kLnRoom && 4 * stage <= kLnRoom;
@@ -920,14 +983,9 @@ cudaError_t ln_bwd_cols(const LnArgs& a, cudaStream_t st, int sms, int* parts)
 template <typename T, int VEC>
 cudaError_t ln_bwd_vec(const LnArgs& a, cudaStream_t st, int sms, int* parts)
 {
-    if constexpr (VEC == 1) {
-        if (a.K <= 256 * 8) return ln_bwd_cols<T, VEC, 8, 256, 4, true>(a, st, sms, parts);
-        if (a.K <= 1024 * 8) return ln_bwd_cols<T, VEC, 8, 1024, 1, true>(a, st, sms, parts);
-    } else {
-        if (a.K <= 256 * 16) return ln_bwd_cols<T, VEC, 16, 256, 2, true>(a, st, sms, parts);
-        if (a.K <= 512 * 16) return ln_bwd_cols<T, VEC, 16, 512, 1, true>(a, st, sms, parts);
-        if (a.K <= 768 * 16) return ln_bwd_cols<T, VEC, 16, 768, 1, true>(a, st, sms, parts);
-    }
+    if (a.K <= 256 * 16) return ln_bwd_cols<T, VEC, 16, 256, 2, true>(a, st, sms, parts);
+    if (a.K <= 512 * 16) return ln_bwd_cols<T, VEC, 16, 512, 1, true>(a, st, sms, parts);
+    if (a.K <= 768 * 16) return ln_bwd_cols<T, VEC, 16, 768, 1, true>(a, st, sms, parts);
     return ln_bwd_cols<T, VEC, 16, 1024, 1, false>(a, st, sms, parts);
 }
 
