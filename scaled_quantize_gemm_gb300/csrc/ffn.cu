@@ -233,9 +233,9 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 // by the epilogue where it is short: an accumulator's 128 x 256 values a CTA take
 // about 8 us through eight warps (gelu, z and codes), which the MMAs of the next
 // tile cover from K of about 3000 on.
-// One GB300, us: glu_fwd 16384 x 4096 -> 2 x 14336 with g, u and codes 1065
-// (3580 TFLOP/s); gemm_act 16384 x 4096 -> 14336 with bias, gelu_tanh, z and codes
-// 580-600; glu_bwd 2048 x 4096 -> 14336 86.
+// One GB300, us: glu_fwd 16384 x 4096 -> 2 x 14336 with g, u and codes 1050
+// (3670 TFLOP/s); gemm_act 16384 x 4096 -> 14336 with bias, gelu_tanh, z and codes
+// 560-600; glu_bwd 2048 x 4096 -> 14336 86.
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1)
     k_ffn_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FfnParams p,
