@@ -255,12 +255,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
     uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
     constexpr uint32_t TMEM_COLS = 2 * BN;
     __shared__ int s_skip;
+    __shared__ int s_stop[2];                  // stages each CTA's producer had issued when it gave up, else -1
     const uint32_t rank = cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // what touches no global memory of the kernel before this one runs ahead
     // of the wait on it
     if (threadIdx.x == 0) {
+        s_stop[0] = s_stop[1] = -1;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -325,6 +327,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                     }
                 }
             }
+            if (aborted) pair_stop(s_stop, rank, issued);
+            // the copies complete on the leader's barriers; whoever gives up a
+            // wait from here on, none of them is in flight any more
+            if (rank == 0) drain_ring<STAGES>(full, issued);
             if (!aborted) {
                 for (int i = 0; i < STAGES; ++i) {     // every stage's last release has landed
                     if (!wait(&empty[stage], phase ^ 1u)) break;
@@ -332,18 +338,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                         stage = 0;
                         phase ^= 1u;
                     }
-                }
-            } else if (rank == 0) {
-                // the pair's copies still in flight complete on the leader's barriers
-                int n = issued < STAGES ? issued : STAGES;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < n; ++i) {
-                    if (--s < 0) {
-                        s = STAGES - 1;
-                        ph ^= 1u;
-                    }
-                    wait_drain(&full[s], ph);
                 }
             }
         }
@@ -382,14 +376,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                 }
                 if (!aborted) mma_pair_commit(&afull[b], 3);
             }
+            mma_pair_commit(drain, 1);                  // completes once every issued MMA is done
+            wait_drain(drain, 0);
             if (!aborted) {
                 for (int j = 0; j < 2; ++j) {           // both accumulators' last releases have landed
                     const int l2 = lt + j;
                     if (!wait(&aempty[l2 & 1], ((uint32_t)(l2 >> 1) & 1u) ^ 1u)) break;
                 }
-            } else {
-                mma_pair_commit(drain, 1);              // completes once every issued MMA is done
-                wait_drain(drain, 0);
             }
         }
     } else {
@@ -569,7 +562,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         }
     }
     __syncthreads();
-    cluster_sync_all();                        // nothing is pending into either CTA any more
+    cluster_sync_all();
+    if (s_stop[0] >= 0) {                      // (the same in both CTAs)
+        const int total = num_tiles > cid ? (num_tiles - cid + ncl - 1) / ncl * nkb : 0;
+        if (rank == 0 && threadIdx.x == 0) drain_odd<STAGES>(full, s_stop, total, (uint32_t)L::STAGE);
+        cluster_sync_all();
+    }
+    // nothing is pending into either CTA any more
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, TMEM_COLS);
@@ -819,14 +818,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (lane == 0) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
-            bool aborted = false;
             int tile = u0 / w.nkb, kb = u0 - tile * w.nkb;
             int wt = tile / w.mtiles, mt = tile - wt * w.mtiles;
             for (int u = u0; u < u1; ++u) {
-                if (!wait(&empty[stage], phase ^ 1u)) {
-                    aborted = true;
-                    break;
-                }
+                if (!wait(&empty[stage], phase ^ 1u)) break;
                 uint8_t* sw = smem + stage * L::STAGE;
                 mbar_arrive_expect_tx(&full[stage], (uint32_t)L::STAGE);
                 tma_load_2d(sw, &tmW, kb * BK, wt * BOX, &full[stage]);
@@ -848,19 +843,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             // every load is under way: the next kernel's CTAs may take over the
             // SMs as this grid's tail leaves them (all of this grid is resident)
             pdl_trigger();
-            if (aborted) {
-                // wait for the copies still in flight before the CTA can exit
-                int n = issued < STAGES ? issued : STAGES;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < n; ++i) {
-                    if (--s < 0) {
-                        s = STAGES - 1;
-                        ph ^= 1u;
-                    }
-                    wait_drain(&full[s], ph);
-                }
-            }
+            drain_ring<STAGES>(full, issued);    // no copy is in flight when the CTA exits, whoever gives up a wait
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -896,10 +879,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
                 if (!aborted) mma_commit(&afull[b]);
             }
-            if (aborted) {
-                mma_commit(drain);
-                wait_drain(drain, 0);
-            }
+            mma_commit(drain);                   // every MMA issued is done before the tensor memory is freed
+            wait_drain(drain, 0);
         }
     } else {
         const int quarter = warp & 3;
@@ -1158,12 +1139,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (lane == 0) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
-            bool aborted = false;
             for (int i = 0; i < nk; ++i) {
-                if (!wait(&empty[stage], phase ^ 1u)) {
-                    aborted = true;
-                    break;
-                }
+                if (!wait(&empty[stage], phase ^ 1u)) break;
                 uint8_t* sw = smem + stage * L::STAGE;
                 mbar_arrive_expect_tx(&full[stage], (uint32_t)L::STAGE);
                 tma_load_2d(sw, &tmW, (kb0 + i) * BK, wt * BOX, &full[stage]);
@@ -1176,19 +1153,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 }
             }
             pdl_trigger();                       // (the grid is one wave: see ksplit_plan)
-            if (aborted) {
-                // wait for the copies still in flight before the CTA can exit
-                int c = issued < STAGES ? issued : STAGES;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < c; ++i) {
-                    if (--s < 0) {
-                        s = STAGES - 1;
-                        ph ^= 1u;
-                    }
-                    wait_drain(&full[s], ph);
-                }
-            }
+            drain_ring<STAGES>(full, issued);    // no copy is in flight when the CTA exits, whoever gives up a wait
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -1212,12 +1177,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                     phase ^= 1u;
                 }
             }
-            if (!aborted) {
-                mma_commit(afull);
-            } else {
-                mma_commit(drain);
-                wait_drain(drain, 0);
-            }
+            if (!aborted) mma_commit(afull);
+            mma_commit(drain);                   // every MMA issued is done before the tensor memory is freed
+            wait_drain(drain, 0);
         }
     } else {
         if (!GLU && q0 < quads) rows_residual<4>(p, m0 + 4 * q0, n, rs);

@@ -101,6 +101,37 @@ struct Smem {
     static_assert(NBARS * 8 + 16 <= 512, "barriers and the TMEM holder fit before the staging area");
 };
 
+// ------------------------------------------------------------------ giving up
+// A producer's or an MMA thread's last act, whether or not a wait of its own
+// ran out: another warp of the CTA may leave as soon as the error word is set,
+// so a CTA exits only after its copies and its MMAs are known to be done.
+// Issue i of a ring went to stage i % STAGES in phase i / STAGES.
+
+// waits (with a limit) for the last `issued` copies of a ring
+template <int STAGES>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int issued)
+{
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+        wait_drain(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
+}
+// CTA pairs: the odd CTA's copies are counted on the leader's barriers beside
+// the leader's own, so those of a stage that the leader never issued complete
+// no phase.  A producer that gives up writes its count into both CTAs (stop,
+// -1 before); after a cluster barrier, the leader expects the odd CTA's bytes
+// alone for the stages it was ahead by, `total` of them at most, and waits.
+__device__ __forceinline__ void pair_stop(int* stop, uint32_t rank, int issued)
+{
+    stop[rank] = issued;
+    st_shared_cluster_u32(cluster_map(smem_addr(&stop[rank]), rank ^ 1u), (uint32_t)issued);
+}
+template <int STAGES>
+__device__ __forceinline__ void drain_odd(uint64_t* full, const int* stop, int total, uint32_t stage_bytes)
+{
+    const int odd = stop[1] >= 0 ? stop[1] : total;
+    for (int i = stop[0]; i < odd; ++i) mbar_arrive_expect_tx(&full[i % STAGES], stage_bytes);
+    for (int i = stop[0]; i < odd; ++i) wait_drain(&full[i % STAGES], (uint32_t)(i / STAGES) & 1u);
+}
+
 // ------------------------------------------------------------------ host
 // 2-D u8 tensor [rows][inner] (inner contiguous), box box_rows x 128 bytes, 128-byte swizzle
 bool make_tmap(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint32_t box_rows);

@@ -334,6 +334,10 @@ __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t cl_addr)
                  : "memory");
     return v;
 }
+__device__ __forceinline__ void st_shared_cluster_u32(uint32_t cl_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cl_addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cl_addr)
 {
     uint32_t v;
