@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     uint64_t* aempty = afull + 2;
     uint64_t* drain = aempty + 2;
     uint32_t* holder = reinterpret_cast<uint32_t*>(drain + 1);
-    __shared__ int s_last;
+    __shared__ int s_last, s_skip;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // what touches no global memory of the kernel before this one runs ahead
     // of the wait on it
@@ -808,12 +808,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
     }
     pdl_enter();
+    // One decision for the CTA: the epilogue warps meet in named barriers, which
+    // wait for all of them without a limit, so a word that is set between two
+    // warps' reads must not send one of them past the others.
+    if (threadIdx.x == 0) s_skip = *reinterpret_cast<volatile int*>(p.err);
+    __syncthreads();
     const uint32_t tmem_base = *holder;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err(bar, parity, p.err); };
 
-    if (*reinterpret_cast<volatile int*>(p.err)) {
-        // a wait ran out earlier: compute nothing.  (Should the word be set
-        // between two warps' reads, the bounded waits of the rest give up on it.)
+    if (s_skip) {
+        // a wait ran out earlier: compute nothing
     } else if (warp == 0) {
         if (lane == 0) {
             int stage = 0, issued = 0;
