@@ -231,19 +231,7 @@ __device__ __forceinline__ void producer_loop(uint8_t* smem, uint64_t* full, uin
             }
         }
     }
-    if (aborted) {
-        // wait for the copies still in flight before the CTA can exit
-        int n = issued < STAGES ? issued : STAGES;
-        int s = stage;
-        uint32_t ph = phase;
-        for (int i = 0; i < n; ++i) {
-            if (--s < 0) {
-                s = STAGES - 1;
-                ph ^= 1u;
-            }
-            wait_drain(&full[s], ph);
-        }
-    }
+    drain_ring<STAGES>(full, issued);
 }
 
 // ================================================================== mode 0
@@ -308,12 +296,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     constexpr uint32_t TMEM_COLS = 2 * BN;
     static_assert(TMEM_COLS <= 512, "two accumulators must fit in tensor memory");
     __shared__ int s_skip;
+    __shared__ int s_stop[2];                  // stages each CTA's producer had issued when it gave up, else -1
     const uint32_t rank = cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr bool a_mn = (LAYOUT & 1) != 0, b_mn = (LAYOUT & 2) != 0;   // MN-major operands
 
     if (threadIdx.x == 0) {
         s_skip = rank == 0 ? *reinterpret_cast<volatile int*>(&g_dev_error) : 0;
+        s_stop[0] = s_stop[1] = -1;
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);            // the leader's expect_tx arrival (both CTAs' bytes)
             mbar_init(&empty[s], 1);           // the leader's multicast commit
@@ -375,6 +365,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                     }
                 }
             }
+            if (aborted) pair_stop(s_stop, rank, issued);
+            // the copies complete on the leader's barriers; whoever gives up a
+            // wait from here on, none of them is in flight any more
+            if (rank == 0) drain_ring<STAGES>(full, issued);
             if (!aborted) {
                 for (int i = 0; i < STAGES; ++i) {     // every stage's last release has landed
                     if (!wait_bounded_cluster(&empty[stage], phase ^ 1u)) break;
@@ -382,18 +376,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                }
-            } else if (rank == 0) {
-                // the pair's copies still in flight complete on the leader's barriers
-                int n = issued < STAGES ? issued : STAGES;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < n; ++i) {
-                    if (--s < 0) {
-                        s = STAGES - 1;
-                        ph ^= 1u;
-                    }
-                    wait_drain(&full[s], ph);
                 }
             }
         }
@@ -435,14 +417,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 }
                 if (!aborted) mma_pair_commit(&afull[b], 3);
             }
+            mma_pair_commit(drain, 1);                  // completes once every issued MMA is done
+            wait_drain(drain, 0);
             if (!aborted) {
                 for (int j = 0; j < 2; ++j) {           // both accumulators' last releases have landed
                     const int l2 = lt + j;
                     if (!wait_bounded_cluster(&aempty[l2 & 1], ((uint32_t)(l2 >> 1) & 1u) ^ 1u)) break;
                 }
-            } else {
-                mma_pair_commit(drain, 1);              // completes once every issued MMA is done
-                wait_drain(drain, 0);
             }
         }
     } else {
@@ -538,7 +519,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         }
     }
     __syncthreads();
-    cluster_sync_all();                        // nothing is pending into either CTA any more
+    cluster_sync_all();
+    if (s_stop[0] >= 0) {                      // (the same in both CTAs)
+        const int total = num_tiles > cid ? (num_tiles - cid + ncl - 1) / ncl * nkb : 0;
+        if (rank == 0 && threadIdx.x == 0) drain_odd<STAGES>(full, s_stop, total, (uint32_t)L::STAGE);
+        cluster_sync_all();
+    }
+    // nothing is pending into either CTA any more
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, TMEM_COLS);
@@ -687,10 +674,8 @@ __global__ void __launch_bounds__(kPromoThreads, 1)
                     }
                 }
             }
-            if (aborted) {
-                mma_commit(drain);
-                wait_drain(drain, 0);
-            }
+            mma_commit(drain);                   // every MMA issued is done before the tensor memory is freed
+            wait_drain(drain, 0);
         }
     } else if (warp == 2) {
         if (lane == 0) {
@@ -1027,18 +1012,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     }
                 }
             }
-            if (aborted) {
-                int n = issued < STAGES ? issued : STAGES;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < n; ++i) {
-                    if (--s < 0) {
-                        s = STAGES - 1;
-                        ph ^= 1u;
-                    }
-                    wait_drain(&full[s], ph);
-                }
-            }
+            drain_ring<STAGES>(full, issued);
         } else if (warp == 1 && lane == 0) {
             int stage = 0, lt = 0, cw = 0;
             uint32_t phase = 0;
@@ -1089,10 +1063,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 }
                 if (!aborted) mma_commit(&afull[b]);
             }
-            if (aborted) {
-                mma_commit(drain);
-                wait_drain(drain, 0);
-            }
+            mma_commit(drain);                   // every MMA issued is done before the tensor memory is freed
+            wait_drain(drain, 0);
         }
     } else if (warp < 12) {
         regs_inc<kMxEpiRegs>();
