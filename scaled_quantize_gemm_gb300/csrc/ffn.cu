@@ -437,6 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             for (int c = c_begin; c < c_end && row0 < p.M; c += 32) {
                 const int col = nb * TN + c, left = p.N - col;
                 if (left <= 0) break;
+                __syncwarp();                  // tcgen05.ld takes a converged warp
                 float2 v[16];
                 if constexpr (KIND == kEpiGlu) {
                     uint32_t rg[32], ru[32];
@@ -511,6 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         uint32_t r[16];
+                        __syncwarp();
                         tmem_ld_32x32b_x16(taddr + (uint32_t)(c + 16 * h), r);
                         tmem_ld_wait();
                         float2 dg[8], du[8];
@@ -946,6 +948,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             uint32_t rs[L::SHARE];                          // the residual, fetched ahead of the sums
             if (!GLU && whole) rows_residual<L::SHARE>(p, mt * NT + t0, n, rs);
             if (!bar_all(1, ETH, wait(&afull[b], (uint32_t)(seg >> 1) & 1u))) break;
+            __syncwarp();                      // tcgen05.ld takes a converged warp, which bar_all does not leave
             tc_fence_after();
             // this CTA's block of sums: in shared memory for a whole glu tile
             // (the barrier above says that the last one has been read)
@@ -1195,6 +1198,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             const int quarter = warp & 3, t0 = ((warp - 2) >> 2) * L::SHARE, wr = quarter * 32 + lane;
             const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)t0;
             float* sums = reinterpret_cast<float*>(smem);
+            __syncwarp();                      // (as in k_ffn_rows)
             if constexpr (L::SHARE >= 16) {
 #pragma unroll
                 for (int c = 0; c < L::SHARE; c += 16) {
