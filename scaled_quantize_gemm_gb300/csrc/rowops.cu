@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
             c12 = block_total2(red[g][par], span);
         } else {
             c12 = make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
+            if (BULK) __syncwarp();             // (shuffles order no memory)
         }
         // the group is past its reads of the row before, whose stage is free
         if constexpr (BULK && STAGES > 1) stage(ahead, r + (STAGES - 1) * step);
