@@ -93,9 +93,11 @@ class GatedFFN:
             sq.fp8_quantize(w, FORMATS[i], sq.TENSOR, q, delayed_state=self._state(i), history_len=self.H)
 
     # ------------------------------------------------------------ one pass
-    def _run(self, x, gu, mu, rstd, y):
+    def _run(self, x, gu, mu, rstd, y, codes):
+        """One pass; `codes` names the buffers of n's and h's codes: a training step's are read again by its backward
+        pass, so nothing else may write them."""
         M, K, F, H = x.shape[0], self.K, self.F, self.H
-        qn, qh = self._get("qn", (M, K), torch.uint8), self._get("qh", (M, F), torch.uint8)
+        qn, qh = self._get("qn" + codes, (M, K), torch.uint8), self._get("qh" + codes, (M, F), torch.uint8)
         sq.fp8_layernorm_fwd(x, self.gamma, self.beta, self.eps, None, mu=mu, rstd=rstd, q_out=qn, q_format=sq.E4M3,
                              q_state=self._state(N), history_len=H)
         sq.fp8_glu_fwd(qn, sq.E4M3, self._scale(N), self.q_gate_up, sq.E4M3, self._scale(W_GU), self.act, gu_out=gu,
@@ -108,7 +110,7 @@ class GatedFFN:
     def decode(self, x, y=None):
         """y for any number of tokens, on the frozen weights; keeps nothing for a backward pass."""
         y = torch.empty_like(x) if y is None else y
-        self._run(x, None, None, None, y)
+        self._run(x, None, None, None, y, "_decode")
         return y
 
     def forward(self, x):
@@ -118,7 +120,7 @@ class GatedFFN:
         gu = self._get("gu", (M, 2 * self.F), torch.bfloat16)
         mu, rstd = self._get("mu", (M,), torch.float32), self._get("rstd", (M,), torch.float32)
         y = torch.empty_like(x)
-        qn, qh = self._run(x, gu, mu, rstd, y)
+        qn, qh = self._run(x, gu, mu, rstd, y, "")
         self._saved = (x, gu, mu, rstd, qn, qh)
         return y
 
@@ -127,10 +129,10 @@ class GatedFFN:
         if self._saved is None:
             raise RuntimeError("backward without a forward")
         x, gu, mu, rstd, qn, qh = self._saved
-        self._saved = None
         M, K, F, H = x.shape[0], self.K, self.F, self.H
         if M % 16:
             raise ValueError(f"a training step takes a multiple of 16 tokens, got {M}")
+        self._saved = None
         dev = x.device
         qdy, qdgu = self._get("qdy", (M, K), torch.uint8), self._get("qdgu", (M, 2 * F), torch.uint8)
         sq.fp8_quantize(dy, sq.E5M2, sq.TENSOR, qdy, delayed_state=self._state(DY), history_len=H)
