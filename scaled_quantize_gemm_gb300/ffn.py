@@ -17,6 +17,8 @@ data and weight gradients as they are.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 import scaled_quantize_gemm_gb300 as sq
@@ -26,6 +28,10 @@ N, W_GU, H_, W_DOWN, DY, DGU = range(6)
 FORMATS = [sq.E4M3, sq.E4M3, sq.E4M3, sq.E4M3, sq.E5M2, sq.E5M2]
 
 
+def _capturing() -> bool:
+    return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+
+
 class GatedFFN:
     """One sublayer's weights, scaling states and buffers.
 
@@ -33,6 +39,12 @@ class GatedFFN:
     rows, then the up projection's), w_down [K][F] bf16; K, F multiples of 16.
     A training step takes a number of tokens that is a multiple of 16 (the
     weight gradients contract over them); ``decode`` takes any number.
+
+    The buffers are the block's own, one set for all calls, so its calls follow
+    one another on one stream (or in streams that wait for each other), and one
+    forward is kept at a time.  Calls may be captured into CUDA graphs, also
+    for several numbers of tokens: a buffer that a call was given lives as long
+    as the block.
     """
 
     def __init__(self, gamma, beta, w_gate_up, w_down, act: int = sq.ACT_SILU, eps: float = 1e-5,
@@ -48,7 +60,9 @@ class GatedFFN:
         sq.fp8_scale_init(self.states, 6, history_len)
         self.q_gate_up = torch.empty((F2, K), dtype=torch.uint8, device=dev)
         self.q_down = torch.empty((K, self.F), dtype=torch.uint8, device=dev)
-        self._buffers = {}
+        self._buffers = {}                   # name -> the largest buffer so far, in bytes
+        self._views = {}                     # name -> its last view
+        self._kept = []                      # every buffer: a captured graph may replay on it
         self._saved = None
 
     # ------------------------------------------------------------ states and scratch
@@ -61,21 +75,32 @@ class GatedFFN:
         j = (i + 1) * sq.state_floats(self.H) - 1
         return self.states[j:j + 1]
 
-    def _get(self, name, shape, dtype):
-        """a buffer that lives as long as its shape is asked for"""
+    def _bytes(self, name, nbytes, make):
+        """A buffer of at least `nbytes` that lives as long as the block.  A larger one than before is at least twice
+        as large, so all the smaller ones together are no larger than it.  One that is made while a graph is being
+        captured belongs to that graph (its memory, and what fills it, come with the replay) and is not handed on."""
         t = self._buffers.get(name)
-        if t is None or t.shape != torch.Size(shape) or t.dtype != dtype:
-            t = self._buffers[name] = torch.empty(shape, dtype=dtype, device=self.states.device)
+        if t is None or t.numel() < nbytes:
+            t = make(max(nbytes, 0 if t is None else 2 * t.numel()), dtype=torch.uint8, device=self.states.device)
+            self._kept.append(t)
+            if not _capturing():
+                self._buffers[name] = t
         return t
+
+    def _get(self, name, shape, dtype):
+        v = self._views.get(name)
+        if v is not None and v.shape == shape and v.dtype is dtype:
+            return v
+        nbytes = math.prod(shape) * dtype.itemsize
+        t = self._bytes(name, nbytes, torch.empty)
+        v = t[:nbytes].view(dtype).view(shape)
+        if t is self._buffers.get(name):
+            self._views[name] = v
+        return v
 
     def _workspace(self, name, nbytes):
         """scratch of the split products (zeroed when made, left so by every call)"""
-        if nbytes == 0:
-            return None
-        t = self._buffers.get(name)
-        if t is None or t.numel() < nbytes:
-            t = self._buffers[name] = torch.zeros(nbytes, dtype=torch.uint8, device=self.states.device)
-        return t
+        return self._bytes(name, nbytes, torch.zeros) if nbytes else None
 
     def calibrate(self, x):
         """One forward pass that sets the activations' and weights' scales from what it records."""

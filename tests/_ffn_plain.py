@@ -12,7 +12,8 @@ def _val(q, fmt, scale):
 
 def _cast(v, q, fmt, state, H):
     q.copy_((v * state[H]).clamp(-FMAX[fmt], FMAX[fmt]).to(F8[fmt]).view(torch.uint8))
-    state[0] = torch.maximum(state[0], v.abs().max())
+    if v.numel():
+        state[0] = torch.maximum(state[0], v.abs().max())
 
 
 def _act(x, act):
@@ -45,7 +46,8 @@ def quantize(x, fmt, gran, q, delayed_state=None, history_len=0):
 
 def layernorm_fwd(x, gamma, beta, eps, y, mu=None, rstd=None, q_out=None, q_format=0, q_state=None, history_len=0):
     v = x.float()
-    m, r = v.mean(1), (v.var(1, unbiased=False) + eps).rsqrt()
+    m = v.mean(1)
+    r = ((v - m[:, None]).square().mean(1) + eps).rsqrt()
     if mu is not None:
         mu.copy_(m)
         rstd.copy_(r)

@@ -1,10 +1,13 @@
 """What GatedFFN keeps between its calls, on the CPU (entry points: _ffn_plain.py)."""
+import weakref
+
 import pytest
 import torch
 
 import _ffn_plain
 import scaled_quantize_gemm_gb300 as sq
 from _ffn_ref import gen, randn
+from scaled_quantize_gemm_gb300 import ffn
 from scaled_quantize_gemm_gb300.ffn import GatedFFN
 
 BF = torch.bfloat16
@@ -49,3 +52,79 @@ def test_a_refused_backward_keeps_the_forward(block):
     for _ in range(2):
         with pytest.raises(ValueError, match="multiple of 16"):
             b.backward(r(5, K).to(BF))
+
+
+# ---------------------------------------------------------------- buffers that a captured graph may hold
+@pytest.fixture
+def made(monkeypatch):
+    """weak references to every tensor that torch.empty and torch.zeros make, in order"""
+    refs = []
+    for name in ("empty", "zeros"):
+        def make(*a, _f=getattr(torch, name), **kw):
+            t = _f(*a, **kw)
+            refs.append(weakref.ref(t))
+            return t
+        monkeypatch.setattr(torch, name, make)
+    return refs
+
+
+def test_buffers_outlive_other_batch_sizes(made, block):
+    """What a call of 100 tokens uses (and a graph of it replays on) still exists after calls of 105, 300 and 1."""
+    b, r = block
+    x, y = r(100, K).to(BF), torch.empty(100, K, dtype=BF)
+    before = len(made)
+    b.decode(x, y)
+    mine = made[before:]
+    assert len(mine) == 4                    # the codes of n and h, two workspaces
+    for tokens in (105, 300, 1):
+        b.decode(r(tokens, K).to(BF))
+    assert all(w() is not None for w in mine)
+
+
+def test_training_buffers_outlive_other_batch_sizes(made, block):
+    b, r = block
+
+    def step(tokens):
+        b.forward(r(tokens, K).to(BF))
+        return b.backward(r(tokens, K).to(BF))
+
+    before = len(made)
+    grads = step(8 * M)                      # larger than the fixture's: new buffers
+    mine = [w for w in made[before:] if not any(w() is t for t in grads)]
+    mine = [w for w in mine if w() is not None]           # (the output y is the caller's)
+    assert len(mine) >= 7
+    step(M)
+    step(17 * M)
+    assert all(w() is not None for w in mine)
+
+
+def test_growing_batches_keep_little(made, block):
+    """The buffers grow by doubling: what is kept of all the smaller ones is no more than the largest."""
+    b, r = block
+    before = len(made)
+    for tokens in range(1, 65):
+        b.decode(r(tokens, K).to(BF))
+    alive = [w() for w in made[before:] if w() is not None]
+    assert sum(t.numel() for t in alive) <= 4 * 64 * (K + F + 64 + 64)
+
+
+def test_a_call_without_tokens(block):
+    b, r = block
+    assert b.decode(r(0, K).to(BF)).shape == (0, K)
+
+
+def test_a_buffer_made_during_a_capture_stays_with_the_graph(made, block, monkeypatch):
+    """Its memory and its zeros come with the replay: calls outside the graph get others."""
+    b, r = block
+    x = r(100, K).to(BF)
+    before = len(made)
+    with monkeypatch.context() as mp:
+        mp.setattr(ffn, "_capturing", lambda: True)
+        b.decode(x, torch.empty_like(x))
+    graph = made[before:]
+    assert len(graph) == 4 and all(w() is not None for w in graph)
+    before = len(made)
+    b.decode(x, torch.empty_like(x))
+    assert len(made) == before + 4
+    b.decode(x, torch.empty_like(x))
+    assert len(made) == before + 4
