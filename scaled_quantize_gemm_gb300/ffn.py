@@ -8,8 +8,11 @@ parts, gated):
 
 with per-tensor delayed scaling for every cast.  ``forward`` and ``backward``
 are a training step (weights cast from bf16 every step, as they change);
-``freeze`` casts the weights once and ``decode`` runs a few tokens at a time
-with the scales as they stand: three kernels, each streaming its weights once.
+``freeze`` casts the weights once and keeps the scales of that moment, and
+``decode`` runs a few tokens at a time with both: three kernels, each streaming
+its weights once.  Codes are turned back with the steps that they were cast
+with, wherever ``update_scales`` falls: between ``freeze`` and ``decode``, or
+between ``forward`` and ``backward``.
 
 The backward pass takes dY in E5M2 (HYBRID) and never writes the gradient of
 h: its product's epilogue turns it into the codes of [dg | du], which feed the
@@ -60,20 +63,22 @@ class GatedFFN:
         sq.fp8_scale_init(self.states, 6, history_len)
         self.q_gate_up = torch.empty((F2, K), dtype=torch.uint8, device=dev)
         self.q_down = torch.empty((K, self.F), dtype=torch.uint8, device=dev)
+        self._frozen = torch.empty_like(self.states)     # the states as they were when the weights were last cast
+        self._cast = False                   # ... which they have been
         self._buffers = {}                   # name -> the largest buffer so far, in bytes
         self._views = {}                     # name -> its last view
         self._kept = []                      # every buffer: a captured graph may replay on it
         self._saved = None
 
     # ------------------------------------------------------------ states and scratch
-    def _state(self, i):
+    def _state(self, i, states=None):
         n = sq.state_floats(self.H)
-        return self.states[i * n:(i + 1) * n]
+        return (self.states if states is None else states)[i * n:(i + 1) * n]
 
-    def _scale(self, i):
+    def _scale(self, i, states=None):
         """the dequantisation step of a state's codes (one element)"""
         j = (i + 1) * sq.state_floats(self.H) - 1
-        return self.states[j:j + 1]
+        return (self.states if states is None else states)[j:j + 1]
 
     def _bytes(self, name, nbytes, make):
         """A buffer of at least `nbytes` that lives as long as the block.  A larger one than before is at least twice
@@ -113,47 +118,56 @@ class GatedFFN:
         sq.fp8_update_scale(self.states, 6, self.H, FORMATS)
 
     def freeze(self):
-        """Casts both weights with their current scales, for ``decode``."""
+        """Casts both weights with their current scales and keeps all scales as they are now, for ``decode``."""
         for w, q, i in ((self.w_gate_up, self.q_gate_up, W_GU), (self.w_down, self.q_down, W_DOWN)):
             sq.fp8_quantize(w, FORMATS[i], sq.TENSOR, q, delayed_state=self._state(i), history_len=self.H)
+        self._frozen.copy_(self.states)
+        self._cast = True
 
     # ------------------------------------------------------------ one pass
-    def _run(self, x, gu, mu, rstd, y, codes):
-        """One pass; `codes` names the buffers of n's and h's codes: a training step's are read again by its backward
-        pass, so nothing else may write them."""
+    def _run(self, x, gu, mu, rstd, y, codes, states):
+        """One pass with the activations' scales in `states`; `codes` names the buffers of n's and h's codes: a
+        training step's are read again by its backward pass, so nothing else may write them."""
         M, K, F, H = x.shape[0], self.K, self.F, self.H
+        s_gu, s_down = self._scale(W_GU, self._frozen), self._scale(W_DOWN, self._frozen)
         qn, qh = self._get("qn" + codes, (M, K), torch.uint8), self._get("qh" + codes, (M, F), torch.uint8)
         sq.fp8_layernorm_fwd(x, self.gamma, self.beta, self.eps, None, mu=mu, rstd=rstd, q_out=qn, q_format=sq.E4M3,
-                             q_state=self._state(N), history_len=H)
-        sq.fp8_glu_fwd(qn, sq.E4M3, self._scale(N), self.q_gate_up, sq.E4M3, self._scale(W_GU), self.act, gu_out=gu,
-                       q_out=qh, q_format=sq.E4M3, q_state=self._state(H_), history_len=H,
+                             q_state=self._state(N, states), history_len=H)
+        sq.fp8_glu_fwd(qn, sq.E4M3, self._scale(N, states), self.q_gate_up, sq.E4M3, s_gu, self.act, gu_out=gu,
+                       q_out=qh, q_format=sq.E4M3, q_state=self._state(H_, states), history_len=H,
                        workspace=self._workspace("ws_gu", sq.fp8_glu_fwd_workspace_bytes(M, F, K)))
-        sq.fp8_gemm_act(qh, sq.E4M3, self._scale(H_), self.q_down, sq.E4M3, self._scale(W_DOWN), sq.ACT_NONE, D=y,
+        sq.fp8_gemm_act(qh, sq.E4M3, self._scale(H_, states), self.q_down, sq.E4M3, s_down, sq.ACT_NONE, D=y,
                         residual=x, workspace=self._workspace("ws_down", sq.fp8_gemm_act_workspace_bytes(M, K, F)))
         return qn, qh
 
     def decode(self, x, y=None):
-        """y for any number of tokens, on the frozen weights; keeps nothing for a backward pass."""
+        """y for any number of tokens, on the frozen weights and scales; keeps nothing for a backward pass and leaves
+        the training step's statistics alone."""
+        if not self._cast:
+            raise RuntimeError("decode needs the weights' codes: call freeze (or forward) first")
         y = torch.empty_like(x) if y is None else y
-        self._run(x, None, None, None, y, "_decode")
+        self._run(x, None, None, None, y, "_decode", self._frozen)
         return y
 
     def forward(self, x):
-        """y [M][K] bf16 of x [M][K] bf16; keeps what ``backward`` needs."""
+        """y [M][K] bf16 of x [M][K] bf16; keeps what ``backward`` needs, x itself among it."""
         M = x.shape[0]
         self.freeze()
         gu = self._get("gu", (M, 2 * self.F), torch.bfloat16)
         mu, rstd = self._get("mu", (M,), torch.float32), self._get("rstd", (M,), torch.float32)
         y = torch.empty_like(x)
-        qn, qh = self._run(x, gu, mu, rstd, y, "")
-        self._saved = (x, gu, mu, rstd, qn, qh)
+        qn, qh = self._run(x, gu, mu, rstd, y, "", self.states)
+        cast = self._get("cast", self.states.shape, torch.float32)       # the scales of qn and qh
+        cast.copy_(self.states)
+        self._saved = (x, gu, mu, rstd, qn, qh, cast)
         return y
 
     def backward(self, dy):
-        """-> (dx bf16, dgamma, dbeta, dw_gate_up, dw_down, all fp32) of the last forward."""
+        """-> (dx bf16, dgamma, dbeta, dw_gate_up, dw_down, all fp32) of the last forward, on the weights' codes as
+        last cast (by it, or by a ``freeze`` since)."""
         if self._saved is None:
             raise RuntimeError("backward without a forward")
-        x, gu, mu, rstd, qn, qh = self._saved
+        x, gu, mu, rstd, qn, qh, cast = self._saved
         M, K, F, H = x.shape[0], self.K, self.F, self.H
         if M % 16:
             raise ValueError(f"a training step takes a multiple of 16 tokens, got {M}")
@@ -161,18 +175,18 @@ class GatedFFN:
         dev = x.device
         qdy, qdgu = self._get("qdy", (M, K), torch.uint8), self._get("qdgu", (M, 2 * F), torch.uint8)
         sq.fp8_quantize(dy, sq.E5M2, sq.TENSOR, qdy, delayed_state=self._state(DY), history_len=H)
-        sq.fp8_glu_bwd(qdy, sq.E5M2, self._scale(DY), self.q_down, sq.E4M3, self._scale(W_DOWN), gu, self.act, qdgu,
-                       sq.E5M2, self._state(DGU), H)
+        sq.fp8_glu_bwd(qdy, sq.E5M2, self._scale(DY), self.q_down, sq.E4M3,
+                       self._scale(W_DOWN, self._frozen), gu, self.act, qdgu, sq.E5M2, self._state(DGU), H)
         dn = self._get("dn", (M, K), torch.bfloat16)
         dw_gu = torch.empty((2 * F, K), device=dev)
         dw_down = torch.empty((K, F), device=dev)
         s_dy, s_dgu = self._scale(DY), self._scale(DGU)
-        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.K_MAJOR, self.q_gate_up, sq.E4M3, self._scale(W_GU), sq.MN_MAJOR,
-                           dn, M, K, 2 * F)
-        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.MN_MAJOR, qn, sq.E4M3, self._scale(N), sq.MN_MAJOR, dw_gu, 2 * F,
-                           K, M)
-        sq.fp8_gemm_layout(qdy, sq.E5M2, s_dy, sq.MN_MAJOR, qh, sq.E4M3, self._scale(H_), sq.MN_MAJOR, dw_down, K, F,
-                           M)
+        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.K_MAJOR, self.q_gate_up, sq.E4M3,
+                           self._scale(W_GU, self._frozen), sq.MN_MAJOR, dn, M, K, 2 * F)
+        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.MN_MAJOR, qn, sq.E4M3, self._scale(N, cast), sq.MN_MAJOR, dw_gu,
+                           2 * F, K, M)
+        sq.fp8_gemm_layout(qdy, sq.E5M2, s_dy, sq.MN_MAJOR, qh, sq.E4M3, self._scale(H_, cast), sq.MN_MAJOR, dw_down, K,
+                           F, M)
         dx, dgamma, dbeta = torch.empty_like(x), torch.empty(K, device=dev), torch.empty(K, device=dev)
         ws = self._get("ws_ln", (max(16, sq.fp8_layernorm_bwd_workspace_bytes(M, K)),), torch.uint8)
         sq.fp8_layernorm_bwd(dn, x, self.gamma, mu, rstd, dx, dgamma, dbeta, ws, dres=dy)

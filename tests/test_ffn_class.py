@@ -128,3 +128,72 @@ def test_a_buffer_made_during_a_capture_stays_with_the_graph(made, block, monkey
     assert len(made) == before + 4
     b.decode(x, torch.empty_like(x))
     assert len(made) == before + 4
+
+
+# ---------------------------------------------------------------- scales that move
+def _move(b):
+    """what an update does once the maxima have moved"""
+    for i in range(6):
+        b._state(i)[0] = 7.0 + i
+    b.update_scales()
+
+
+def test_scales_updated_between_forward_and_backward(block):
+    """The backward pass takes the forward's codes back with the steps that they were cast with."""
+    b, r = block
+    x, dy = r(M, K).to(BF), r(M, K).to(BF)
+    b.forward(x)
+    want = b.backward(dy)
+    b.forward(x)
+    gradients = b.states[4 * (b.H + 2):].clone()
+    _move(b)
+    b.states[4 * (b.H + 2):] = gradients     # dY and [dg | du] are cast in the backward pass, with the newest
+    assert _same(b.backward(dy), want)
+
+
+def test_scales_updated_between_freeze_and_decode(block):
+    b, r = block
+    x = r(7, K).to(BF)
+    b.freeze()
+    want = b.decode(x)
+    _move(b)
+    assert torch.equal(b.decode(x), want)
+    b.freeze()
+    moved = b.decode(x)
+    assert not torch.equal(moved, want)
+    assert float((moved.float() - want.float()).norm()) <= 0.3 * float((want.float() - x.float()).norm())
+
+
+def test_freeze_between_forward_and_backward(block):
+    """The weights' codes and their step change together."""
+    b, r = block
+    x, dy = r(M, K).to(BF), r(M, K).to(BF)
+    b.forward(x)
+    want = b.backward(dy)
+    b.forward(x)
+    gradients = b.states[4 * (b.H + 2):].clone()
+    _move(b)
+    b.freeze()
+    b.states[4 * (b.H + 2):] = gradients
+    for p, q in zip(b.backward(dy), want):
+        assert float((p.float() - q.float()).norm()) <= 0.3 * float(q.float().norm())
+
+
+def test_decode_leaves_the_training_statistics(block):
+    """Serving a sequence with large values does not move the scales of the training step."""
+    b, r = block
+    b.freeze()
+    states = b.states.clone()
+    b.decode((r(9, K) * 1000).to(BF))
+    assert torch.equal(b.states, states)
+
+
+def test_decode_needs_codes(monkeypatch):
+    """Weights that were never cast are refused, not read."""
+    _ffn_plain.install(monkeypatch)
+    g = gen(2, "cpu")
+    b = GatedFFN(torch.ones(K), None, randn(g, 2 * F, K, device="cpu").to(BF), randn(g, K, F, device="cpu").to(BF))
+    with pytest.raises(RuntimeError, match="freeze"):
+        b.decode(torch.zeros(3, K, dtype=BF))
+    b.freeze()
+    b.decode(torch.zeros(3, K, dtype=BF))

@@ -66,3 +66,50 @@ def test_decode_between_forward_and_backward(tokens):
     got = b.backward(dy)
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def _move(b):
+    for i in range(6):
+        b._state(i)[0] = 7.0 + i
+    b.update_scales()
+
+
+def test_scales_updated_within_a_step():
+    b, g = _ready(3)
+    x, dy = randn(g, 48, K).to(BF), (randn(g, 48, K) * 1e-3).to(BF)
+    for _ in range(2):
+        b.forward(x)
+        b.backward(dy)
+        b.update_scales()
+    b.forward(x)
+    want = [t.clone() for t in b.backward(dy)]
+    b.forward(x)
+    gradients = b.states[4 * (b.H + 2):].clone()
+    _move(b)
+    b.states[4 * (b.H + 2):] = gradients
+    got = b.backward(dy)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_a_graph_follows_the_weights_that_are_frozen():
+    """A graph of decode reads the codes and the scales where freeze writes them."""
+    b, g = _ready(4)
+    x = randn(g, 3, K).to(BF)
+    y = torch.empty_like(x)
+    b.decode(x, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.decode(x, y)
+    before = y.clone()
+    _move(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, before)
+    b.w_down.mul_(-2)
+    b.freeze()
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = y.clone()
+    assert torch.equal(b.decode(x), replayed) and not torch.equal(replayed, before)
