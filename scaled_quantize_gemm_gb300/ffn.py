@@ -68,6 +68,7 @@ class GatedFFN:
         self._buffers = {}                   # name -> the largest buffer so far, in bytes
         self._views = {}                     # name -> its last view
         self._kept = []                      # every buffer: a captured graph may replay on it
+        self._spaces = []                    # the workspaces among them
         self._saved = None
 
     # ------------------------------------------------------------ states and scratch
@@ -80,14 +81,17 @@ class GatedFFN:
         j = (i + 1) * sq.state_floats(self.H) - 1
         return (self.states if states is None else states)[j:j + 1]
 
-    def _bytes(self, name, nbytes, make):
+    def _bytes(self, name, nbytes, zero=False):
         """A buffer of at least `nbytes` that lives as long as the block.  A larger one than before is at least twice
         as large, so all the smaller ones together are no larger than it.  One that is made while a graph is being
         captured belongs to that graph (its memory, and what fills it, come with the replay) and is not handed on."""
         t = self._buffers.get(name)
         if t is None or t.numel() < nbytes:
-            t = make(max(nbytes, 0 if t is None else 2 * t.numel()), dtype=torch.uint8, device=self.states.device)
+            n = max(nbytes, 0 if t is None else 2 * t.numel())
+            t = (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=self.states.device)
             self._kept.append(t)
+            if zero:
+                self._spaces.append(t)
             if not _capturing():
                 self._buffers[name] = t
         return t
@@ -97,7 +101,7 @@ class GatedFFN:
         if v is not None and v.shape == shape and v.dtype is dtype:
             return v
         nbytes = math.prod(shape) * dtype.itemsize
-        t = self._bytes(name, nbytes, torch.empty)
+        t = self._bytes(name, nbytes)
         v = t[:nbytes].view(dtype).view(shape)
         if t is self._buffers.get(name):
             self._views[name] = v
@@ -105,7 +109,13 @@ class GatedFFN:
 
     def _workspace(self, name, nbytes):
         """scratch of the split products (zeroed when made, left so by every call)"""
-        return self._bytes(name, nbytes, torch.zeros) if nbytes else None
+        return self._bytes(name, nbytes, zero=True) if nbytes else None
+
+    def reset_workspaces(self):
+        """Zeroes the workspaces: to be called after ``fp8_device_status`` returned ERR_TIMEOUT, as a kernel that gave
+        up leaves its counters as they were, and later calls would join their sums too early or never."""
+        for t in self._spaces:
+            t.zero_()
 
     def calibrate(self, x):
         """One forward pass that sets the activations' and weights' scales from what it records."""

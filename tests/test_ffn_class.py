@@ -197,3 +197,25 @@ def test_decode_needs_codes(monkeypatch):
         b.decode(torch.zeros(3, K, dtype=BF))
     b.freeze()
     b.decode(torch.zeros(3, K, dtype=BF))
+
+
+# ---------------------------------------------------------------- after a wait that ran out
+def test_workspaces_can_be_zeroed_again(block, monkeypatch):
+    """A kernel that gave up leaves counters behind; the plain forms refuse a workspace that is not zero."""
+    b, r = block
+    b.freeze()
+    x = r(100, K).to(BF)
+    want = b.decode(x)
+    with monkeypatch.context() as mp:        # a workspace of a captured graph
+        mp.setattr(ffn, "_capturing", lambda: True)
+        b.decode(r(300, K).to(BF))
+    b.decode(r(120, K).to(BF))               # ... and one that a larger one has replaced
+    spaces = list(b._spaces)
+    assert len(spaces) >= 4
+    for t in spaces:
+        t[3] = 1
+    with pytest.raises(AssertionError, match="not zero"):
+        b.decode(x)
+    b.reset_workspaces()
+    assert torch.equal(b.decode(x), want)
+    assert not any(bool(t.any()) for t in spaces)

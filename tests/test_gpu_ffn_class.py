@@ -113,3 +113,22 @@ def test_a_graph_follows_the_weights_that_are_frozen():
     torch.cuda.synchronize()
     replayed = y.clone()
     assert torch.equal(b.decode(x), replayed) and not torch.equal(replayed, before)
+
+
+def test_decode_after_a_wait_that_ran_out():
+    """The status is read and cleared, the workspaces zeroed, and decode is right again."""
+    b, g = _ready(5)
+    x = randn(g, 3, K).to(BF)
+    want = b.decode(x).clone()
+    waited = torch.zeros(1, dtype=torch.int32, device=DEV)
+    assert sq.fp8_device_status(True) == sq.OK
+    side = torch.cuda.Stream()
+    for i in range(8):
+        sq.fp8_selftest_wait_timeout(30 + 20 * i, waited, stream=side)
+        for _ in range(20):
+            b.decode(x)
+        torch.cuda.synchronize()
+        assert sq.fp8_device_status(True) == sq.ERR_TIMEOUT
+        b.reset_workspaces()
+        assert torch.equal(b.decode(x), want)
+        assert sq.fp8_device_status(True) == sq.OK
