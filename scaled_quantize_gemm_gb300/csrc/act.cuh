@@ -152,9 +152,9 @@ __device__ __forceinline__ void act_fd2(float2 x, float2& f, float2& d)
         d = __ffma2_rn(__fmul2_rn(xc, f2(0.3989422804014327f)), ex, phi);
     } else {
         // At |x| = C the value on the negative side and the derivative's
-        // distance from 0 or 1 are below 2^-102: x is held there, so that
+        // distance from 0 or 1 are below 2^-115: x is held there, so that
         // exp(-u) stays finite and u', which grows as x^2, meets no 0 * inf.
-        constexpr float C = ACT == kActSilu ? 80.0f : 9.5f;
+        constexpr float C = ACT == kActSilu ? 86.0f : 9.95f;
         const float2 xn = max2_nan(x, -C);
         const float2 xc = min2_nan(xn, C);
         const float2 xx = __fmul2_rn(xc, xc);
