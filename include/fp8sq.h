@@ -420,7 +420,9 @@ FP8SQ_API int fp8_linear_fwd_noalloc(const void* x, const void* w, int64_t M, in
 /* ---- 5c. a feed-forward sublayer around the FP8 linear ----------------------
  * The pages stop at the linear layer; these are the operators a transformer's
  * feed-forward sublayer puts around it (te.LayerNorm and te.LayerNormMLP of
- * [TE] name the same parts).  Inputs and outputs must not overlap.
+ * [TE] name the same parts).  An output must not overlap any other buffer of
+ * the call (FP8SQ_ERR_INVALID_ARG), but for two in place exactly, the residual
+ * stream's: sum_out over residual or x, and D over a residual of its type.
  *
  * fp8_layernorm_fwd: s = x + residual (rounded to the type, written to
  *   sum_out; s = x without a residual), mu = sum(s)/K, var = sum((s - mu)^2)/K,

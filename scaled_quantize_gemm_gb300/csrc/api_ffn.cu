@@ -2,6 +2,7 @@
 // operators (include/fp8sq.h, section 5c).  Every argument is checked on the
 // host before anything is enqueued.
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_runtime.h>
 
 #include "../../include/fp8sq.h"
@@ -60,6 +61,36 @@ int check_operands(const char* fn, const uint8_t* A, int a_format, const float* 
     return FP8SQ_OK;
 }
 
+// A buffer of `bytes` bytes that a call reads, or writes (out).
+struct Span {
+    const char* name;
+    const void* p;
+    uint64_t bytes;
+    bool out;
+};
+// Refuses an output that overlaps another buffer of the call.  In place exactly
+// (the same bytes from first to last) are the pairs where each element is read
+// before it is written, by the thread that writes it: `into` over one of `over`.
+int check_overlap(const char* fn, std::initializer_list<Span> spans, const void* into = nullptr,
+                  std::initializer_list<const void*> over = {})
+{
+    for (const Span& a : spans) {
+        if (!a.out || !a.p || !a.bytes) continue;
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p);
+        for (const Span& b : spans) {
+            if (&a == &b || !b.p || !b.bytes) continue;
+            const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p);
+            if (a0 >= b0 + b.bytes || b0 >= a0 + a.bytes) continue;
+            bool in_place = false;
+            if (a.p == into && a0 == b0 && a.bytes == b.bytes && !b.out)
+                for (const void* o : over) in_place |= o == b.p;
+            if (!in_place) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, a.name, b.name);
+        }
+    }
+    return FP8SQ_OK;
+}
+uint64_t size_of(int dtype) { return dtype == FP8SQ_F32 ? 4 : 2; }
+
 }  // namespace
 
 extern "C" {
@@ -85,6 +116,12 @@ FP8SQ_API int fp8_layernorm_fwd(const void* x, const void* residual, int dtype, 
     int sms, r;
     if ((r = check_cast(fn, q_out, q_format, q_state, q_history_len))) return r;
     if ((r = fp8sq::api_check_device(&sms))) return r;
+    const uint64_t n = (uint64_t)M * (uint64_t)K, bytes = n * size_of(dtype), row = 4 * (uint64_t)M, col = 4 * (uint64_t)K;
+    if ((r = check_overlap(fn, {{"x", x, bytes, false}, {"residual", residual, bytes, false}, {"gamma", gamma, col, false},
+                                {"beta", beta, col, false}, {"sum_out", sum_out, bytes, true}, {"y", y, bytes, true},
+                                {"mu_out", mu_out, row, true}, {"rstd_out", rstd_out, row, true}, {"q_out", q_out, n, true}},
+                           sum_out, {residual, x})))
+        return r;
     fp8sq::LnArgs a;
     a.M = M;
     a.K = K;
@@ -131,6 +168,12 @@ FP8SQ_API int fp8_layernorm_bwd(const void* dy, const void* x, const void* dres,
     if (!aligned(workspace, 16)) return api_fail(FP8SQ_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", fn);
     int sms, r;
     if ((r = fp8sq::api_check_device(&sms))) return r;
+    const uint64_t bytes = (uint64_t)M * (uint64_t)K * size_of(dtype), row = 4 * (uint64_t)M, col = 4 * (uint64_t)K;
+    if ((r = check_overlap(fn, {{"dy", dy, bytes, false}, {"x", x, bytes, false}, {"dres", dres, bytes, false},
+                                {"gamma", gamma, col, false}, {"mu", mu, row, false}, {"rstd", rstd, row, false},
+                                {"dx", dx, bytes, true}, {"dgamma", dgamma, col, true}, {"dbeta", dbeta, col, true},
+                                {"workspace", workspace, need, true}})))
+        return r;
     fp8sq::LnArgs a;
     a.M = M;
     a.K = K;
@@ -179,6 +222,14 @@ FP8SQ_API int fp8_gemm_act(const uint8_t* A, int a_format, const float* a_scale,
     if (workspace && ws_bytes < need) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, need);
     int sms;
     if ((r = fp8sq::api_check_device(&sms))) return r;
+    const uint64_t n = (uint64_t)M * (uint64_t)N;
+    if ((r = check_overlap(fn, {{"A", A, (uint64_t)M * (uint64_t)K, false}, {"B", B, (uint64_t)N * (uint64_t)K, false},
+                                {"a_scale", a_scale, 4, false}, {"b_scale", b_scale, 4, false},
+                                {"bias", bias, 4 * (uint64_t)N, false}, {"residual", residual, n * size_of(res_dtype), false},
+                                {"z_out", z_out, 2 * n, true}, {"D", D, n * size_of(d_dtype), true}, {"q_out", q_out, n, true},
+                                {"workspace", workspace, need, true}},
+                           D, {residual})))
+        return r;
     fp8sq::FfnArgs a;
     a.kind = fp8sq::kFfnAct;
     a.M = M;
@@ -223,6 +274,12 @@ FP8SQ_API int fp8_glu_fwd(const uint8_t* A, int a_format, const float* a_scale, 
     if (workspace && ws_bytes < need) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, need);
     int sms;
     if ((r = fp8sq::api_check_device(&sms))) return r;
+    const uint64_t n = (uint64_t)M * (uint64_t)F;
+    if ((r = check_overlap(fn, {{"A", A, (uint64_t)M * (uint64_t)K, false}, {"W", W, 2 * (uint64_t)F * (uint64_t)K, false},
+                                {"a_scale", a_scale, 4, false}, {"w_scale", w_scale, 4, false},
+                                {"gu_out", gu_out, 4 * n, true}, {"h_out", h_out, 2 * n, true}, {"q_out", q_out, n, true},
+                                {"workspace", workspace, need, true}})))
+        return r;
     fp8sq::FfnArgs a;
     a.kind = fp8sq::kFfnGlu;
     a.M = M;
@@ -259,6 +316,11 @@ FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scal
     if ((r = check_cast(fn, q_dgu, q_format, q_state, q_history_len))) return r;
     int sms;
     if ((r = fp8sq::api_check_device(&sms))) return r;
+    const uint64_t n = (uint64_t)M * (uint64_t)F;
+    if ((r = check_overlap(fn, {{"dY", dY, (uint64_t)M * (uint64_t)K, false}, {"Wd", Wd, (uint64_t)K * (uint64_t)F, false},
+                                {"dy_scale", dy_scale, 4, false}, {"w_scale", w_scale, 4, false}, {"gu", gu, 4 * n, false},
+                                {"q_dgu", q_dgu, 2 * n, true}})))
+        return r;
     fp8sq::FfnArgs a;
     a.kind = fp8sq::kFfnGluBwd;
     a.M = M;
@@ -305,6 +367,11 @@ FP8SQ_API int fp8_act_bwd(const void* dy, const void* z, int64_t M, int64_t N, i
     if (!aligned(workspace, 16)) return api_fail(FP8SQ_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", fn);
     int sms;
     if ((r = fp8sq::api_check_device(&sms))) return r;
+    const uint64_t n = (uint64_t)M * (uint64_t)N;
+    if ((r = check_overlap(fn, {{"dy", dy, 2 * n, false}, {"z", z, 2 * n, false}, {"dbias", dbias, 4 * (uint64_t)N, true},
+                                {"dz_out", dz_out, 2 * n, true}, {"q_out", q_out, n, true},
+                                {"workspace", workspace, need, true}})))
+        return r;
     fp8sq::ActBwdArgs a;
     a.M = M;
     a.N = N;

@@ -38,7 +38,7 @@ struct FfnParams {
     const float* sB;
     int act;
     const float* bias;       // [N] or null
-    const void* res;         // [M][N] or null
+    const void* res;         // [M][N] or null; may be D itself (read coherently, before the same thread writes)
     int res_f32;
     void* D;                 // [M][N] or null
     int d_f32;
@@ -188,25 +188,40 @@ struct Stager {
     }
 };
 
-// a whole 32-byte sector in one load (16-byte loads by row take each twice)
+// a whole 32-byte sector in one load (16-byte loads by row take each twice).
+// RO: through the read-only path; not the residual, which the call may be
+// overwriting in place (other elements of it, at the time).
+template <bool RO>
 __device__ __forceinline__ void ldg32(uint4& a, uint4& b, const void* p)
 {
-    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-        : "l"(p));
+    if constexpr (RO)
+        asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+            : "l"(p));
+    else
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p)
+                     : "memory");
+}
+template <bool RO>
+__device__ __forceinline__ uint4 ldg16(const uint4* p)
+{
+    if constexpr (RO) return __ldg(p);
+    else return *p;
 }
 // 32 columns of a row of bf16 (64 bytes) or fp32 (128 bytes) into registers,
 // ahead of their use; zeros past `bytes_left`
-template <int N>
+template <int N, bool RO>
 __device__ __forceinline__ void fetch_row(uint4* raw, const void* src, int bytes_left)
 {
     const uint4* s = static_cast<const uint4*>(src);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        if (16 * (i + 2) <= bytes_left && (reinterpret_cast<uintptr_t>(src) & 31) == 0) ldg32(raw[i], raw[i + 1], s + i);
+        if (16 * (i + 2) <= bytes_left && (reinterpret_cast<uintptr_t>(src) & 31) == 0) ldg32<RO>(raw[i], raw[i + 1], s + i);
         else {
-            raw[i] = 16 * (i + 1) <= bytes_left ? __ldg(s + i) : make_uint4(0, 0, 0, 0);
-            raw[i + 1] = 16 * (i + 2) <= bytes_left ? __ldg(s + i + 1) : make_uint4(0, 0, 0, 0);
+            raw[i] = 16 * (i + 1) <= bytes_left ? ldg16<RO>(s + i) : make_uint4(0, 0, 0, 0);
+            raw[i + 1] = 16 * (i + 2) <= bytes_left ? ldg16<RO>(s + i + 1) : make_uint4(0, 0, 0, 0);
         }
     }
 }
@@ -405,13 +420,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             const int left = row < p.M ? min(p.N - col, 32) : 0;
             if constexpr (KIND == kEpiAct) {
                 if (!p.res) return;
-                if (p.res_f32) fetch_row<8>(pre, static_cast<const float*>(p.res) + (int64_t)row * p.N + col, 4 * left);
-                else fetch_row<4>(pre, static_cast<const __nv_bfloat16*>(p.res) + (int64_t)row * p.N + col, 2 * left);
+                if (p.res_f32) fetch_row<8, false>(pre, static_cast<const float*>(p.res) + (int64_t)row * p.N + col, 4 * left);
+                else fetch_row<4, false>(pre, static_cast<const __nv_bfloat16*>(p.res) + (int64_t)row * p.N + col, 2 * left);
             } else if constexpr (KIND == kEpiGluBwd) {
                 // 16 columns of g, then of u
                 const __nv_bfloat16* s = p.gu + (int64_t)row * 2 * p.N + col;
-                fetch_row<2>(pre, s, 2 * left);
-                fetch_row<2>(pre + 2, s + p.N, 2 * left);
+                fetch_row<2, true>(pre, s, 2 * left);
+                fetch_row<2, true>(pre + 2, s + p.N, 2 * left);
             }
         };
         int lt = 0;
@@ -656,11 +671,11 @@ __device__ __forceinline__ void rows_residual(const FfnParams& p, int m0, int n,
     if (p.res_f32) {
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            if (m0 + j < p.M) r[j] = __ldg(static_cast<const uint32_t*>(p.res) + (int64_t)(m0 + j) * p.N + n);
+            if (m0 + j < p.M) r[j] = static_cast<const uint32_t*>(p.res)[(int64_t)(m0 + j) * p.N + n];
     } else {
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            if (m0 + j < p.M) r[j] = __ldg(static_cast<const uint16_t*>(p.res) + (int64_t)(m0 + j) * p.N + n);
+            if (m0 + j < p.M) r[j] = static_cast<const uint16_t*>(p.res)[(int64_t)(m0 + j) * p.N + n];
     }
 }
 

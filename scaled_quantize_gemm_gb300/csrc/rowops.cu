@@ -65,11 +65,11 @@ __device__ __forceinline__ void record_amax(float amax, float* state)
 
 // ------------------------------------------------------------------ any row length
 template <typename T>
-__global__ void __launch_bounds__(256) k_ln_fwd_any(const T* x, const T* __restrict__ res,
-                                                    const float* __restrict__ gamma, const float* __restrict__ beta,
-                                                    float eps, int64_t R, int64_t K, T* sum, T* __restrict__ y,
-                                                    float* __restrict__ mu, float* __restrict__ rstd,
-                                                    uint8_t* __restrict__ q, int fmt, float* qstate, int H)
+__global__ void __launch_bounds__(256) k_ln_fwd_any(const T* x, const T* res, const float* __restrict__ gamma,
+                                                    const float* __restrict__ beta, float eps, int64_t R, int64_t K,
+                                                    T* sum, T* __restrict__ y, float* __restrict__ mu,
+                                                    float* __restrict__ rstd, uint8_t* __restrict__ q, int fmt,
+                                                    float* qstate, int H)
 {
     pdl_enter();
     __shared__ float red[8];
@@ -329,6 +329,8 @@ __device__ __forceinline__ float2 block_total2(const float (*red)[32], int span)
 // at most MAXT threads, 1536 threads (six CTAs at 4096 columns: 82 us for 16384
 // rows in bf16 with residual, 96 % of the copy rate; four 93, eight 105).
 constexpr int kLnCols = 16;         // columns a thread holds
+// sum may be res or x itself (a thread reads both where it writes, and before),
+// so none of the three is declared free of aliases.
 // CODES: y also (or only) as FP8 codes under a delayed state, cast from fp32.
 struct LnCast {
     uint8_t* q;
@@ -337,9 +339,8 @@ struct LnCast {
 };
 template <typename T, int VEC, int MAXT, int MINB, bool CODES>
 __global__ void __launch_bounds__(MAXT, MINB)
-    k_ln_fwd(const T* __restrict__ x, const T* __restrict__ res, const float* __restrict__ gamma,
-             const float* __restrict__ beta, float eps, int64_t R, int K, T* __restrict__ sum, T* __restrict__ y,
-             float* __restrict__ mu, float* __restrict__ rstd, LnCast cast)
+    k_ln_fwd(const T* x, const T* res, const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
+             int64_t R, int K, T* sum, T* __restrict__ y, float* __restrict__ mu, float* __restrict__ rstd, LnCast cast)
 {
     constexpr int NV = kLnCols / VEC;
     using P = Pack<T, VEC>;
