@@ -181,6 +181,8 @@ class GatedFFN:
         M, K, F, H = x.shape[0], self.K, self.F, self.H
         if M % 16:
             raise ValueError(f"a training step takes a multiple of 16 tokens, got {M}")
+        if dy.shape != x.shape or dy.dtype != x.dtype or not dy.is_contiguous():
+            raise ValueError(f"dy: {tuple(dy.shape)} {dy.dtype}, the forward had {tuple(x.shape)} {x.dtype} (contiguous)")
         self._saved = None
         dev = x.device
         qdy, qdgu = self._get("qdy", (M, K), torch.uint8), self._get("qdgu", (M, 2 * F), torch.uint8)

@@ -219,3 +219,18 @@ def test_workspaces_can_be_zeroed_again(block, monkeypatch):
     b.reset_workspaces()
     assert torch.equal(b.decode(x), want)
     assert not any(bool(t.any()) for t in spaces)
+
+
+# ---------------------------------------------------------------- refusals
+def test_a_gradient_of_another_form_is_refused_before_anything_runs(block):
+    b, r = block
+    x, dy = r(M, K).to(BF), r(M, K).to(BF)
+    b.forward(x)
+    want = b.backward(dy)
+    b.forward(x)
+    states = b.states.clone()
+    for bad in (r(M - 1, K).to(BF), r(M, K), r(K, M).to(BF).T, r(M * K).to(BF)):
+        with pytest.raises(ValueError, match="dy"):
+            b.backward(bad)
+    assert torch.equal(b.states, states)
+    assert _same(b.backward(dy), want)
