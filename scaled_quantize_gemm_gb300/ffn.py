@@ -59,12 +59,13 @@ class GatedFFN:
         self.gamma, self.beta, self.w_gate_up, self.w_down = gamma, beta, w_gate_up, w_down
         self.K, self.F, self.act, self.eps, self.H = K, F2 // 2, act, eps, history_len
         dev = w_gate_up.device
-        self.states = torch.empty(6 * sq.state_floats(history_len), device=dev)
+        self._states = torch.empty(6 * sq.state_floats(history_len), device=dev)
         sq.fp8_scale_init(self.states, 6, history_len)
         self.q_gate_up = torch.empty((F2, K), dtype=torch.uint8, device=dev)
         self.q_down = torch.empty((K, self.F), dtype=torch.uint8, device=dev)
         self._frozen = torch.empty_like(self.states)     # the states as they were when the weights were last cast
         self._cast = False                   # ... which they have been
+        self._live, self._kept_scales = self._split(self.states), self._split(self._frozen)
         self._buffers = {}                   # name -> the largest buffer so far, in bytes
         self._views = {}                     # name -> its last view
         self._kept = []                      # every buffer: a captured graph may replay on it
@@ -72,14 +73,25 @@ class GatedFFN:
         self._saved = None
 
     # ------------------------------------------------------------ states and scratch
-    def _state(self, i, states=None):
-        n = sq.state_floats(self.H)
-        return (self.states if states is None else states)[i * n:(i + 1) * n]
+    @property
+    def states(self):
+        """the six delayed-scaling states, one after another; assigning copies into them (views and graphs hold them)"""
+        return self._states
 
-    def _scale(self, i, states=None):
-        """the dequantisation step of a state's codes (one element)"""
-        j = (i + 1) * sq.state_floats(self.H) - 1
-        return (self.states if states is None else states)[j:j + 1]
+    @states.setter
+    def states(self, values):
+        self._states.copy_(values)
+
+    def _split(self, states):
+        """the six states and the dequantisation steps of their codes (one element each), as views"""
+        blocks = states.view(6, sq.state_floats(self.H))
+        return list(blocks), list(blocks[:, -1:])
+
+    def _state(self, i):
+        return self._live[0][i]
+
+    def _scale(self, i):
+        return self._live[1][i]
 
     def _bytes(self, name, nbytes, zero=False):
         """A buffer of at least `nbytes` that lives as long as the block.  A larger one than before is at least twice
@@ -135,19 +147,20 @@ class GatedFFN:
         self._cast = True
 
     # ------------------------------------------------------------ one pass
-    def _run(self, x, gu, mu, rstd, y, codes, states):
-        """One pass with the activations' scales in `states`; `codes` names the buffers of n's and h's codes: a
-        training step's are read again by its backward pass, so nothing else may write them."""
+    def _run(self, x, gu, mu, rstd, y, codes, scales):
+        """One pass with the activations' states and steps in `scales`; `codes` names the buffers of n's and h's
+        codes: a training step's are read again by its backward pass, so nothing else may write them."""
         M, K, F, H = x.shape[0], self.K, self.F, self.H
-        s_gu, s_down = self._scale(W_GU, self._frozen), self._scale(W_DOWN, self._frozen)
+        state, step = scales
+        w_step = self._kept_scales[1]
         qn, qh = self._get("qn" + codes, (M, K), torch.uint8), self._get("qh" + codes, (M, F), torch.uint8)
         sq.fp8_layernorm_fwd(x, self.gamma, self.beta, self.eps, None, mu=mu, rstd=rstd, q_out=qn, q_format=sq.E4M3,
-                             q_state=self._state(N, states), history_len=H)
-        sq.fp8_glu_fwd(qn, sq.E4M3, self._scale(N, states), self.q_gate_up, sq.E4M3, s_gu, self.act, gu_out=gu,
-                       q_out=qh, q_format=sq.E4M3, q_state=self._state(H_, states), history_len=H,
+                             q_state=state[N], history_len=H)
+        sq.fp8_glu_fwd(qn, sq.E4M3, step[N], self.q_gate_up, sq.E4M3, w_step[W_GU], self.act, gu_out=gu, q_out=qh,
+                       q_format=sq.E4M3, q_state=state[H_], history_len=H,
                        workspace=self._workspace("ws_gu", sq.fp8_glu_fwd_workspace_bytes(M, F, K)))
-        sq.fp8_gemm_act(qh, sq.E4M3, self._scale(H_, states), self.q_down, sq.E4M3, s_down, sq.ACT_NONE, D=y,
-                        residual=x, workspace=self._workspace("ws_down", sq.fp8_gemm_act_workspace_bytes(M, K, F)))
+        sq.fp8_gemm_act(qh, sq.E4M3, step[H_], self.q_down, sq.E4M3, w_step[W_DOWN], sq.ACT_NONE, D=y, residual=x,
+                        workspace=self._workspace("ws_down", sq.fp8_gemm_act_workspace_bytes(M, K, F)))
         return qn, qh
 
     def decode(self, x, y=None):
@@ -156,7 +169,7 @@ class GatedFFN:
         if not self._cast:
             raise RuntimeError("decode needs the weights' codes: call freeze (or forward) first")
         y = torch.empty_like(x) if y is None else y
-        self._run(x, None, None, None, y, "_decode", self._frozen)
+        self._run(x, None, None, None, y, "_decode", self._kept_scales)
         return y
 
     def forward(self, x):
@@ -166,7 +179,7 @@ class GatedFFN:
         gu = self._get("gu", (M, 2 * self.F), torch.bfloat16)
         mu, rstd = self._get("mu", (M,), torch.float32), self._get("rstd", (M,), torch.float32)
         y = torch.empty_like(x)
-        qn, qh = self._run(x, gu, mu, rstd, y, "", self.states)
+        qn, qh = self._run(x, gu, mu, rstd, y, "", self._live)
         cast = self._get("cast", self.states.shape, torch.float32)       # the scales of qn and qh
         cast.copy_(self.states)
         self._saved = (x, gu, mu, rstd, qn, qh, cast)
@@ -185,20 +198,19 @@ class GatedFFN:
             raise ValueError(f"dy: {tuple(dy.shape)} {dy.dtype}, the forward had {tuple(x.shape)} {x.dtype} (contiguous)")
         self._saved = None
         dev = x.device
+        w_step, step = self._kept_scales[1], self._split(cast)[1]
         qdy, qdgu = self._get("qdy", (M, K), torch.uint8), self._get("qdgu", (M, 2 * F), torch.uint8)
         sq.fp8_quantize(dy, sq.E5M2, sq.TENSOR, qdy, delayed_state=self._state(DY), history_len=H)
-        sq.fp8_glu_bwd(qdy, sq.E5M2, self._scale(DY), self.q_down, sq.E4M3,
-                       self._scale(W_DOWN, self._frozen), gu, self.act, qdgu, sq.E5M2, self._state(DGU), H)
+        sq.fp8_glu_bwd(qdy, sq.E5M2, self._scale(DY), self.q_down, sq.E4M3, w_step[W_DOWN], gu, self.act, qdgu,
+                       sq.E5M2, self._state(DGU), H)
         dn = self._get("dn", (M, K), torch.bfloat16)
         dw_gu = torch.empty((2 * F, K), device=dev)
         dw_down = torch.empty((K, F), device=dev)
         s_dy, s_dgu = self._scale(DY), self._scale(DGU)
-        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.K_MAJOR, self.q_gate_up, sq.E4M3,
-                           self._scale(W_GU, self._frozen), sq.MN_MAJOR, dn, M, K, 2 * F)
-        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.MN_MAJOR, qn, sq.E4M3, self._scale(N, cast), sq.MN_MAJOR, dw_gu,
-                           2 * F, K, M)
-        sq.fp8_gemm_layout(qdy, sq.E5M2, s_dy, sq.MN_MAJOR, qh, sq.E4M3, self._scale(H_, cast), sq.MN_MAJOR, dw_down, K,
-                           F, M)
+        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.K_MAJOR, self.q_gate_up, sq.E4M3, w_step[W_GU], sq.MN_MAJOR, dn,
+                           M, K, 2 * F)
+        sq.fp8_gemm_layout(qdgu, sq.E5M2, s_dgu, sq.MN_MAJOR, qn, sq.E4M3, step[N], sq.MN_MAJOR, dw_gu, 2 * F, K, M)
+        sq.fp8_gemm_layout(qdy, sq.E5M2, s_dy, sq.MN_MAJOR, qh, sq.E4M3, step[H_], sq.MN_MAJOR, dw_down, K, F, M)
         dx, dgamma, dbeta = torch.empty_like(x), torch.empty(K, device=dev), torch.empty(K, device=dev)
         ws = self._get("ws_ln", (max(16, sq.fp8_layernorm_bwd_workspace_bytes(M, K)),), torch.uint8)
         sq.fp8_layernorm_bwd(dn, x, self.gamma, mu, rstd, dx, dgamma, dbeta, ws, dres=dy)

@@ -221,6 +221,20 @@ def test_workspaces_can_be_zeroed_again(block, monkeypatch):
     assert not any(bool(t.any()) for t in spaces)
 
 
+def test_states_of_a_checkpoint(block):
+    """Assigned or copied, they are what the next step and the next freeze take."""
+    b, r = block
+    x, saved = r(7, K).to(BF), b.states.clone()
+    b.freeze()
+    want = b.decode(x)
+    where = b.states.data_ptr()
+    _move(b)
+    b.states = saved
+    assert b.states.data_ptr() == where and torch.equal(b.states, saved)
+    b.freeze()
+    assert torch.equal(b.decode(x), want)
+
+
 # ---------------------------------------------------------------- refusals
 def test_a_gradient_of_another_form_is_refused_before_anything_runs(block):
     b, r = block
