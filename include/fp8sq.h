@@ -519,8 +519,8 @@ FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scal
 /* ---- 6. diagnostics --------------------------------------------------------
  * fp8_device_status: synchronises the current device and returns
  *   FP8SQ_ERR_TIMEOUT if any bounded device-side wait of this library ran out
- *   since the last clear (the kernel that hit it wrote nothing further and
- *   returned), FP8SQ_OK otherwise.  clear != 0 resets the word.  While the
+ *   since the last clear, FP8SQ_OK otherwise.  The kernel that hit it stopped and
+ *   returned; what it and the kernels beside it wrote is not to be used.  clear != 0 resets the word.  While the
  *   word is set, GEMM kernels return early without computing.
  * fp8_selftest_wait_timeout: exercises that failure path on purpose, with
  *   no fault and no hang: one thread waits, through the library's bounded

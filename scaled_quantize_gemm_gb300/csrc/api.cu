@@ -213,7 +213,7 @@ FP8SQ_API const char* fp8_last_error(void) { return g_msg; }
 
 FP8SQ_API int fp8_device_status(int clear)
 {
-    // the GEMM kernels are the ones with device-side waits (the casts have none)
+    // set by the products' waits and by those of the LayerNorm backward's row copies (the casts have none)
     const int v = fp8sq::read_device_error(clear);
     if (v < 0) return fail(FP8SQ_ERR_CUDA, "cannot read the device error word");
     if (v) return fail(FP8SQ_ERR_TIMEOUT, "a bounded device-side wait ran out");

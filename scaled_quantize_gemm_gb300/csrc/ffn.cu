@@ -248,9 +248,10 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 // by the epilogue where it is short: an accumulator's 128 x 256 values a CTA take
 // about 8 us through eight warps (gelu, z and codes), which the MMAs of the next
 // tile cover from K of about 3000 on.
-// One GB300, us: glu_fwd 16384 x 4096 -> 2 x 14336 with g, u and codes 1050
-// (3670 TFLOP/s); gemm_act 16384 x 4096 -> 14336 with bias, gelu_tanh, z and codes
-// 560-600; glu_bwd 2048 x 4096 -> 14336 86.
+// One GB300, us, a few passes on a cool GPU / back to back at the power limit:
+// glu_fwd 16384 x 4096 -> 2 x 14336 with g, u and codes 1040-1070 / 1170-1240 (3640 /
+// 3200 TFLOP/s); gemm_act 16384 x 4096 -> 14336 with bias, gelu_tanh, z and codes
+// 553-569 / 632-667; glu_bwd 2048 x 4096 -> 14336 86 (under the profiler).
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1)
     k_ffn_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FfnParams p,
@@ -609,9 +610,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
 // of one accumulator; the pair meets in shared memory (a whole tile) or in the
 // partial sums.
 // One GB300, us, weights from DRAM: gated block 4096 -> 2 x 14336, one token
-// 23.2 (117 MB; a kernel that does nothing but load the same boxes takes 22.6),
-// 64 tokens 26.4; 14336 -> 4096 with residual, one token 14.6 (59 MB; loads
-// alone 12.4; from about 48 tokens k_ffn_ksplit is faster).
+// 22.6-23.1 (117 MB; a probe that did nothing but load the same boxes took
+// 22.6), 64 tokens 26.4; 14336 -> 4096 with residual, one token 14.4 (59 MB; the
+// probe 12.4; from about 48 tokens k_ffn_ksplit is faster).
 //   warp 0 producer, warp 1 MMA, warps 2-17 epilogue (TMEM lane = weight row,
 //   four warps per lane quarter, each a quarter of the tokens)
 // A lane of a finishing warp holds one output column, so a token's stores are

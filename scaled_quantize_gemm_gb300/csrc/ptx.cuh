@@ -17,10 +17,13 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p)
 // Programmatic dependent launch.  Kernels are launched with programmatic
 // stream serialisation (launch_k), so a kernel's launch is processed while
 // the previous kernel on the stream runs and its CTAs are placed as that
-// kernel's CTAs exit.  Every kernel of this library starts with pdl_enter(),
-// which waits until every kernel it depends on has completed with its memory
-// operations visible, so the kernel's reads and writes keep plain stream
-// order.  Kernels do not trigger their dependents early
+// kernel's CTAs exit.  Every kernel of this library calls pdl_enter() before it
+// reads or writes anything that another kernel may touch; it waits until every
+// kernel it depends on has completed with its memory operations visible, so
+// reads and writes keep plain stream order.  Most call it first; the
+// feed-forward products and the LayerNorms initialise barriers, allocate tensor
+// memory and prefetch weights into L2 (where all SMs meet) ahead of it.
+// Kernels do not trigger their dependents early
 // (griddepcontrol.launch_dependents; but see pdl_trigger): measured on the GB300, an early
 // trigger let chains of waiting CTAs build up behind the persistent GEMMs
 // (a fine-grained backward took 278 us with it, 239 us without, 248 us with
@@ -350,10 +353,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cl_addr)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 // The same without release semantics, for a barrier that hands over tensor
-// memory only: tcgen05.wait::ld has completed the reads and
-// tcgen05.fence::before_thread_sync orders them before the arrival, so the
-// thread's global stores need not be waited for (a release at cluster scope
-// puts a memory barrier behind them).
+// memory only, and no memory.  The order of tcgen05 operations between threads
+// is the tcgen05 fences' own: PTX defines before_thread_sync to order what came
+// before it (here reads that wait::ld has completed) against the execution
+// ordering operations that follow, and after_thread_sync on the other side
+// likewise; its example hands over through a relaxed store and a relaxed load.
+// A release would only add the thread's global stores, which nobody on the other
+// side reads (at cluster scope it puts a memory barrier behind them).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cl_addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
