@@ -424,8 +424,8 @@ def _ws(t) -> tuple:
 
 def fp8_layernorm_fwd(x, gamma, beta, eps: float, y, mu=None, rstd=None, residual=None, sum_out=None, q_out=None,
                       q_format: int = E4M3, q_state=None, history_len: int = 0, stream=None) -> None:
-    """y = LayerNorm(x) gamma + beta; with a residual, of sum_out = x + residual; with q_out, y's FP8 codes under
-    the delayed state q_state (y may then be None)."""
+    """y = LayerNorm(x) gamma + beta; with a residual, of sum_out = x + residual (which may be residual or x itself);
+    with q_out, y's FP8 codes under the delayed state q_state (y may then be None)."""
     T = _t()
     px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
     dt = x.dtype
@@ -488,7 +488,8 @@ def _operands(A, a_scale, B, b_scale, names) -> tuple:
 def fp8_gemm_act(A, a_format: int, a_scale, B, b_format: int, b_scale, act: int, D=None, bias=None, residual=None,
                  z_out=None, q_out=None, q_format: int = E4M3, q_state=None, history_len: int = 0, workspace=None,
                  stream=None) -> None:
-    """y = act(z) + residual, z = A B^T sA sB + bias, into D (bf16 / fp32) and / or FP8 codes q_out; z into z_out."""
+    """y = act(z) + residual, z = A B^T sA sB + bias, into D (bf16 / fp32; it may be the residual itself) and / or FP8
+    codes q_out; z into z_out."""
     T = _t()
     pa, M, K, sa, pb, N, kb, sb = _operands(A, a_scale, B, b_scale, ("A", "B"))
     if kb != K:

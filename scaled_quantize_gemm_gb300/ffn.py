@@ -164,8 +164,8 @@ class GatedFFN:
         return qn, qh
 
     def decode(self, x, y=None):
-        """y for any number of tokens, on the frozen weights and scales; keeps nothing for a backward pass and leaves
-        the training step's statistics alone."""
+        """y (which may be x itself) for any number of tokens, on the frozen weights and scales; keeps nothing for a
+        backward pass and leaves the training step's statistics alone."""
         if not self._cast:
             raise RuntimeError("decode needs the weights' codes: call freeze (or forward) first")
         y = torch.empty_like(x) if y is None else y

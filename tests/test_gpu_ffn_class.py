@@ -117,6 +117,16 @@ def test_a_graph_follows_the_weights_that_are_frozen():
     assert torch.equal(b.decode(x), replayed) and not torch.equal(replayed, before)
 
 
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_decode_in_place(M):
+    b, g = _ready(6)
+    x = randn(g, M, K).to(BF)
+    want = b.decode(x)
+    b.decode(x, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x, want)
+
+
 def test_decode_after_a_wait_that_ran_out():
     """The status is read and cleared, the workspaces zeroed, and decode is right again."""
     b, g = _ready(5)
