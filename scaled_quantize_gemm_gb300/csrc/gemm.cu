@@ -365,19 +365,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                     }
                 }
             }
-            if (aborted) pair_stop(s_stop, rank, issued);
-            // the copies complete on the leader's barriers; whoever gives up a
-            // wait from here on, none of them is in flight any more
-            if (rank == 0) drain_ring<STAGES>(full, issued);
-            if (!aborted) {
-                for (int i = 0; i < STAGES; ++i) {     // every stage's last release has landed
-                    if (!wait_bounded_cluster(&empty[stage], phase ^ 1u)) break;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+            if (__builtin_expect(aborted, 0)) pair_stop(s_stop, rank, issued);
+            bool released = !aborted;
+            for (int i = 0; i < STAGES && released; ++i) {     // every stage's last release has landed
+                released = wait_bounded_cluster(&empty[stage], phase ^ 1u);
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
+            // (else the copies, which complete on the leader's barriers)
+            if (__builtin_expect(!released && rank == 0, 0)) drain_ring<STAGES>(full, issued);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -417,13 +415,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
                 }
                 if (!aborted) mma_pair_commit(&afull[b], 3);
             }
-            mma_pair_commit(drain, 1);                  // completes once every issued MMA is done
-            wait_drain(drain, 0);
-            if (!aborted) {
-                for (int j = 0; j < 2; ++j) {           // both accumulators' last releases have landed
-                    const int l2 = lt + j;
-                    if (!wait_bounded_cluster(&aempty[l2 & 1], ((uint32_t)(l2 >> 1) & 1u) ^ 1u)) break;
-                }
+            bool released = !aborted;
+            for (int j = 0; j < 2 && released; ++j) {       // both accumulators' last releases have landed
+                const int l2 = lt + j;
+                released = wait_bounded_cluster(&aempty[l2 & 1], ((uint32_t)(l2 >> 1) & 1u) ^ 1u);
+            }
+            if (__builtin_expect(!released, 0)) {
+                mma_pair_commit(drain, 1);                  // completes once every issued MMA is done
+                wait_drain(drain, 0);
             }
         }
     } else {
@@ -520,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     }
     __syncthreads();
     cluster_sync_all();
-    if (s_stop[0] >= 0) {                      // (the same in both CTAs)
+    if (__builtin_expect(s_stop[0] >= 0, 0)) {                      // (the same in both CTAs)
         const int total = num_tiles > cid ? (num_tiles - cid + ncl - 1) / ncl * nkb : 0;
         if (rank == 0 && threadIdx.x == 0) drain_odd<STAGES>(full, s_stop, total, (uint32_t)L::STAGE);
         cluster_sync_all();

@@ -104,7 +104,8 @@ struct Smem {
 // ------------------------------------------------------------------ giving up
 // A producer's or an MMA thread's last act, whether or not a wait of its own
 // ran out: another warp of the CTA may leave as soon as the error word is set,
-// so a CTA exits only after its copies and its MMAs are known to be done.
+// so a CTA exits only after its copies and its MMAs are known to be done (which
+// the last releases of a pair's stages and accumulators say too).
 // Issue i of a ring went to stage i % STAGES in phase i / STAGES.
 
 // waits (with a limit) for the last `issued` copies of a ring

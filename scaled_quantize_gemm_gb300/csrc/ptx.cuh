@@ -140,6 +140,7 @@ __device__ __forceinline__ bool wait_bounded_err(uint64_t* bar, uint32_t parity,
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity)
 {
     const uint32_t a = smem_addr(bar);
+    if (mbar_try_wait(a, parity)) return;
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(a, parity))
         if (global_timer_ns() - t0 > 100000000ull) return;
