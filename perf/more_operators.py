@@ -336,7 +336,7 @@ def _run_own(s):
             p = s["plan"] = torch.empty(sq.fp8_expert_plan_ints(T, k, E), dtype=torch.int32, device="cuda")
         sq.fp8_expert_plan(s["ids"], E, p)
         sq.fp8_expert_dispatch(s["x"], p, k, E, s["rows"])
-        offsets, counts, row_of, _ = sq.expert_plan_views(p, T, k, E)
+        offsets, counts, row_of = sq.expert_plan_views(p, T, k, E)
         rows = s["rows"].view(F8["e4m3"]) if c["dtype"] == "codes" else s["rows"]
         return {"rows": rows, "offsets": offsets, "counts": counts, "row_of": row_of}
     p = _plan(s)
