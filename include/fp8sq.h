@@ -516,6 +516,103 @@ FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scal
                           const float* w_scale, int64_t M, int64_t F, int64_t K, const void* gu, int act,
                           uint8_t* q_dgu, int q_format, float* q_state, int q_history_len, void* stream);
 
+/* ---- 5d. RMSNorm, and a sublayer of experts -----------------------------------
+ * As in 5c, an output must not overlap any other buffer of the call, but for the
+ * residual stream in place (sum_out over residual or x, y of the combination
+ * over its residual).
+ *
+ * fp8_rmsnorm_fwd: s = x + residual (rounded to the type, written to sum_out;
+ *   s = x without a residual), rstd = 1/sqrt(sum(s^2)/K + eps), y = s rstd gamma,
+ *   in fp32.
+ *     dtype         of x, residual, sum_out, y [M][K]: BF16 or F32
+ *     residual, sum_out  both or neither
+ *     rstd_out      f32 [M] or NULL (the backward pass needs it)
+ *     q_out         u8 [M][K] or NULL: the codes of the fp32 y in q_format; y may
+ *                   then be NULL.  Their scale, q_gran:
+ *       TENSOR             the delayed state q_state (max|y| into q_state[0])
+ *       TILE_1x128         scales_out f32 [M][K/128]              (K % 128 == 0)
+ *       MX32               scales_out u8 [M][K/32]                (K % 32 == 0)
+ *       TILE_1x128_POW2, MX32_TILED, MX32_FLOOR_TILED  scales_out u8, the tiled
+ *                          layout                            (M, K % 128 == 0)
+ *     each by the rule of fp8_quantize on the fp32 y.
+ *   Any M >= 0 and K >= 1 otherwise; buffers 16-byte aligned.
+ * fp8_rmsnorm_bwd: with xh = x rstd and w = dy gamma,
+ *   dx = rstd (w - xh mean(w xh)) + dres, dgamma = sum over rows of dy xh (fp32,
+ *   in a fixed order).  x is what the forward normalised; the rest as in
+ *   fp8_layernorm_bwd.
+ *
+ * A routing gives each of T tokens k experts out of E: ids int32 [T][k]
+ * (an id outside [0, E) is no expert: that slot is left out).  The rows of
+ * an expert lie together, in the order of (token, slot), in buffers of
+ * R = fp8_expert_rows(T, k, E) rows; an expert's segment begins and ends on a
+ * multiple of 32 rows, and the rows that fill it up hold zeros: dispatch and
+ * combine_bwd write them so, and the products of zero rows are zero rows.  Rows
+ * behind the last segment are neither read nor written.
+ * fp8_expert_plan: writes the plan of a routing, int32 [fp8_expert_plan_ints],
+ *   16-byte aligned.  The first 2 E + 1 are offsets [E + 1] (the first row of each
+ *   expert, and the end of the last) and counts [E]; the last T k are the sorted
+ *   row of each slot or -1.  What lies between is the library's.  Every other call
+ *   takes the plan with the T, k, E it was made for.
+ *   1 <= k <= 64, 1 <= E <= 1024.
+ * fp8_expert_dispatch: out[row of (t, j)] = x[t], x [T][K] of elem_bytes 1, 2 or
+ *   4 an element; the gradient of x is fp8_expert_combine without weights.
+ * fp8_expert_combine: y[t] = residual[t] + sum over j of weights[t][j]
+ *   rows[row of (t, j)], in fp32 in the order of j, the residual last.  rows [R][K],
+ *   y and residual (or NULL) [T][K] of dtype; weights f32 [T][k], or NULL for ones.
+ * fp8_expert_combine_bwd: from dy [T][K] of dtype, for each slot with an expert:
+ *   drows = weights[t][j] dy[t], as drows [R][K] of dtype and / or as the codes
+ *   q_out [R][K] of the fp32 values under q_state; dweights[t][j] = sum over columns of
+ *   dy[t] rows[row] (fp32; 0 for a slot without an expert), f32 [T][k] or NULL (rows
+ *   may then be NULL).  At least one of the three.
+ *
+ * The experts' products, forms of fp8_glu_fwd, fp8_gemm_layout and fp8_glu_bwd on
+ * such rows; a_scale f32[1], b_scales f32 [E] (w_scales likewise), the rest as
+ * there:
+ * fp8_expert_glu_fwd: A [R][K], W [E][2F][K]; gu_out [R][2F], h_out / q_out [R][F].
+ * fp8_expert_gemm: D[r] = A[r] B_e^T: B [E][N][K] (K_MAJOR), or [E][K][N]
+ *   (MN_MAJOR: the data gradient on the forward's weights).  D bf16 or f32 [R][N].
+ * fp8_expert_glu_bwd: dY [R][K], Wd [E][K][F], gu [R][2F]; q_dgu [R][2F].
+ * fp8_expert_wgrad: D[e] = A_e^T B_e over the rows of expert e, A [R][M], B [R][N],
+ *   D bf16 or f32 [E][M][N], zeros for an expert without rows; b_scale f32[1].
+ *   Sizes: K % 16 == 0 and K > 0; N % 16 == 0 (F: 16); where the weights are read
+ *   MN-major K % 32 == 0; wgrad M % 32 == 0.  E 2F and E K below 2^31.
+ *   workspace  NULL, or fp8_expert_workspace_bytes(T, k, E, N, K) bytes (N = 2F for
+ *     the gated product), 256-byte aligned, zero before its first use, as in
+ *     fp8_gemm_act.
+ */
+FP8SQ_API int fp8_rmsnorm_fwd(const void* x, const void* residual, int dtype, const float* gamma, float eps, int64_t M,
+                              int64_t K, void* sum_out, void* y, float* rstd_out, uint8_t* q_out, int q_format,
+                              int q_gran, float* q_state, int q_history_len, void* scales_out, void* stream);
+FP8SQ_API size_t fp8_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
+FP8SQ_API int fp8_rmsnorm_bwd(const void* dy, const void* x, const void* dres, int dtype, const float* gamma,
+                              const float* rstd, int64_t M, int64_t K, void* dx, float* dgamma, void* workspace,
+                              size_t ws_bytes, void* stream);
+FP8SQ_API int64_t fp8_expert_rows(int64_t T, int k, int E);
+FP8SQ_API int64_t fp8_expert_plan_ints(int64_t T, int k, int E);
+FP8SQ_API int fp8_expert_plan(const int32_t* ids, int64_t T, int k, int E, int32_t* plan, void* stream);
+FP8SQ_API int fp8_expert_dispatch(const void* x, int elem_bytes, int64_t K, const int32_t* plan, int64_t T, int k, int E,
+                                  void* out, void* stream);
+FP8SQ_API int fp8_expert_combine(const void* rows, int dtype, int64_t K, const float* weights, const void* residual,
+                                 const int32_t* plan, int64_t T, int k, int E, void* y, void* stream);
+FP8SQ_API int fp8_expert_combine_bwd(const void* dy, int dtype, int64_t K, const void* rows, const float* weights,
+                                     const int32_t* plan, int64_t T, int k, int E, float* dweights, void* drows,
+                                     uint8_t* q_out, int q_format, float* q_state, int q_history_len, void* stream);
+FP8SQ_API size_t fp8_expert_workspace_bytes(int64_t T, int k, int E, int64_t N, int64_t K);
+FP8SQ_API int fp8_expert_glu_fwd(const uint8_t* A, int a_format, const float* a_scale, const uint8_t* W, int w_format,
+                                 const float* w_scales, const int32_t* plan, int64_t T, int k, int E, int64_t F, int64_t K,
+                                 int act, void* gu_out, void* h_out, uint8_t* q_out, int q_format, float* q_state,
+                                 int q_history_len, void* workspace, size_t ws_bytes, void* stream);
+FP8SQ_API int fp8_expert_gemm(const uint8_t* A, int a_format, const float* a_scale, const uint8_t* B, int b_format,
+                              const float* b_scales, int b_major, const int32_t* plan, int64_t T, int k, int E, int64_t N,
+                              int64_t K, void* D, int d_dtype, void* workspace, size_t ws_bytes, void* stream);
+FP8SQ_API int fp8_expert_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scale, const uint8_t* Wd, int w_format,
+                                 const float* w_scales, const int32_t* plan, int64_t T, int k, int E, int64_t F, int64_t K,
+                                 const void* gu, int act, uint8_t* q_dgu, int q_format, float* q_state, int q_history_len,
+                                 void* stream);
+FP8SQ_API int fp8_expert_wgrad(const uint8_t* A, int a_format, const float* a_scale, const uint8_t* B, int b_format,
+                               const float* b_scale, const int32_t* plan, int64_t T, int k, int E, int64_t M, int64_t N,
+                               void* D, int d_dtype, void* stream);
+
 /* ---- 6. diagnostics --------------------------------------------------------
  * fp8_device_status: synchronises the current device and returns
  *   FP8SQ_ERR_TIMEOUT if any bounded device-side wait of this library ran out
@@ -530,7 +627,7 @@ FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scal
  *   cleared.
  * fp8_last_error: message for the calling thread's last non-zero status
  *   (static thread-local storage; never NULL).
- * fp8_abi_version: 7.  Section 5c only adds entry points to it.  Changes from 6: fp8_linear_fwd / fp8_linear_bwd,
+ * fp8_abi_version: 7.  Sections 5c and 5d only add entry points to it.  Changes from 6: fp8_linear_fwd / fp8_linear_bwd,
  *   fp8_linear_workspace_bytes and fp8_quantize_rows_cols accept
  *   TILE_1x128_POW2 (the fine-grained units with power-of-two scales).
  *   Changes from 5 to 6: fp8_gemm_cast added (the GEMM's

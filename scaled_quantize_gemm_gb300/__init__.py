@@ -83,6 +83,20 @@ def lib() -> ctypes.CDLL:
                 "fp8_glu_fwd_workspace_bytes": (Z, [I64, I64, I64]),
                 "fp8_glu_fwd": (I, [P, I, P, P, I, P, I64, I64, I64, I, P, P, P, I, P, I, P, Z, P]),
                 "fp8_glu_bwd": (I, [P, I, P, P, I, P, I64, I64, I64, P, I, P, I, P, I, P]),
+                "fp8_rmsnorm_fwd": (I, [P, P, I, P, c.c_float, I64, I64, P, P, P, P, I, I, P, I, P, P]),
+                "fp8_rmsnorm_bwd_workspace_bytes": (Z, [I64, I64]),
+                "fp8_rmsnorm_bwd": (I, [P, P, P, I, P, P, I64, I64, P, P, P, Z, P]),
+                "fp8_expert_rows": (I64, [I64, I, I]),
+                "fp8_expert_plan_ints": (I64, [I64, I, I]),
+                "fp8_expert_plan": (I, [P, I64, I, I, P, P]),
+                "fp8_expert_dispatch": (I, [P, I, I64, P, I64, I, I, P, P]),
+                "fp8_expert_combine": (I, [P, I, I64, P, P, P, I64, I, I, P, P]),
+                "fp8_expert_combine_bwd": (I, [P, I, I64, P, P, P, I64, I, I, P, P, P, I, P, I, P]),
+                "fp8_expert_workspace_bytes": (Z, [I64, I, I, I64, I64]),
+                "fp8_expert_glu_fwd": (I, [P, I, P, P, I, P, P, I64, I, I, I64, I64, I, P, P, P, I, P, I, P, Z, P]),
+                "fp8_expert_gemm": (I, [P, I, P, P, I, P, I, P, I64, I, I, I64, I64, P, I, P, Z, P]),
+                "fp8_expert_glu_bwd": (I, [P, I, P, P, I, P, P, I64, I, I, I64, I64, P, I, P, I, P, I, P]),
+                "fp8_expert_wgrad": (I, [P, I, P, P, I, P, P, I64, I, I, I64, I64, P, I, P]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
@@ -577,6 +591,230 @@ def fp8_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scale, gu, ac
     pq, ps = _cast(q_dgu, "q_dgu", M, 2 * F, q_state, history_len)
     _check(lib().fp8_glu_bwd(pa, dy_format, sa, pb, w_format, sw, M, F, K, pg, act, pq, q_format, ps, history_len,
                              _stream(stream)))
+
+
+# ------------------------------------------------- RMSNorm, and a sublayer of experts
+def fp8_rmsnorm_fwd(x, gamma, eps: float, y, rstd=None, residual=None, sum_out=None, q_out=None, q_format: int = E4M3,
+                    gran: int = TENSOR, q_state=None, history_len: int = 0, scales_out=None, stream=None) -> None:
+    """y = x rstd gamma, rstd = 1 / sqrt(mean(x^2) + eps); with a residual, of sum_out = x + residual (which may be
+    residual or x itself); with q_out, y's FP8 codes (y may then be None): gran TENSOR under the delayed state q_state,
+    TILE_1x128, TILE_1x128_POW2, MX32, MX32_TILED or MX32_FLOOR_TILED with the units' scales in scales_out."""
+    T = _t()
+    px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
+    dt = x.dtype
+    pr = psum = py = prs = pq = ps = psc = None
+    if residual is not None or sum_out is not None:
+        if residual is None or sum_out is None:
+            raise ValueError("residual and sum_out come together")
+        pr, psum = _mat(residual, "residual", M, K, dt), _mat(sum_out, "sum_out", M, K, dt)
+    if q_out is not None:
+        if gran == TENSOR:
+            pq, ps = _cast(q_out, "q_out", M, K, q_state, history_len)
+        else:
+            pq = _mat(q_out, "q_out", M, K, T.uint8)
+            _need(scales_out, "scales_out", T.float32 if gran == TILE_1x128 else T.uint8, _scale_bytes(gran, M, K))
+            psc = scales_out.data_ptr()
+    if y is not None or pq is None:
+        py = _mat(y, "y", M, K, dt)
+    if rstd is not None:
+        prs = _vec(rstd, "rstd", M)
+    r = (_lib or lib()).fp8_rmsnorm_fwd(
+        px, pr, BF16 if dt is T.bfloat16 else F32, _vec(gamma, "gamma", K), eps, M, K, psum, py, prs, pq, q_format, gran,
+        ps, history_len, psc, _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
+
+
+def fp8_rmsnorm_bwd_workspace_bytes(M: int, K: int) -> int:
+    return lib().fp8_rmsnorm_bwd_workspace_bytes(M, K)
+
+
+def fp8_rmsnorm_bwd(dy, x, gamma, rstd, dx, dgamma, workspace, dres=None, stream=None) -> None:
+    """dx (+ dres) and dgamma of an RMSNorm from its input x and saved rstd."""
+    T = _t()
+    px, M, K = _sized(x, "x", (T.bfloat16, T.float32))
+    dt = x.dtype
+    _need(workspace, "workspace", T.uint8)
+    _check(lib().fp8_rmsnorm_bwd(
+        _mat(dy, "dy", M, K, dt), px, None if dres is None else _mat(dres, "dres", M, K, dt),
+        BF16 if dt is T.bfloat16 else F32, _vec(gamma, "gamma", K), _vec(rstd, "rstd", M), M, K,
+        _mat(dx, "dx", M, K, dt), _vec(dgamma, "dgamma", K), *_ws(workspace), _stream(stream)))
+
+
+def fp8_expert_rows(tokens: int, top_k: int, experts: int) -> int:
+    """rows of the sorted buffers of a routing of `tokens` tokens to top_k experts each"""
+    return (_lib or lib()).fp8_expert_rows(tokens, top_k, experts)
+
+
+def fp8_expert_plan_ints(tokens: int, top_k: int, experts: int) -> int:
+    return (_lib or lib()).fp8_expert_plan_ints(tokens, top_k, experts)
+
+
+def expert_plan_views(plan, tokens: int, top_k: int, experts: int) -> tuple:
+    """(offsets [E + 1], counts [E], row_of [tokens][top_k]) of a plan: each expert's first sorted row, its rows, and
+    the sorted row of every slot or -1"""
+    n = fp8_expert_plan_ints(tokens, top_k, experts)
+    return (plan[:experts + 1], plan[experts + 1:2 * experts + 1],
+            plan[n - tokens * top_k:n].view(tokens, top_k))
+
+
+_plan_sizes = {}
+
+
+def _routing(plan, tokens: int, top_k: int, experts: int) -> tuple:
+    """(pointer of the plan, rows of the sorted buffers)"""
+    key = (tokens, top_k, experts)
+    size = _plan_sizes.get(key)
+    if size is None:
+        if len(_plan_sizes) >= 4096:
+            _plan_sizes.clear()
+        size = _plan_sizes[key] = (fp8_expert_plan_ints(*key), fp8_expert_rows(*key))
+    if plan is None or plan.dtype is not _torch.int32 or plan.numel() < size[0] or not plan.is_contiguous():
+        _need(plan, "plan", _torch.int32, 4 * size[0])
+    return plan.data_ptr(), size[1]
+
+
+def fp8_expert_plan(ids, experts: int, plan, stream=None) -> None:
+    """The plan of a routing ids [tokens][top_k] (int32; an id outside [0, experts) leaves the slot out)."""
+    T = _t()
+    pi, n, k = _sized(ids, "ids", (T.int32,))
+    pp, _ = _routing(plan, n, k, experts)
+    r = (_lib or lib()).fp8_expert_plan(pi, n, k, experts, pp, _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
+
+
+def fp8_expert_dispatch(x, plan, top_k: int, experts: int, rows, stream=None) -> None:
+    """rows[row of (t, j)] = x[t] of FP8 codes (uint8), bf16 or fp32; zeros in the rows that fill up a segment."""
+    T = _t()
+    px, n, K = _sized(x, "x", (T.uint8, T.bfloat16, T.float32))
+    pp, R = _routing(plan, n, top_k, experts)
+    r = (_lib or lib()).fp8_expert_dispatch(px, x.element_size(), K, pp, n, top_k, experts,
+                                            _mat(rows, "rows", R, K, x.dtype),
+                                            _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
+
+
+def fp8_expert_combine(rows, plan, top_k: int, experts: int, y, weights=None, residual=None, stream=None) -> None:
+    """y[t] = residual[t] + sum over j of weights[t][j] rows[row of (t, j)] (weights None: ones); y may be the
+    residual itself."""
+    T = _t()
+    py, n, K = _sized(y, "y", (T.bfloat16, T.float32))
+    dt = y.dtype
+    pp, R = _routing(plan, n, top_k, experts)
+    r = (_lib or lib()).fp8_expert_combine(
+        _mat(rows, "rows", R, K, dt), BF16 if dt is T.bfloat16 else F32, K,
+        None if weights is None else _mat(weights, "weights", n, top_k, T.float32),
+        None if residual is None else _mat(residual, "residual", n, K, dt), pp, n, top_k, experts, py,
+        _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
+
+
+def fp8_expert_combine_bwd(dy, plan, top_k: int, experts: int, weights, rows=None, dweights=None, drows=None, q_out=None,
+                           q_format: int = E5M2, q_state=None, history_len: int = 0, stream=None) -> None:
+    """The gradients of fp8_expert_combine: of its rows (weights[t][j] dy[t], as drows and / or as FP8 codes q_out under
+    the delayed state q_state) and of its weights (dweights, from the rows)."""
+    T = _t()
+    pd, n, K = _sized(dy, "dy", (T.bfloat16, T.float32))
+    dt = dy.dtype
+    pp, R = _routing(plan, n, top_k, experts)
+    pq, ps = _cast(q_out, "q_out", R, K, q_state, history_len)
+    _check(lib().fp8_expert_combine_bwd(
+        pd, BF16 if dt is T.bfloat16 else F32, K, None if rows is None else _mat(rows, "rows", R, K, dt),
+        _mat(weights, "weights", n, top_k, T.float32), pp, n, top_k, experts,
+        None if dweights is None else _mat(dweights, "dweights", n, top_k, T.float32),
+        None if drows is None else _mat(drows, "drows", R, K, dt), pq, q_format, ps, history_len, _stream(stream)))
+
+
+def fp8_expert_workspace_bytes(tokens: int, top_k: int, experts: int, N: int, K: int) -> int:
+    return lib().fp8_expert_workspace_bytes(tokens, top_k, experts, N, K)
+
+
+def _expert_weights(W, name: str) -> tuple:
+    """(pointer, experts, rows, columns) of the experts' weights, FP8 codes [E][rows][columns]"""
+    if W is None or W.dtype is not _torch.uint8 or not W.is_contiguous():
+        _need(W, name, _torch.uint8)
+    if W.dim() != 3:
+        raise ValueError(f"{name}: expected [experts][rows][columns], got shape {tuple(W.shape)}")
+    return (W.data_ptr(), *W.shape)
+
+
+def fp8_expert_glu_fwd(A, a_format: int, a_scale, W, w_format: int, w_scales, act: int, plan, tokens: int, top_k: int,
+                       h_out=None, gu_out=None, q_out=None, q_format: int = E4M3, q_state=None, history_len: int = 0,
+                       workspace=None, stream=None) -> None:
+    """fp8_glu_fwd of rows sorted by expert: h = act(g) u, [g | u] = A W_e^T sA sW[e], W [E][2F][K]."""
+    T = _t()
+    pw, E, F2, K = _expert_weights(W, "W")
+    F = F2 // 2
+    if F2 != 2 * F:
+        raise ValueError(f"W: shape {tuple(W.shape)}, the second has to be even")
+    pp, R = _routing(plan, tokens, top_k, E)
+    ph = pg = pq = ps = pws = None
+    nw = 0
+    if gu_out is not None:
+        pg = _mat(gu_out, "gu_out", R, F2, T.bfloat16)
+    if h_out is not None:
+        ph = _mat(h_out, "h_out", R, F, T.bfloat16)
+    if q_out is not None:
+        pq, ps = _cast(q_out, "q_out", R, F, q_state, history_len)
+    if workspace is not None:
+        pws, nw = _ws(workspace)
+    r = (_lib or lib()).fp8_expert_glu_fwd(
+        _mat(A, "A", R, K, T.uint8), a_format, _vec(a_scale, "a_scale", 1), pw, w_format, _vec(w_scales, "w_scales", E),
+        pp, tokens, top_k, E, F, K, act, pg, ph, pq, q_format, ps, history_len, pws, nw,
+        _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
+
+
+def fp8_expert_gemm(A, a_format: int, a_scale, B, b_format: int, b_scales, b_major: int, plan, tokens: int, top_k: int,
+                    D, workspace=None, stream=None) -> None:
+    """D[r] = A[r] B_e^T sA sB[e] of rows sorted by expert, B [E][N][K] (K_MAJOR) or [E][K][N] (MN_MAJOR)."""
+    T = _t()
+    pb, E, N, K = _expert_weights(B, "B")
+    if b_major == MN_MAJOR:
+        N, K = K, N
+    pp, R = _routing(plan, tokens, top_k, E)
+    pws, nw = (None, 0) if workspace is None else _ws(workspace)
+    r = (_lib or lib()).fp8_expert_gemm(
+        _mat(A, "A", R, K, T.uint8), a_format, _vec(a_scale, "a_scale", 1), pb, b_format, _vec(b_scales, "b_scales", E),
+        b_major, pp, tokens, top_k, E, N, K, _mat(D, "D", R, N, T.float32 if D is not None and D.dtype is T.float32
+                                                  else T.bfloat16),
+        F32 if D.dtype is T.float32 else BF16, pws, nw, _current_stream() if stream is None else _stream(stream))
+    if r:
+        _check(r)
+
+
+def fp8_expert_glu_bwd(dY, dy_format: int, dy_scale, Wd, w_format: int, w_scales, gu, act: int, plan, tokens: int,
+                       top_k: int, q_dgu, q_format: int, q_state, history_len: int, stream=None) -> None:
+    """fp8_glu_bwd of rows sorted by expert: codes of [dg | du] from dY [R][K], Wd [E][K][F] and [g | u]."""
+    T = _t()
+    pw, E, K, F = _expert_weights(Wd, "Wd")
+    pp, R = _routing(plan, tokens, top_k, E)
+    if q_dgu is None:
+        raise ValueError("q_dgu is required")
+    pq, ps = _cast(q_dgu, "q_dgu", R, 2 * F, q_state, history_len)
+    _check(lib().fp8_expert_glu_bwd(
+        _mat(dY, "dY", R, K, T.uint8), dy_format, _vec(dy_scale, "dy_scale", 1), pw, w_format,
+        _vec(w_scales, "w_scales", E), pp, tokens, top_k, E, F, K, _mat(gu, "gu", R, 2 * F, T.bfloat16), act, pq,
+        q_format, ps, history_len, _stream(stream)))
+
+
+def fp8_expert_wgrad(A, a_format: int, a_scale, B, b_format: int, b_scale, plan, tokens: int, top_k: int, D,
+                     stream=None) -> None:
+    """D[e] = A_e^T B_e sA sB over the rows of each expert: A [R][M], B [R][N], D [E][M][N] bf16 or fp32."""
+    T = _t()
+    if D is None or D.dim() != 3:
+        raise ValueError("D: expected [experts][M][N]")
+    _need(D, "D")
+    dt = _dtype_code(D)
+    E, M, N = D.shape
+    pp, R = _routing(plan, tokens, top_k, E)
+    _check(lib().fp8_expert_wgrad(
+        _mat(A, "A", R, M, T.uint8), a_format, _vec(a_scale, "a_scale", 1), _mat(B, "B", R, N, T.uint8), b_format,
+        _vec(b_scale, "b_scale", 1), pp, tokens, top_k, E, M, N, D.data_ptr(), dt, _stream(stream)))
 
 
 def fp8_selftest_wait_timeout(limit_us: int, waited_out, stream=None) -> None:

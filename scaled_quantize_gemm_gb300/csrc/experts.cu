@@ -1,0 +1,144 @@
+// experts.cu -- the experts' products of a mixture-of-experts sublayer, on rows
+// sorted by expert (experts_rows.cu): the gated product, the plain product with
+// the weights stored either way (down projection, data gradient), the gated
+// backward pass and the weight gradients, on the CTA pairs of ffn_pair.cuh.
+#include <atomic>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ffn_pair.cuh"
+#include "gemm_common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace fp8sq {
+
+// Co-resident pairs of a kernel on the current device, asked once per device.
+template <int KIND, int GROUP>
+static cudaError_t expert_pairs(int smem, int* pairs)
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) {
+        const int c = cache[dev].load(std::memory_order_relaxed);
+        if (c > 0) {
+            *pairs = c - 1;
+            return cudaSuccess;
+        }
+    }
+    const void* kern = reinterpret_cast<const void*>(k_ffn_pair<KIND, GROUP>);
+    e = smem_attr_once(kern, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kFfnThreads<KIND>);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) cache[dev].store(n + 1, std::memory_order_relaxed);
+    *pairs = n;
+    return cudaSuccess;
+}
+
+template <int KIND, int GROUP>
+static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cudaStream_t st, const char** why)
+{
+    constexpr bool GLU = KIND == kEpiGlu;
+    const int64_t R = a.layout.rows;
+    CUtensorMap ta, tb;
+    bool ok;
+    if constexpr (GROUP == kWgrad) ok = make_tmap(&ta, a.A, a.M, R, BK) && make_tmap(&tb, a.B, a.N, R, BK);
+    else if constexpr (GROUP == kRowsMn) ok = make_tmap(&ta, a.A, a.K, R, BM) && make_tmap(&tb, a.B, a.N, a.E * a.K, BK);
+    else ok = make_tmap(&ta, a.A, a.K, R, BM) && make_tmap(&tb, a.B, a.K, a.E * (GLU ? 2 * a.N : a.N), kFfnBH);
+    if (!ok) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+    constexpr int smem = FfnSmem<KIND>::BYTES;
+    int pairs = 0;
+    const cudaError_t e = expert_pairs<KIND, GROUP>(smem, &pairs);
+    if (e != cudaSuccess) {
+        *why = "cluster occupancy query failed";
+        return e;
+    }
+    if (pairs < 1) {
+        *why = "no CTA pair of this kernel fits on the device";
+        return cudaErrorNotSupported;
+    }
+    // the tiles in use are known on the device alone: at most this many
+    constexpr int tile_n = GLU ? kFfnBH : kFfnBN;
+    TileSched sched{(int)((a.M + 2 * BM - 1) / (2 * BM)), (int)((a.N + tile_n - 1) / tile_n), 8};
+    const int64_t most = (GROUP == kWgrad ? (int64_t)a.E * sched.num_m : a.layout.max_tiles) * sched.num_n;
+    uint32_t idesc = make_idesc(a.a_format, a.b_format, kFfnBN);
+    idesc = (idesc & ~(0x1Fu << 24)) | ((uint32_t)((2 * BM) >> 4) << 24);   // M = 256 over the pair
+    if (GROUP == kWgrad) idesc |= 1u << 15;                                  // A MN-major
+    if (GROUP >= kRowsMn) idesc |= 1u << 16;                                 // B MN-major
+    // outputs stored in bulk; a map that the epilogue does not use is a copy of A's
+    CUtensorMap o[3] = {ta, ta, ta};
+    if constexpr (KIND == kEpiGluBwd) {
+        ok = make_tmap_codes(&o[0], a.q_out, R, a.N, 2 * a.N) && make_tmap_codes(&o[1], a.q_out + a.N, R, a.N, 2 * a.N);
+    } else if constexpr (GLU) {
+        __nv_bfloat16* z = p.Z;
+        if (z) ok = make_tmap_out(&o[0], z, R, a.N, true, 2 * a.N) && make_tmap_out(&o[1], z + a.N, R, a.N, true, 2 * a.N);
+    } else {
+        ok = make_tmap_out(&o[1], p.D, GROUP == kWgrad ? a.E * a.M : R, a.N, a.d_dtype == kBF16);
+    }
+    if (!ok) {
+        *why = "cuTensorMapEncodeTiled failed (output)";
+        return cudaErrorInvalidValue;
+    }
+    auto kern = k_ffn_pair<KIND, GROUP>;
+    launch_k(kern, (unsigned)(2 * (most < pairs ? most : pairs)), kFfnThreads<KIND>, (size_t)smem, st, ta, tb, p, idesc,
+             sched, o[0], o[1], o[2]);
+    return cudaGetLastError();
+}
+
+size_t expert_workspace(int64_t, int, int, int64_t, int64_t) { return 0; }
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int, const char** why)
+{
+    *why = nullptr;
+    if (a.N == 0 || (a.kind == kExpertWgrad ? a.M == 0 : a.layout.rows == 0)) return cudaSuccess;
+    FfnParams p = {};
+    p.M = (int)(a.kind == kExpertWgrad ? a.M : a.layout.rows);
+    p.N = (int)a.N;
+    p.K = (int)a.K;
+    p.sA = a.a_scale;
+    p.sB = a.b_scale;
+    p.act = a.act;
+    p.D = a.D;
+    p.d_f32 = a.d_dtype == kF32;
+    p.Z = static_cast<__nv_bfloat16*>(a.Z);
+    p.Q = a.q_out;
+    p.qfmt = a.q_format;
+    p.qstate = a.q_state;
+    p.qH = a.q_history_len;
+    p.gu = static_cast<const __nv_bfloat16*>(a.gu);
+    p.E = a.E;
+    p.offsets = a.plan;
+    p.ntiles = a.plan + 2 * a.E + 1;
+    p.tiles = reinterpret_cast<const int4*>(a.plan + a.layout.tiles_at);
+    p.max_tiles = (int)a.layout.max_tiles;
+    const cudaError_t e = device_error_word(&p.err);
+    if (e != cudaSuccess) return e;
+    switch (a.kind) {
+    case kExpertGlu: return launch_pair<kEpiGlu, kRows>(a, p, st, why);
+    case kExpertGluBwd: return launch_pair<kEpiGluBwd, kRowsMn>(a, p, st, why);
+    case kExpertWgrad: return launch_pair<kEpiAct, kWgrad>(a, p, st, why);
+    default: return a.b_mn ? launch_pair<kEpiAct, kRowsMn>(a, p, st, why) : launch_pair<kEpiAct, kRows>(a, p, st, why);
+    }
+}
+
+}  // namespace fp8sq

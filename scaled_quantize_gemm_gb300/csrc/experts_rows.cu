@@ -1,0 +1,505 @@
+// experts_rows.cu -- rows sorted by expert and back, for experts' products.
+//
+//   plan         a stable counting sort of the assignments ids[T][k]: expert e's
+//                rows are [offsets[e], offsets[e] + counts[e]) of the sorted
+//                buffers, in the order of (token, slot), and its segment ends on
+//                a multiple of 32 rows
+//   dispatch     rows[row_of[t][j]] = x[t]; the rest of a segment is zero
+//   combine      y[t] = residual[t] + sum over j of w[t][j] rows[row_of[t][j]]
+//   combine_bwd  drows[row_of[t][j]] = w[t][j] dy[t] (FP8 codes and / or as
+//                stored), dw[t][j] = <dy[t], rows[row_of[t][j]]>
+//
+// All are bound by memory: a token's row is read once and written (or summed
+// from) its k places, whole rows at a time.  No atomics on data: every sum runs
+// in the order of the slots, so the same call gives the same bits.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "act.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+
+namespace fp8sq {
+
+namespace {
+
+// ------------------------------------------------------------------ plan
+// One cluster of CL CTAs, each warp a contiguous share of the assignments:
+// counts per warp and expert in shared memory, a sum over the warps of a CTA,
+// over the CTAs through distributed shared memory and over the experts (padded
+// to 32), then a second pass over the assignments that gives each its row.  The
+// lanes of a warp that hold the same expert find each other with match_any, so
+// the order within an expert is that of the assignments.  One launch for any
+// size; bound by the latency of its few passes (SORT_US us).
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortBatch = 8;       // loads of ids in flight per lane
+
+struct SortArgs {
+    const int32_t* ids;
+    int64_t n;                      // assignments
+    int E;
+    int32_t* plan;
+    int tiles_at, row_of_at;
+};
+
+__global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int ctas)
+{
+    extern __shared__ int32_t sort_smem[];
+    const int E = a.E;
+    int32_t* hist = sort_smem;                          // [warp][E]
+    int32_t* total = hist + kSortWarps * E;             // [E], read by the other CTAs of the cluster
+    int32_t* base = total + E;                          // [E] first row of this CTA's share of an expert
+    int32_t* first_tile = base + E;                     // [E]
+    __shared__ int32_t scan[2][kSortWarps];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int rank = blockIdx.x;
+    for (int e = lane; e < E; e += 32) hist[warp * E + e] = 0;
+    pdl_enter();
+    const int64_t warps = (int64_t)ctas * kSortWarps;
+    const int64_t per = ((a.n + warps - 1) / warps + 31) & ~(int64_t)31;
+    const int64_t from = ((int64_t)rank * kSortWarps + warp) * per, to = from + per < a.n ? from + per : a.n;
+    // calls f(first index of 32, the lane's expert or -1, the lanes with the same)
+    auto each = [&](auto&& f) {
+        for (int64_t i = from; i < to; i += 32 * kSortBatch) {
+            int32_t id[kSortBatch];
+#pragma unroll
+            for (int b = 0; b < kSortBatch; ++b) {
+                const int64_t at = i + 32 * b + lane;
+                id[b] = at < to ? a.ids[at] : -1;
+            }
+#pragma unroll
+            for (int b = 0; b < kSortBatch; ++b) {
+                if (i + 32 * b >= to) break;
+                const int32_t e = (uint32_t)id[b] < (uint32_t)E ? id[b] : -1;
+                f(i + 32 * b, e, __match_any_sync(0xFFFFFFFFu, e));
+            }
+        }
+    };
+    const uint32_t below = (1u << lane) - 1u;
+    int32_t* mine = hist + warp * E;
+    __syncwarp();
+    each([&](int64_t, int32_t e, uint32_t same) {
+        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
+        __syncwarp();
+    });
+    __syncthreads();
+    for (int e = t; e < E; e += kSortThreads) {
+        int32_t run = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int32_t c = hist[w * E + e];
+            hist[w * E + e] = run;
+            run += c;
+        }
+        total[e] = run;
+    }
+    if (ctas > 1) cluster_sync_all();
+    else __syncthreads();
+    // thread e: the expert's counts over the cluster, then the padded rows and
+    // the tiles of the experts before it
+    static_assert(kExpertMax <= kSortThreads, "an expert a thread");
+    int32_t all = 0, before = 0;
+    if (t < E) {
+        if (ctas > 1) {
+            const uint32_t at = smem_addr(total + t);
+            for (int r = 0; r < ctas; ++r) {
+                const int32_t v = (int32_t)ld_shared_cluster_u32(cluster_map(at, (uint32_t)r));
+                if (r < rank) before += v;
+                all += v;
+            }
+        } else {
+            all = total[t];
+        }
+    }
+    const int32_t padded = (all + kExpertPad - 1) & ~(kExpertPad - 1);
+    const int32_t ntiles = (padded + kExpertTile - 1) / kExpertTile;
+    int32_t rs = padded, ts = ntiles;                   // inclusive sums over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t r = __shfl_up_sync(0xFFFFFFFFu, rs, o), q = __shfl_up_sync(0xFFFFFFFFu, ts, o);
+        if (lane >= o) {
+            rs += r;
+            ts += q;
+        }
+    }
+    if (lane == 31) {
+        scan[0][warp] = rs;
+        scan[1][warp] = ts;
+    }
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+        rs += scan[0][w];
+        ts += scan[1][w];
+    }
+    if (t < E) {
+        base[t] = rs - padded + before;
+        first_tile[t] = ts - ntiles;
+        if (rank == 0) {
+            a.plan[t] = rs - padded;
+            a.plan[E + 1 + t] = all;
+            if (t == E - 1) {
+                a.plan[E] = rs;
+                a.plan[2 * E + 1] = ts;
+            }
+        }
+    }
+    if (ctas > 1) cluster_sync_all();                   // the totals have been read: a CTA may end
+    else __syncthreads();
+    int32_t* row_of = a.plan + a.row_of_at;
+    each([&](int64_t i, int32_t e, uint32_t same) {
+        int32_t row = -1;
+        if (e >= 0) row = base[e] + mine[e] + __popc(same & below);
+        __syncwarp();
+        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
+        __syncwarp();
+        if (i + lane < to) row_of[i + lane] = row;
+    });
+    // row tiles of the products, in groups of neighbours of one expert
+    if (rank == 0) {
+        __threadfence_block();
+        __syncthreads();
+        int4* tiles = reinterpret_cast<int4*>(a.plan + a.tiles_at);
+        for (int e = warp; e < E; e += kSortWarps) {
+            const int32_t begin = a.plan[e], end = a.plan[e + 1], t0 = first_tile[e];
+            const int32_t m = (end - begin + kExpertTile - 1) / kExpertTile;
+            for (int32_t i = lane; i < m; i += 32) {
+                const int32_t g = i / kExpertGroup * kExpertGroup, left = m - g;
+                const int32_t size = left < kExpertGroup ? left : kExpertGroup;
+                tiles[t0 + i] = make_int4(t0 + g, e << 8 | size, begin + g * kExpertTile, end);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dispatch
+// The rows of expert `e` that fill up its segment: columns [c0, c0 + span) of
+// each, zeroed by the CTA's threads.
+struct Segments {
+    const int32_t* plan;
+    int E;
+    int64_t rows;                   // of the sorted buffers; nothing is touched past them
+    __device__ __forceinline__ int64_t pad_begin(int e) const { return (int64_t)plan[e] + plan[E + 1 + e]; }
+    __device__ __forceinline__ int64_t pad_end(int e) const
+    {
+        const int64_t end = plan[e + 1];
+        return end < rows ? end : rows;
+    }
+};
+
+constexpr int kMoveThreads = 256;
+
+// An item is one chunk of kMoveThreads vectors of a token's row: one load, k
+// stores a thread.  Before them the experts' padding, a chunk of all of an
+// expert's (at most 31) rows an item.
+template <typename V>
+__global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __restrict__ x, const int32_t* __restrict__ row_of,
+                                                                  Segments seg, int64_t T, int k, int64_t vecs,
+                                                                  int64_t chunks, V* __restrict__ out)
+{
+    pdl_enter();
+    const int64_t pads = (int64_t)seg.E * chunks, items = pads + T * chunks;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        if (it < pads) {
+            const int e = (int)(it / chunks);
+            const int64_t c = (it - (int64_t)e * chunks) * kMoveThreads + threadIdx.x;
+            const int64_t end = seg.pad_end(e);
+            if (c < vecs)
+                for (int64_t r = seg.pad_begin(e); r < end; ++r) out[r * vecs + c] = V{};
+            continue;
+        }
+        const int64_t t = (it - pads) / chunks, c = (it - pads - t * chunks) * kMoveThreads + threadIdx.x;
+        if (c >= vecs) continue;
+        const V v = x[t * vecs + c];
+        const int32_t* to = row_of + t * k;
+#pragma unroll 4
+        for (int j = 0; j < k; ++j) {
+            const int64_t r = __ldg(to + j);
+            if (r >= 0 && r < seg.rows) out[r * vecs + c] = v;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// An item is a chunk of kMoveThreads vectors of a token's row, up to eight rows'
+// loads in flight a thread; fp32 sums in the order of the slots, the residual
+// last.  y may be the residual itself.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* __restrict__ rows, const int32_t* __restrict__ row_of,
+                                                                 const float* __restrict__ w, const T* res, int64_t nt,
+                                                                 int k, int64_t K, int64_t chunks, int64_t R, T* y)
+{
+    using P = Pack<T, VEC>;
+    using Raw = typename P::Raw;
+    pdl_enter();
+    for (int64_t it = blockIdx.x; it < nt * chunks; it += gridDim.x) {
+        const int64_t t = it / chunks, c = ((it - t * chunks) * kMoveThreads + threadIdx.x) * VEC;
+        if (c >= K) continue;
+        float acc[VEC] = {};
+        Raw rr{};
+        if (res) rr = *reinterpret_cast<const Raw*>(res + t * K + c);
+        constexpr int FLY = 8;
+        for (int j0 = 0; j0 < k; j0 += FLY) {
+            Raw raw[FLY];
+            float wj[FLY];
+#pragma unroll
+            for (int j = 0; j < FLY; ++j) {
+                int64_t r = -1;
+                if (j0 + j < k) r = __ldg(row_of + t * k + j0 + j);
+                wj[j] = 0.0f;
+                raw[j] = Raw{};
+                if (r >= 0 && r < R) {
+                    raw[j] = __ldg(reinterpret_cast<const Raw*>(rows + r * K + c));
+                    wj[j] = w ? __ldg(w + t * k + j0 + j) : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < FLY; ++j) {
+                float v[VEC];
+                P::to_floats(raw[j], v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] = fmaf(wj[j], v[i], acc[i]);
+            }
+        }
+        if (res) {
+            float v[VEC];
+            P::to_floats(rr, v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] += v[i];
+        }
+        *reinterpret_cast<Raw*>(y + t * K + c) = P::from_floats(acc);
+    }
+}
+
+// ------------------------------------------------------------------ combine, backward
+// A CTA takes a token at a time and up to JB of its slots at once: dy[t] is read
+// once for them, the JB dot products accumulate in registers.  The padding of
+// the experts' segments comes first, shared out by expert.
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[VEC], float m, int fmt)
+{
+    if constexpr (VEC == 1) {
+        *q = code1(__fmul_rn(v[0], m), fmt);
+    } else {
+        uint16_t h[VEC / 2];
+#pragma unroll
+        for (int j = 0; j < VEC; j += 2) {
+            const float a = __fmul_rn(v[j], m), b = __fmul_rn(v[j + 1], m);
+            h[j / 2] = (uint16_t)(fmt == kE4M3 ? cvt_e4m3x2(a, b) : cvt_e5m2x2(a, b));
+        }
+        if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(q) = h[0] | (uint32_t)h[1] << 16;
+        else *reinterpret_cast<uint16_t*>(q) = h[0];
+    }
+}
+struct CombineBwdOut {
+    uint8_t* q;
+    int fmt, H;
+    float* state;
+    void* drows;
+    float* dw;
+};
+template <typename T, int VEC, int JB>
+__global__ void __launch_bounds__(256) k_expert_combine_bwd(const T* __restrict__ dy, const T* __restrict__ rows,
+                                                            const int32_t* __restrict__ row_of, const float* __restrict__ w,
+                                                            Segments seg, int64_t nt, int k, int64_t K, CombineBwdOut o)
+{
+    using P = Pack<T, VEC>;
+    using Raw = typename P::Raw;
+    __shared__ float red[2][8][JB];
+    pdl_enter();
+    const int th = threadIdx.x, lane = th & 31, warp = th >> 5, warps = blockDim.x >> 5;
+    T* drows = static_cast<T*>(o.drows);
+    const float none[VEC] = {};
+    for (int64_t e = blockIdx.x; e < seg.E; e += gridDim.x) {
+        const int64_t end = seg.pad_end((int)e);
+        for (int64_t r = seg.pad_begin((int)e); r < end; ++r)
+            for (int64_t c = (int64_t)th * VEC; c < K; c += (int64_t)blockDim.x * VEC) {
+                if (drows) *reinterpret_cast<Raw*>(drows + r * K + c) = Raw{};
+                if (o.q) store_codes<VEC>(o.q + r * K + c, none, 0.0f, o.fmt);
+            }
+    }
+    const float m = o.q ? o.state[o.H] : 1.0f;
+    float amax = 0.0f;
+    int par = 0;
+    for (int64_t t = blockIdx.x; t < nt; t += gridDim.x) {
+        for (int j0 = 0; j0 < k; j0 += JB) {
+            int64_t at[JB];
+            float wj[JB], dot[JB] = {};
+#pragma unroll
+            for (int j = 0; j < JB; ++j) {
+                int64_t r = j0 + j < k ? __ldg(row_of + t * k + j0 + j) : -1;
+                at[j] = r < seg.rows ? r : -1;
+                wj[j] = at[j] >= 0 ? __ldg(w + t * k + j0 + j) : 0.0f;
+            }
+            for (int64_t c = (int64_t)th * VEC; c < K; c += (int64_t)blockDim.x * VEC) {
+                float d[VEC];
+                P::to_floats(__ldg(reinterpret_cast<const Raw*>(dy + t * K + c)), d);
+                Raw raw[JB];
+                if (o.dw) {
+#pragma unroll
+                    for (int j = 0; j < JB; ++j)
+                        if (at[j] >= 0) raw[j] = __ldg(reinterpret_cast<const Raw*>(rows + at[j] * K + c));
+                }
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    if (at[j] < 0) continue;
+                    float v[VEC];
+                    if (o.dw) {
+                        P::to_floats(raw[j], v);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) dot[j] = fmaf(d[i], v[i], dot[j]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[i] = d[i] * wj[j];
+                    if (drows) *reinterpret_cast<Raw*>(drows + at[j] * K + c) = P::from_floats(v);
+                    if (o.q) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) amax = max_nan(amax, fabsf(v[i]));
+                        store_codes<VEC>(o.q + at[j] * K + c, v, m, o.fmt);
+                    }
+                }
+            }
+            if (o.dw) {
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    const float s = warp_sum(dot[j]);
+                    if (lane == 0) red[par][warp][j] = s;
+                }
+                __syncthreads();
+                if (th < JB && j0 + th < k) {
+                    float s = 0.0f;
+                    for (int i = 0; i < warps; ++i) s += red[par][i][th];
+                    o.dw[t * k + j0 + th] = s;
+                }
+                par ^= 1;
+            }
+        }
+    }
+    if (o.q) record_amax(amax, o.state);
+}
+
+template <typename F>
+cudaError_t with_vector(int64_t row_bytes, F&& f)
+{
+    if (row_bytes % 16 == 0) return f(uint4{});
+    if (row_bytes % 8 == 0) return f(uint2{});
+    if (row_bytes % 4 == 0) return f(uint32_t{});
+    if (row_bytes % 2 == 0) return f(uint16_t{});
+    return f(uint8_t{});
+}
+
+template <typename T, int VEC>
+cudaError_t combine(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    auto kern = k_expert_combine<T, VEC>;
+    const int64_t chunks = cdiv(a.K, kMoveThreads * VEC);
+    const int64_t cap = resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms), items = a.T * chunks;
+    launch_k(kern, (unsigned)(items < cap ? items : cap), kMoveThreads, 0, st, static_cast<const T*>(a.rows),
+             a.plan + a.layout.row_of_at, a.weights, static_cast<const T*>(a.residual), a.T, a.k, a.K, chunks,
+             a.layout.rows, static_cast<T*>(a.y));
+    return cudaGetLastError();
+}
+template <typename T, int VEC, int JB>
+cudaError_t combine_bwd_slots(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    auto kern = k_expert_combine_bwd<T, VEC, JB>;
+    const int64_t lanes = cdiv(a.K, VEC);
+    const int threads = (int)(lanes >= 256 ? 256 : lanes < 1 ? 32 : (lanes + 31) & ~(int64_t)31);
+    const int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, 0, sms);
+    const int64_t most = a.T > a.E ? a.T : a.E;
+    launch_k(kern, (unsigned)(most < cap ? most : cap), threads, 0, st, static_cast<const T*>(a.dy),
+             static_cast<const T*>(a.rows), a.plan + a.layout.row_of_at, a.weights, Segments{a.plan, a.E, a.layout.rows},
+             a.T, a.k, a.K, CombineBwdOut{a.q, a.q_format, a.q_history_len, a.q_state, a.drows, a.dweights});
+    return cudaGetLastError();
+}
+template <typename T, int VEC>
+cudaError_t combine_bwd(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    return a.k <= 4 ? combine_bwd_slots<T, VEC, 4>(a, st, sms) : combine_bwd_slots<T, VEC, 8>(a, st, sms);
+}
+// the widest vector of 16, 8, 4 or 2 bytes that divides a row
+template <typename T>
+cudaError_t with_elements(const ExpertRowsArgs& a, cudaStream_t st, int sms, bool bwd)
+{
+    constexpr int WIDE = 16 / (int)sizeof(T);
+    auto go = [&](auto n) {
+        constexpr int VEC = decltype(n)::value;
+        return bwd ? combine_bwd<T, VEC>(a, st, sms) : combine<T, VEC>(a, st, sms);
+    };
+    if (a.K % WIDE == 0) return go(std::integral_constant<int, WIDE>{});
+    if (a.K % (WIDE / 2) == 0) return go(std::integral_constant<int, WIDE / 2>{});
+    if (a.K % (WIDE / 4) == 0) return go(std::integral_constant<int, WIDE / 4>{});
+    return go(std::integral_constant<int, 1>{});
+}
+
+}  // namespace
+
+ExpertLayout expert_layout(int64_t T, int k, int E)
+{
+    ExpertLayout l;
+    const int64_t n = T * k, active = E < n ? E : n;
+    l.rows = (n + (kExpertPad - 1) * active) & ~(int64_t)(kExpertPad - 1);
+    l.max_tiles = l.rows / kExpertTile + active;
+    l.tiles_at = (2 * (int64_t)E + 2 + 3) & ~(int64_t)3;
+    l.row_of_at = l.tiles_at + 4 * l.max_tiles;
+    l.ints = l.row_of_at + n;
+    return l;
+}
+
+cudaError_t launch_expert_plan(const ExpertRowsArgs& a, cudaStream_t st)
+{
+    const int64_t n = a.T * a.k;
+    // one CTA as long as a warp has four rounds of 32 ids (or no more to gain)
+    const int ctas = n <= 4 * 32 * kSortWarps ? 1 : 8;
+    const int smem = (kSortWarps + 3) * a.E * (int)sizeof(int32_t);
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_expert_plan),
+                                   (kSortWarps + 3) * kExpertMax * (int)sizeof(int32_t));
+    if (e != cudaSuccess) return e;
+    SortArgs s{a.ids, n, a.E, a.plan_out, (int)a.layout.tiles_at, (int)a.layout.row_of_at};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_expert_plan, s, ctas);
+}
+
+cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    const int64_t bytes = a.K * a.size;
+    return with_vector(bytes, [&](auto v) {
+        using V = decltype(v);
+        auto kern = k_expert_dispatch<V>;
+        const int64_t vecs = bytes / (int64_t)sizeof(V), chunks = cdiv(vecs, kMoveThreads);
+        const int64_t cap = resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms);
+        const int64_t items = (a.T + a.E) * chunks;
+        launch_k(kern, (unsigned)(items < cap ? items : cap), kMoveThreads, 0, st, static_cast<const V*>(a.x),
+                 a.plan + a.layout.row_of_at, Segments{a.plan, a.E, a.layout.rows}, a.T, a.k, vecs, chunks,
+                 static_cast<V*>(a.rows_out));
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_expert_combine(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    return a.dtype == kBF16 ? with_elements<__nv_bfloat16>(a, st, sms, false) : with_elements<float>(a, st, sms, false);
+}
+
+cudaError_t launch_expert_combine_bwd(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    return a.dtype == kBF16 ? with_elements<__nv_bfloat16>(a, st, sms, true) : with_elements<float>(a, st, sms, true);
+}
+
+}  // namespace fp8sq

@@ -127,6 +127,9 @@ struct LnArgs {
     int q_format = kE4M3;
     float* q_state = nullptr;
     int q_history_len = 0;
+    int q_gran = kTensor;            // RMSNorm: the codes' scaling unit (kTensor: the delayed state)
+    int q_unit = 0;                  // ... as the kernel stores its scale
+    void* q_scales = nullptr;
     float* mu = nullptr;
     float* rstd = nullptr;
     const void* dy = nullptr;        // backward
@@ -139,6 +142,10 @@ struct LnArgs {
 cudaError_t launch_layernorm_fwd(const LnArgs& a, cudaStream_t st, int sms);
 cudaError_t launch_layernorm_bwd(const LnArgs& a, cudaStream_t st, int sms);
 size_t layernorm_bwd_workspace(int64_t M, int64_t K);
+// rmsnorm.cu (mu, beta and dbeta unused)
+cudaError_t launch_rmsnorm_fwd(const LnArgs& a, cudaStream_t st, int sms);
+cudaError_t launch_rmsnorm_bwd(const LnArgs& a, cudaStream_t st, int sms);
+size_t rmsnorm_bwd_workspace(int64_t M, int64_t K);
 struct ActBwdArgs {
     int64_t M = 0, N = 0;
     const void* dy = nullptr;        // bf16
@@ -154,6 +161,78 @@ struct ActBwdArgs {
 };
 cudaError_t launch_act_bwd(const ActBwdArgs& a, cudaStream_t st, int sms);
 size_t act_bwd_workspace(int64_t M, int64_t N);
+
+// experts_rows.cu: rows sorted by expert and back
+constexpr int kExpertPad = 32;       // an expert's segment of the sorted rows is a multiple of this
+constexpr int kExpertTile = 256;     // rows of a product's tile
+constexpr int kExpertGroup = 8;      // neighbouring tiles of one expert that share the weights' tiles in L2
+constexpr int kExpertMax = 1024;     // experts
+constexpr int kExpertSlots = 64;     // experts of a token
+// The plan of a routing, int32: offsets [E + 1], counts [E], the number of row
+// tiles; at tiles_at the tiles, four each {first tile of its group, expert << 8
+// | tiles in the group, the group's first row, the expert's last row + 1}; at
+// row_of_at the sorted row of every assignment, or -1.
+struct ExpertLayout {
+    int64_t rows = 0, max_tiles = 0, tiles_at = 0, row_of_at = 0, ints = 0;
+};
+ExpertLayout expert_layout(int64_t T, int k, int E);
+struct ExpertRowsArgs {
+    int64_t T = 0, K = 0;
+    int k = 0, E = 0;
+    ExpertLayout layout;
+    const int32_t* ids = nullptr;
+    int32_t* plan_out = nullptr;
+    const int32_t* plan = nullptr;
+    const void* x = nullptr;         // dispatch: [T][K] of `size` bytes an element
+    int size = 1;
+    void* rows_out = nullptr;
+    int dtype = kBF16;               // combine and its backward pass
+    const void* rows = nullptr;
+    const float* weights = nullptr;
+    const void* residual = nullptr;
+    void* y = nullptr;
+    const void* dy = nullptr;
+    void* drows = nullptr;
+    float* dweights = nullptr;
+    uint8_t* q = nullptr;
+    int q_format = kE5M2;
+    float* q_state = nullptr;
+    int q_history_len = 0;
+};
+cudaError_t launch_expert_plan(const ExpertRowsArgs& a, cudaStream_t st);
+cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t st, int sms);
+cudaError_t launch_expert_combine(const ExpertRowsArgs& a, cudaStream_t st, int sms);
+cudaError_t launch_expert_combine_bwd(const ExpertRowsArgs& a, cudaStream_t st, int sms);
+
+// experts.cu: the experts' products (per-tensor scale of A, a scale for each
+// expert's B)
+enum { kExpertGemm = 0, kExpertGlu = 1, kExpertGluBwd = 2, kExpertWgrad = 3 };
+struct ExpertGemmArgs {
+    int kind = kExpertGemm;
+    int64_t T = 0;
+    int k = 0, E = 0;
+    ExpertLayout layout;
+    const int32_t* plan = nullptr;
+    int64_t M = 0, N = 0, K = 0;     // M: wgrad (rows of each D); N: columns (glu: features); K: contraction
+    bool b_mn = false;               // gemm: B [E][K][N]
+    const uint8_t* A = nullptr;
+    const uint8_t* B = nullptr;
+    int a_format = kE4M3, b_format = kE4M3;
+    const float* a_scale = nullptr;
+    const float* b_scale = nullptr;  // [E] (wgrad: one)
+    int act = 0;
+    const void* gu = nullptr;        // glu_bwd: bf16 [R][2F]
+    void* D = nullptr;               // gemm [R][N], glu h bf16 [R][F], wgrad [E][M][N]
+    int d_dtype = kBF16;
+    void* Z = nullptr;               // glu: bf16 [R][2F]
+    uint8_t* q_out = nullptr;
+    int q_format = kE4M3;
+    float* q_state = nullptr;
+    int q_history_len = 0;
+    void* workspace = nullptr;
+};
+cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int sms, const char** why);
+size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K);
 
 // api.cu: the calling thread's error message and the sm_103 device check
 int api_fail(int code, const char* fmt, ...);
