@@ -185,6 +185,49 @@ struct Stager {
     }
 };
 
+// 32 columns of sums, scaled, as bf16 or fp32 through two halves of a warp's
+// staging area in turn: a half is written again once the bulk stores of two
+// turns ago have read it.
+__device__ __forceinline__ void stage_halves(uint8_t* buf, int lane, uint32_t& half, const CUtensorMap* m,
+                                             const uint32_t (&r)[32], float scale, bool f32, int col, int row0, int left)
+{
+    auto turn = [&](auto&& fill, int cols, int at) {
+        uint8_t* p = buf + half * 2 * kStageBytes;
+        half ^= 1u;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        fill(p + 32 * lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            for (int i = 0; i < 2; ++i)
+                if (at + i * cols < left) bulk_store_2d(m, col + at + i * cols, row0, p + i * kStageBytes);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    };
+    auto v = [&](int j) {
+        return __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
+    };
+    if (!f32) {
+        turn([&](uint8_t* p) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(p + (c >> 1) * kStageBytes + (c & 1) * 16) =
+                    make_uint4(pack_bf16(v(4 * c)), pack_bf16(v(4 * c + 1)), pack_bf16(v(4 * c + 2)), pack_bf16(v(4 * c + 3)));
+        }, 16, 0);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            turn([&](uint8_t* p) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 a = v(8 * h + 2 * c), b = v(8 * h + 2 * c + 1);
+                    *reinterpret_cast<float4*>(p + (c >> 1) * kStageBytes + (c & 1) * 16) = make_float4(a.x, a.y, b.x, b.y);
+                }
+            }, 8, 16 * h);
+    }
+}
+
 // a whole 32-byte sector in one load (16-byte loads by row take each twice).
 // RO: through the read-only path; not the residual, which the call may be
 // overwriting in place (other elements of it, at the time).
@@ -232,6 +275,18 @@ __device__ __forceinline__ float2 raw_f32(const uint4* raw, int j)
     const uint4 w = raw[j >> 1];
     return (j & 1) ? make_float2(__uint_as_float(w.z), __uint_as_float(w.w))
                    : make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+}
+// Waits for the loads from tensor memory, of which r is one: no use of r is
+// moved ahead of it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 {
@@ -486,6 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             }
         };
         int lt = 0;
+        [[maybe_unused]] uint32_t half = 0;
         for (int t = cid; t < num_tiles; t += ncl) {
             const PairTile x = pair_tile<GROUP>(p, sched, t);
             const bool some = GROUP != kWgrad || x.nkb > 0;          // (else zeros)
@@ -508,6 +564,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             const bool ok = !some || wait(&afull[b], u & 1u);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
+            if constexpr (GROUP != kNoGroups && KIND == kEpiAct) {
+                // The product alone: short contractions (a weight gradient's few
+                // hundred rows) leave it little time, so the next 32 columns leave
+                // tensor memory while these are stored, and the accumulator is handed
+                // back before the last are.
+                constexpr int CHUNKS = TN / PARTS / 32;
+                uint32_t r[2][32];
+                auto load = [&](int i) {
+                    if (some) {
+                        tmem_ld_32x32b_x32(taddr + (uint32_t)(c_begin + 32 * i), r[i & 1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[i & 1][j] = 0;
+                    }
+                };
+                __syncwarp();                  // tcgen05.ld takes a converged warp
+                load(0);
+                if (some) tmem_ld_wait_for(r[0]);
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) {
+                    if (i + 1 < CHUNKS) {
+                        load(i + 1);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (some && lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+                    }
+                    const int col = nb * TN + c_begin + 32 * i, left = p.N - col;
+                    if (row0 < end && left > 0)
+                        stage_halves(out.buf, lane, half, &tmO1, r[i & 1], some ? scale : 0.0f, p.d_f32, col, store0, left);
+                    __syncwarp();
+                    if (i + 1 < CHUNKS && some) tmem_ld_wait_for(r[(i + 1) & 1]);
+                }
+            } else {
 #pragma unroll 1
             for (int c = c_begin; c < c_end && row0 < end; c += 32) {
                 const int col = nb * TN + c, left = p.N - col;
@@ -541,14 +631,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                     }
                     __syncwarp();
                 } else if constexpr (KIND == kEpiAct) {
-                    uint32_t r[32] = {};
-                    if (some) {
-                        tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
-                        tmem_ld_wait();
-                    }
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        v[j] = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(some ? scale : 0.0f));
+                        v[j] = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
                     out.next_chunk();
                     if (p.bias) {
                         const int from = (c - c_begin) / 4;       // the lane that holds column c
@@ -632,7 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             }
             tc_fence_before();
             __syncwarp();
-            if (some && lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+            if (lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+            }
         }
         stage_store_drain(lane);
         if (p.Q) {

@@ -128,7 +128,6 @@ struct LnArgs {
     float* q_state = nullptr;
     int q_history_len = 0;
     int q_gran = kTensor;            // RMSNorm: the codes' scaling unit (kTensor: the delayed state)
-    int q_unit = 0;                  // ... as the kernel stores its scale
     void* q_scales = nullptr;
     float* mu = nullptr;
     float* rstd = nullptr;

@@ -15,7 +15,6 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "rowvec.cuh"
-#include "scales.cuh"
 
 namespace fp8sq {
 
@@ -191,52 +190,14 @@ __device__ __forceinline__ float2 block_total2(const float (*red)[32], int span)
 constexpr int kLnCols = 16;         // columns a thread holds
 // sum may be res or x itself (a thread reads both where it writes, and before),
 // so none of the three is declared free of aliases.
-// CODES: y also (or only) as FP8 codes, cast from fp32, under a delayed state or
-// (kCodes128, kCodes32) with the scale of each unit of 128 or 32 columns: the
-// lanes that hold a unit are neighbours, so its amax is a few shuffles, and the
-// two divisions that the fp32 scale takes (the multiplier and the step) are
-// one instruction stream, even lanes taking one and odd lanes the other.
-// RMS: no mean, one sum a row (16384 x 4096 bf16 with residual: codes in 1x128
-// tiles TILES_US us).
-enum { kNoCodes = 0, kCodesDelayed = 1, kCodes128 = 2, kCodes32 = 3 };
-// how a unit's scale is stored: fp32 [R][K / 128]; E8M0 in the tiled layout, a
-// 128-column unit's code in all of its four 32-blocks; E8M0 [R][K / 32]; E8M0
-// tiled; the same by the floor rule
-enum { kUnitF32 = 0, kUnitPow2 = 1, kUnitMx = 2, kUnitMxTiled = 3, kUnitMxFloor = 4 };
+// CODES: y also (or only) as FP8 codes under a delayed state, cast from fp32.
+// RMS: no mean, one sum a row (rows of whole 16-byte vectors: rmsnorm.cu).
 struct LnCast {
     uint8_t* q;
     int fmt, H;
     float* state;
-    int unit;
-    void* scales;
 };
-// The multiplier of a unit from its amax (as bits), the same in all of its G
-// lanes; the unit's scale is stored by one of them (none if !live).
-template <int G>
-__device__ __forceinline__ float unit_scale(uint32_t a, const LnCast& cast, int64_t r, int c, int K, bool live)
-{
-    const int lane = threadIdx.x & 31;
-    if (G >= 2 && cast.unit == kUnitF32) {
-        const float fm = cast.fmt == kE4M3 ? Fmt<kE4M3>::fmax : Fmt<kE5M2>::fmax;
-        const float v = __uint_as_float(a);
-        const bool plain = a != 0u && a < 0x7F800000u, odd = lane & 1;
-        const float d = plain ? __fdiv_rn(odd ? v : fm, odd ? fm : v) : 1.0f;      // (as current_scale)
-        if (live && (lane & (G - 1)) == 1) static_cast<float*>(cast.scales)[r * (K / 128) + c / 128] = d;
-        return __shfl_sync(0xFFFFFFFFu, d, lane & ~(G - 1));
-    }
-    float m;
-    const uint32_t code = cast.unit == kUnitMxFloor
-                              ? (cast.fmt == kE4M3 ? mx_scale_floor<kE4M3>(a, m) : mx_scale_floor<kE5M2>(a, m))
-                              : (cast.fmt == kE4M3 ? mx_scale<kE4M3>(a, m) : mx_scale<kE5M2>(a, m));
-    if (live && (lane & (G - 1)) == 0) {
-        uint8_t* sc = static_cast<uint8_t*>(cast.scales);
-        if (cast.unit == kUnitMx) sc[r * (K / 32) + c / 32] = (uint8_t)code;
-        else if (cast.unit == kUnitPow2) *reinterpret_cast<uint32_t*>(sc + mx_tiled_offset(r, c / 32, K)) = code * 0x01010101u;
-        else sc[mx_tiled_offset(r, c / 32, K)] = (uint8_t)code;
-    }
-    return m;
-}
-template <typename T, int VEC, int MAXT, int MINB, int CODES, bool RMS>
+template <typename T, int VEC, int MAXT, int MINB, bool CODES, bool RMS>
 __global__ void __launch_bounds__(MAXT, MINB)
     k_ln_fwd(const T* x, const T* res, const float* __restrict__ gamma, const float* __restrict__ beta, float eps,
              int64_t R, int K, T* sum, T* __restrict__ y, float* __restrict__ mu, float* __restrict__ rstd, LnCast cast)
@@ -252,7 +213,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     __syncthreads();
     pdl_trigger();
     pdl_enter();
-    const float m = CODES == kCodesDelayed ? cast.state[cast.H] : 1.0f;
+    const float m = CODES ? cast.state[cast.H] : 1.0f;
     float amax = 0.0f;
     [[maybe_unused]] int par = 0;
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
@@ -328,11 +289,10 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * nt + t) * VEC;
-            constexpr bool UNITS = CODES >= kCodes128;
-            if (!UNITS && c >= K) continue;             // (units: all lanes take part in the shuffles)
-            float v[VEC], g[VEC] = {}, b[VEC] = {};
+            if (c >= K) continue;
+            float v[VEC], g[VEC], b[VEC] = {};
             P::to_floats(raw[i], v);
-            if (!UNITS || c < K) load_param<VEC>(gamma, c, g);
+            load_param<VEC>(gamma, c, g);
             if constexpr (RMS) {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) v[j] = v[j] * rs * g[j];
@@ -341,26 +301,13 @@ __global__ void __launch_bounds__(MAXT, MINB)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) v[j] = fmaf((v[j] - mean) * rs, g[j], b[j]);
             }
-            if ((!CODES || y) && (!UNITS || c < K)) *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(v);
-            if constexpr (CODES != kNoCodes) {
+            if (!CODES || y) *reinterpret_cast<Raw*>(y + base + c) = P::from_floats(v);
+            if constexpr (CODES) {
                 uint8_t* q = cast.q + base + c;
-                if constexpr (UNITS) {
-                    constexpr int G = (CODES == kCodes128 ? 128 : 32) / VEC;
-                    uint32_t a = 0;
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);   // a NaN above all
-#pragma unroll
-                    for (int o = G / 2; o >= 1; o >>= 1) a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-                    const float mu_ = unit_scale<G>(a, cast, r, c, K, c < K);
-                    if (c >= K) continue;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) v[j] = __fmul_rn(v[j], mu_);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        amax = max_nan(amax, fabsf(v[j]));
-                        v[j] = __fmul_rn(v[j], m);
-                    }
+                for (int j = 0; j < VEC; ++j) {
+                    amax = max_nan(amax, fabsf(v[j]));
+                    v[j] = __fmul_rn(v[j], m);
                 }
                 if constexpr (VEC >= 2) {
                     uint16_t h[VEC / 2];
@@ -377,7 +324,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
             }
         }
     }
-    if constexpr (CODES == kCodesDelayed) record_amax(amax, cast.state);
+    if constexpr (CODES) record_amax(amax, cast.state);
 }
 
 // ------------------------------------------------------------------ LayerNorm backward
@@ -412,7 +359,10 @@ constexpr int kLnGroups = 8;        // groups of a CTA, at most
 // room of a row in the ring with the 16-byte blocks it begins and ends in
 __host__ __device__ constexpr int ln_row_bytes(int K, int size) { return (K * size + 30) & ~15; }
 
-// RMS: no mean, one sum a row and no dbeta.
+// RMS: no mean, one sum a row and no dbeta, and a CTA takes neighbouring rows
+// (every gridDim.x-th row, as LayerNorm has it, 16384 x 4096 bf16 with dres 102
+// us, 8192 x 8192 116; neighbours 85.6 and 86.3; LayerNorm itself 85.4 and 89.2
+// against 89.2 and 92.0).
 template <typename T, int VEC, int C, int STAGES, int MAXT, int MINB, bool KEEP, bool GROUPED, bool RMS>
 __global__ void __launch_bounds__(MAXT, MINB)
     k_ln_bwd(const T* __restrict__ dy, const T* __restrict__ x, const T* __restrict__ dres,
@@ -438,6 +388,10 @@ __global__ void __launch_bounds__(MAXT, MINB)
     __syncthreads();
     pdl_enter();
     const int narr = dres ? 3 : 2;
+    // the CTA's rows: every gridDim.x-th, or (RMS) a run of neighbours
+    const int64_t per = (R + gridDim.x - 1) / gridDim.x;
+    const int64_t from = RMS ? blockIdx.x * per : (int64_t)blockIdx.x * groups;
+    const int64_t end = RMS && from + per < R ? from + per : R;
     // [stage][array][vector i][thread]
     Raw* ring = reinterpret_cast<Raw*>(ln_ring) + threadIdx.x;
     auto slot = [&](int st, int arr, int i) -> Raw* { return ring + ((st * narr + arr) * NV + i) * blockDim.x; };
@@ -449,7 +403,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     auto row = [&](int st, int arr) { return ln_ring + ((g * STAGES + st) * narr + arr) * row_bytes; };
     auto stage = [&](int st, int64_t r) {
         if constexpr (BULK) {
-            if (t == 0 && r < R) {
+            if (t == 0 && r < end) {
                 const int64_t from = r * K * (int)sizeof(T), a0 = from & ~(int64_t)15;
                 int64_t a1 = (from + K * (int)sizeof(T) + 15) & ~(int64_t)15;
                 if (a1 > whole) a1 = whole;
@@ -469,7 +423,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
                 }
             }
         } else {
-            if (r < R) {
+            if (r < end) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = (i * nt + t) * VEC;
@@ -523,7 +477,7 @@ __global__ void __launch_bounds__(MAXT, MINB)
     constexpr bool GREG = KEEP && MAXT <= 512;      // gamma in registers as well
     float2 ag[C / 2] = {}, ab[C / 2] = {}, gam[C / 2];
     if constexpr (GREG) params(gam);
-    const int64_t first = (int64_t)blockIdx.x * groups + g, step = (int64_t)gridDim.x * groups;
+    const int64_t first = from + g, step = (RMS ? 1 : (int64_t)gridDim.x) * groups;
     constexpr int AHEAD = BULK && STAGES == 1 ? 1 : STAGES - 1;          // rows in flight before the first
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s) stage(s, first + s * step);
@@ -531,15 +485,15 @@ __global__ void __launch_bounds__(MAXT, MINB)
     uint32_t phase = 0;
     const float inv = 1.0f / (float)K;
     float mean = 0.0f, rs = 0.0f;
-    if (first < R) {
+    if (first < end) {
         if constexpr (!RMS) mean = __ldg(mu + first);
         rs = __ldg(rstd + first);
     }
-    for (int64_t r = first; r < R; r += step) {
+    for (int64_t r = first; r < end; r += step) {
         int ahead = st + STAGES - 1;
         if (ahead >= STAGES) ahead -= STAGES;
         if constexpr (!BULK) stage(ahead, r + (STAGES - 1) * step);
-        const int64_t rn = r + step < R ? r + step : r;
+        const int64_t rn = r + step < end ? r + step : r;
         const float mean_n = RMS ? 0.0f : __ldg(mu + rn), rs_n = __ldg(rstd + rn);
         if constexpr (BULK) {
             // (an error word that is set already does not end the wait for the copies)
@@ -682,18 +636,18 @@ __global__ void __launch_bounds__(MAXT, MINB)
     }
 }
 
-template <typename T, int VEC, int MAXT, int MINB, int CODES, bool RMS>
+template <typename T, int VEC, int MAXT, int MINB, bool CODES, bool RMS>
 cudaError_t ln_fwd_cta(const LnArgs& a, cudaStream_t st, int sms, int threads)
 {
     auto kern = k_ln_fwd<T, VEC, MAXT, MINB, CODES, RMS>;
     const int64_t cap = resident(reinterpret_cast<const void*>(kern), threads, 0, sms);
     launch_k(kern, (unsigned)(a.M < cap ? a.M : cap), threads, 0, st, static_cast<const T*>(a.x),
              static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, (int)a.K, static_cast<T*>(a.sum),
-             static_cast<T*>(a.y), a.mu, a.rstd, LnCast{a.q, a.q_format, a.q_history_len, a.q_state, a.q_unit, a.q_scales});
+             static_cast<T*>(a.y), a.mu, a.rstd, LnCast{a.q, a.q_format, a.q_history_len, a.q_state});
     return cudaGetLastError();
 }
 
-template <typename T, int VEC, int CODES, bool RMS>
+template <typename T, int VEC, bool CODES, bool RMS>
 cudaError_t ln_fwd_rows(const LnArgs& a, cudaStream_t st, int sms)
 {
     const int threads = 32 * (int)cdiv(a.K, 32 * kLnCols);
@@ -703,7 +657,7 @@ cudaError_t ln_fwd_rows(const LnArgs& a, cudaStream_t st, int sms)
     return ln_fwd_cta<T, VEC, 1024, 1, CODES, RMS>(a, st, sms, threads);
 }
 
-template <typename T, int CODES, bool RMS>
+template <typename T, bool CODES, bool RMS>
 cudaError_t ln_fwd_vec(const LnArgs& a, cudaStream_t st, int sms)
 {
     constexpr int WIDE = 16 / (int)sizeof(T);        // the widest vector of 16, 8 or 4 bytes that divides a row
@@ -717,7 +671,7 @@ template <typename T>
 cudaError_t ln_fwd(const LnArgs& a, cudaStream_t st, int sms)
 {
     if (a.K <= 1024 * kLnCols)
-        return a.q ? ln_fwd_vec<T, kCodesDelayed, false>(a, st, sms) : ln_fwd_vec<T, kNoCodes, false>(a, st, sms);
+        return a.q ? ln_fwd_vec<T, true, false>(a, st, sms) : ln_fwd_vec<T, false, false>(a, st, sms);
     const int64_t cap = (int64_t)sms * 8;
     launch_k(k_ln_fwd_any<T>, (unsigned)(a.M < cap ? a.M : cap), 256, 0, st, static_cast<const T*>(a.x),
              static_cast<const T*>(a.residual), a.gamma, a.beta, a.eps, a.M, a.K, static_cast<T*>(a.sum),
