@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "ffn_pair.cuh"
+#include "ffn_rows.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -105,9 +106,64 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
     return cudaGetLastError();
 }
 
-size_t expert_workspace(int64_t, int, int, int64_t, int64_t) { return 0; }
+// ------------------------------------------------------------------ few rows
+// Whether k_ffn_rows takes a product with N weight rows an expert (glu: 2F).  The
+// routing is known on the device alone, so the rule goes by its sizes: n = T k
+// assignments make a = n / min(E, n) rows an expert.  The tiles of 256 rows read
+// each weight once whatever the rows; the few-rows kernel shares the weights' bytes out
+// evenly and starts sooner, but reads a weight tile again (from L2) for every 32 rows
+// of an expert.  One GB300, us, few rows / tiles (the weights at the copy rate): 8
+// of 64 experts, 4096 -> 2 x 1792, 1 token 26.3 / 29.5 (17.4), 16 tokens 98.8 / 102.7, 64
+// tokens (a = 9) 138 / 141, 128 tokens (17) 159 / 150, 512 tokens (64) 298 / 162; 4 of 32,
+// 2304 -> 2 x 1040, 64 tokens (9) 27.6 / 32.2, 128 tokens (16) 32.0 / 32.9, 256
+// tokens (32) 38.4 / 33.4; 2 of 16, 3584 -> 4096, 64 tokens (9) 43 / 48, 128 tokens (17) 44 /
+// 49, 256 tokens (34) 54 / 49.
+constexpr int kExpertNT = 32;
+constexpr double kExpertFewRows = 12.0;
+static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, int sms)
+{
+    const ExpertLayout l = expert_layout(T, k, E);
+    const int64_t wtiles = (N + BM - 1) / BM, nkb = (K + BK - 1) / BK, most = l.rows / kExpertNT * wtiles;
+    if (most > kRowsMaxTiles || most * nkb >= ((int64_t)1 << 31) || sms > kRowsMaxCtas) return false;
+    const double n = (double)T * k, active = E < n ? E : n, a = n / active;
+    return a <= kExpertFewRows;
+}
 
-cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int, const char** why)
+size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K)
+{
+    if (!expert_few_rows(T, k, E, N, K, 152)) return 0;
+    return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * kExpertNT * BM * sizeof(float);
+}
+
+template <int KIND>
+static cudaError_t launch_few_rows(const ExpertGemmArgs& a, FfnParams p, cudaStream_t st, int sms, const char** why)
+{
+    using L = RowsLayout<KIND, kExpertNT>;
+    const int64_t wrows = L::GLU ? 2 * a.N : a.N;
+    CUtensorMap tw, tx;
+    if (!make_tmap(&tw, a.B, a.K, a.E * wrows, L::COLS) || !make_tmap(&tx, a.A, a.K, a.layout.rows, kExpertNT)) {
+        *why = "cuTensorMapEncodeTiled failed";
+        return cudaErrorInvalidValue;
+    }
+    p.blocks = reinterpret_cast<const int4*>(a.plan + a.layout.blocks_at);
+    p.max_blocks = (int)(a.layout.rows / kExpertPad);
+    p.wrows = (int)wrows;
+    RowsParams w = {};
+    w.wtiles = (int)((a.N + L::COLS - 1) / L::COLS);
+    w.nkb = (int)((a.K + BK - 1) / BK);
+    w.split = a.workspace != nullptr;
+    if (a.workspace) {
+        w.counters = static_cast<uint32_t*>(a.workspace);
+        w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kRowsCounterBytes);
+    }
+    auto kern = k_ffn_rows<KIND, kExpertNT, true>;
+    const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), L::BYTES);
+    if (e != cudaSuccess) return e;
+    launch_k(kern, (unsigned)sms, kRowsThreads, L::BYTES, st, tw, tx, p, w, make_idesc(a.b_format, a.a_format, kExpertNT));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int sms, const char** why)
 {
     *why = nullptr;
     if (a.N == 0 || (a.kind == kExpertWgrad ? a.M == 0 : a.layout.rows == 0)) return cudaSuccess;
@@ -133,6 +189,10 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int, co
     p.max_tiles = (int)a.layout.max_tiles;
     const cudaError_t e = device_error_word(&p.err);
     if (e != cudaSuccess) return e;
+    static_assert(kExpertNT == kExpertPad, "a token tile is one of the plan's blocks");
+    if ((a.kind == kExpertGlu || (a.kind == kExpertGemm && !a.b_mn)) &&
+        expert_few_rows(a.T, a.k, a.E, a.kind == kExpertGlu ? 2 * a.N : a.N, a.K, sms))
+        return a.kind == kExpertGlu ? launch_few_rows<kEpiGlu>(a, p, st, sms, why) : launch_few_rows<kEpiAct>(a, p, st, sms, why);
     switch (a.kind) {
     case kExpertGlu: return launch_pair<kEpiGlu, kRows>(a, p, st, why);
     case kExpertGluBwd: return launch_pair<kEpiGluBwd, kRowsMn>(a, p, st, why);

@@ -43,7 +43,7 @@ struct SortArgs {
     int64_t n;                      // assignments
     int E;
     int32_t* plan;
-    int tiles_at, row_of_at;
+    int tiles_at, blocks_at, row_of_at;
 };
 
 __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int ctas)
@@ -157,11 +157,12 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
         __syncwarp();
         if (i + lane < to) row_of[i + lane] = row;
     });
-    // row tiles of the products, in groups of neighbours of one expert
+    // row tiles of the products, in groups of neighbours of one expert, and blocks
     if (rank == 0) {
         __threadfence_block();
         __syncthreads();
         int4* tiles = reinterpret_cast<int4*>(a.plan + a.tiles_at);
+        int4* blocks = reinterpret_cast<int4*>(a.plan + a.blocks_at);
         for (int e = warp; e < E; e += kSortWarps) {
             const int32_t begin = a.plan[e], end = a.plan[e + 1], t0 = first_tile[e];
             const int32_t m = (end - begin + kExpertTile - 1) / kExpertTile;
@@ -170,6 +171,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
                 const int32_t size = left < kExpertGroup ? left : kExpertGroup;
                 tiles[t0 + i] = make_int4(t0 + g, e << 8 | size, begin + g * kExpertTile, end);
             }
+            const int32_t b0 = begin / kExpertPad, nb = (end - begin) / kExpertPad, last = a.plan[E + 1 + e] - (nb - 1) * kExpertPad;
+            for (int32_t i = lane; i < nb; i += 32)
+                blocks[b0 + i] = make_int4(e, b0, nb, i + 1 < nb ? kExpertPad : last);
         }
     }
 }
@@ -200,6 +204,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __res
                                                                   int64_t chunks, V* __restrict__ out)
 {
     pdl_enter();
+    pdl_trigger();                      // (resident as a whole: the next kernel prepares under this one)
     const int64_t pads = (int64_t)seg.E * chunks, items = pads + T * chunks;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         if (it < pads) {
@@ -444,7 +449,8 @@ ExpertLayout expert_layout(int64_t T, int k, int E)
     l.rows = (n + (kExpertPad - 1) * active) & ~(int64_t)(kExpertPad - 1);
     l.max_tiles = l.rows / kExpertTile + active;
     l.tiles_at = (2 * (int64_t)E + 2 + 3) & ~(int64_t)3;
-    l.row_of_at = l.tiles_at + 4 * l.max_tiles;
+    l.blocks_at = l.tiles_at + 4 * l.max_tiles;
+    l.row_of_at = l.blocks_at + 4 * (l.rows / kExpertPad);
     l.ints = l.row_of_at + n;
     return l;
 }
@@ -458,7 +464,7 @@ cudaError_t launch_expert_plan(const ExpertRowsArgs& a, cudaStream_t st)
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_expert_plan),
                                    (kSortWarps + 3) * kExpertMax * (int)sizeof(int32_t));
     if (e != cudaSuccess) return e;
-    SortArgs s{a.ids, n, a.E, a.plan_out, (int)a.layout.tiles_at, (int)a.layout.row_of_at};
+    SortArgs s{a.ids, n, a.E, a.plan_out, (int)a.layout.tiles_at, (int)a.layout.blocks_at, (int)a.layout.row_of_at};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kSortThreads);

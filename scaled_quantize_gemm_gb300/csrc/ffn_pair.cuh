@@ -46,6 +46,9 @@ struct FfnParams {
     const int32_t* ntiles;
     const int4* tiles;
     int E, max_tiles;
+    // experts, few rows: the plan's blocks of 32 rows, and the weight rows of an expert
+    const int4* blocks;
+    int max_blocks, wrows;
 };
 
 // Ring stages of 32 KB.  Where the epilogue reads rows beside the sums, the

@@ -170,9 +170,11 @@ constexpr int kExpertSlots = 64;     // experts of a token
 // The plan of a routing, int32: offsets [E + 1], counts [E], the number of row
 // tiles; at tiles_at the tiles, four each {first tile of its group, expert << 8
 // | tiles in the group, the group's first row, the expert's last row + 1}; at
-// row_of_at the sorted row of every assignment, or -1.
+// blocks_at every block of 32 rows, four each {expert, the expert's first block,
+// its blocks, rows of the block that are not padding}; at row_of_at the sorted
+// row of every assignment, or -1.
 struct ExpertLayout {
-    int64_t rows = 0, max_tiles = 0, tiles_at = 0, row_of_at = 0, ints = 0;
+    int64_t rows = 0, max_tiles = 0, tiles_at = 0, blocks_at = 0, row_of_at = 0, ints = 0;
 };
 ExpertLayout expert_layout(int64_t T, int k, int E);
 struct ExpertRowsArgs {
