@@ -553,7 +553,7 @@ FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scal
  *   expert, and the end of the last) and counts [E]; the last T k are the sorted
  *   row of each slot or -1.  What lies between is the library's.  Every other call
  *   takes the plan with the T, k, E it was made for.
- *   1 <= k <= 64, 1 <= E <= 1024.
+ *   1 <= k <= 64, 1 <= E <= 1024.  The three calls that move rows take K below 2^23.
  * fp8_expert_dispatch: out[row of (t, j)] = x[t], x [T][K] of elem_bytes 1, 2 or
  *   4 an element; the gradient of x is fp8_expert_combine without weights.
  * fp8_expert_combine: y[t] = residual[t] + sum over j of weights[t][j]

@@ -12,6 +12,8 @@ namespace {
 
 using fp8sq::ExpertLayout;
 
+const int64_t kMaxRow = (int64_t)1 << 23;     // columns of the rows that are moved (a grid dimension counts their chunks)
+
 bool valid_routing(int64_t T, int k, int E)
 {
     return T >= 0 && T < kMaxDim && k >= 1 && k <= fp8sq::kExpertSlots && E >= 1 && E <= fp8sq::kExpertMax;
@@ -208,7 +210,7 @@ FP8SQ_API int fp8_expert_dispatch(const void* x, int elem_bytes, int64_t K, cons
     if (r) return r;
     if (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: elements of 1, 2 or 4 bytes", fn);
     if (K < 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: negative size", fn);
-    if (K >= kMaxDim / 4) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: dimension too large", fn);
+    if (K >= kMaxRow) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: rows of at most %d elements", fn, (int)kMaxRow - 1);
     if ((!x || !out) && T * K != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: null x or out", fn);
     if (!aligned(x, 16) || !aligned(out, 16)) return api_fail(FP8SQ_ERR_MISALIGNED, "%s: x, out must be 16-byte aligned", fn);
     int sms;
@@ -234,7 +236,7 @@ FP8SQ_API int fp8_expert_combine(const void* rows, int dtype, int64_t K, const f
     if (r) return r;
     if (!valid_dtype(dtype)) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: bad dtype", fn);
     if (K < 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: negative size", fn);
-    if (K >= kMaxDim / 4) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: dimension too large", fn);
+    if (K >= kMaxRow) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: rows of at most %d elements", fn, (int)kMaxRow - 1);
     if ((!rows || !y) && T * K != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: null rows or y", fn);
     if (!aligned(rows, 16) || !aligned(residual, 16) || !aligned(y, 16) || !aligned(weights, 4))
         return api_fail(FP8SQ_ERR_MISALIGNED, "%s: rows, residual, y need 16-byte, weights 4-byte alignment", fn);
@@ -266,7 +268,7 @@ FP8SQ_API int fp8_expert_combine_bwd(const void* dy, int dtype, int64_t K, const
     if (r) return r;
     if (!valid_dtype(dtype)) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: bad dtype", fn);
     if (K < 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: negative size", fn);
-    if (K >= kMaxDim / 4) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: dimension too large", fn);
+    if (K >= kMaxRow) return api_fail(FP8SQ_ERR_UNSUPPORTED, "%s: rows of at most %d elements", fn, (int)kMaxRow - 1);
     if ((!dy || !weights) && T * K != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: null dy or weights", fn);
     if (!dweights && !drows && !q_out && T * K != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: no output asked for", fn);
     if (dweights && !rows && T * K != 0) return api_fail(FP8SQ_ERR_INVALID_ARG, "%s: dweights needs the rows", fn);

@@ -67,7 +67,7 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
-    constexpr int smem = FfnSmem<KIND>::BYTES;
+    constexpr int smem = FfnSmem<KIND, GROUP>::BYTES;
     int pairs = 0;
     const cudaError_t e = expert_pairs<KIND, GROUP>(smem, &pairs);
     if (e != cudaSuccess) {
@@ -94,7 +94,7 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
         __nv_bfloat16* z = p.Z;
         if (z) ok = make_tmap_out(&o[0], z, R, a.N, true, 2 * a.N) && make_tmap_out(&o[1], z + a.N, R, a.N, true, 2 * a.N);
     } else {
-        ok = make_tmap_out(&o[1], p.D, GROUP == kWgrad ? a.E * a.M : R, a.N, a.d_dtype == kBF16);
+        ok = make_tmap_lines(&o[1], p.D, GROUP == kWgrad ? a.E * a.M : R, a.N, a.d_dtype == kBF16);
     }
     if (!ok) {
         *why = "cuTensorMapEncodeTiled failed (output)";

@@ -31,12 +31,13 @@ namespace {
 // One cluster of CL CTAs, each warp a contiguous share of the assignments:
 // counts per warp and expert in shared memory, a sum over the warps of a CTA,
 // over the CTAs through distributed shared memory and over the experts (padded
-// to 32), then a second pass over the assignments that gives each its row.  The
+// to 32), after which each assignment gets its row.  The
 // lanes of a warp that hold the same expert find each other with match_any, so
 // the order within an expert is that of the assignments.  One launch for any
 // size; bound by the latency of its few passes (SORT_US us).
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortBatch = 8;       // loads of ids in flight per lane
+constexpr int kSortCtas = 8;        // of the cluster, where one CTA is not enough
 
 struct SortArgs {
     const int32_t* ids;
@@ -54,45 +55,54 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
     int32_t* total = hist + kSortWarps * E;             // [E], read by the other CTAs of the cluster
     int32_t* base = total + E;                          // [E] first row of this CTA's share of an expert
     int32_t* first_tile = base + E;                     // [E]
+    int32_t* first_row = first_tile + E;                // [E]
+    int32_t* count = first_row + E;                     // [E] over the cluster
     __shared__ int32_t scan[2][kSortWarps];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int rank = blockIdx.x;
     for (int e = lane; e < E; e += 32) hist[warp * E + e] = 0;
     pdl_enter();
+    pdl_trigger();                      // (the next kernel's launch runs under this one)
     const int64_t warps = (int64_t)ctas * kSortWarps;
     const int64_t per = ((a.n + warps - 1) / warps + 31) & ~(int64_t)31;
     const int64_t from = ((int64_t)rank * kSortWarps + warp) * per, to = from + per < a.n ? from + per : a.n;
-    // calls f(first index of 32, the lane's expert or -1, the lanes with the same)
-    auto each = [&](auto&& f) {
-        for (int64_t i = from; i < to; i += 32 * kSortBatch) {
-            int32_t id[kSortBatch];
-#pragma unroll
-            for (int b = 0; b < kSortBatch; ++b) {
-                const int64_t at = i + 32 * b + lane;
-                id[b] = at < to ? a.ids[at] : -1;
-            }
-#pragma unroll
-            for (int b = 0; b < kSortBatch; ++b) {
-                if (i + 32 * b >= to) break;
-                const int32_t e = (uint32_t)id[b] < (uint32_t)E ? id[b] : -1;
-                f(i + 32 * b, e, __match_any_sync(0xFFFFFFFFu, e));
-            }
-        }
-    };
     const uint32_t below = (1u << lane) - 1u;
     int32_t* mine = hist + warp * E;
+    // A batch of ids from index i on: the expert of each (or -1) and its rank among
+    // the warp's so far, whose counts go up.
+    int32_t id[kSortBatch], rank_of[kSortBatch];
+    auto batch = [&](int64_t i) {
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            const int64_t at = i + 32 * b + lane;
+            id[b] = at < to ? a.ids[at] : -1;
+        }
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            if (i + 32 * b >= to) break;
+            if ((uint32_t)id[b] >= (uint32_t)E) id[b] = -1;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[b]);
+            const int32_t seen = id[b] >= 0 ? mine[id[b]] : 0;
+            rank_of[b] = seen + __popc(same & below);
+            __syncwarp();
+            if (id[b] >= 0 && (same & below) == 0) mine[id[b]] = seen + __popc(same);
+            __syncwarp();
+        }
+    };
     __syncwarp();
-    each([&](int64_t, int32_t e, uint32_t same) {
-        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
-        __syncwarp();
-    });
+    for (int64_t i = from; i < to; i += 32 * kSortBatch) batch(i);
     __syncthreads();
     for (int e = t; e < E; e += kSortThreads) {
         int32_t run = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int32_t c = hist[w * E + e];
-            hist[w * E + e] = run;
-            run += c;
+        for (int w = 0; w < kSortWarps; w += 8) {
+            int32_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = hist[(w + i) * E + e];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                hist[(w + i) * E + e] = run;
+                run += c[i];
+            }
         }
         total[e] = run;
     }
@@ -105,10 +115,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
     if (t < E) {
         if (ctas > 1) {
             const uint32_t at = smem_addr(total + t);
-            for (int r = 0; r < ctas; ++r) {
-                const int32_t v = (int32_t)ld_shared_cluster_u32(cluster_map(at, (uint32_t)r));
-                if (r < rank) before += v;
-                all += v;
+            int32_t v[kSortCtas];
+#pragma unroll
+            for (int r = 0; r < kSortCtas; ++r) v[r] = (int32_t)ld_shared_cluster_u32(cluster_map(at, (uint32_t)r));
+#pragma unroll
+            for (int r = 0; r < kSortCtas; ++r) {
+                if (r < rank) before += v[r];
+                all += v[r];
             }
         } else {
             all = total[t];
@@ -137,6 +150,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
     if (t < E) {
         base[t] = rs - padded + before;
         first_tile[t] = ts - ntiles;
+        first_row[t] = rs - padded;
+        count[t] = all;
         if (rank == 0) {
             a.plan[t] = rs - padded;
             a.plan[E + 1 + t] = all;
@@ -148,33 +163,32 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
     }
     if (ctas > 1) cluster_sync_all();                   // the totals have been read: a CTA may end
     else __syncthreads();
+    // the rows: the only batch's ranks are at hand, more are found once more
+    // (counting on from the warps before)
     int32_t* row_of = a.plan + a.row_of_at;
-    each([&](int64_t i, int32_t e, uint32_t same) {
-        int32_t row = -1;
-        if (e >= 0) row = base[e] + mine[e] + __popc(same & below);
-        __syncwarp();
-        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (i + lane < to) row_of[i + lane] = row;
-    });
-    // row tiles of the products, in groups of neighbours of one expert, and blocks
-    if (rank == 0) {
-        __threadfence_block();
-        __syncthreads();
-        int4* tiles = reinterpret_cast<int4*>(a.plan + a.tiles_at);
-        int4* blocks = reinterpret_cast<int4*>(a.plan + a.blocks_at);
-        for (int e = warp; e < E; e += kSortWarps) {
-            const int32_t begin = a.plan[e], end = a.plan[e + 1], t0 = first_tile[e];
-            const int32_t m = (end - begin + kExpertTile - 1) / kExpertTile;
-            for (int32_t i = lane; i < m; i += 32) {
-                const int32_t g = i / kExpertGroup * kExpertGroup, left = m - g;
-                const int32_t size = left < kExpertGroup ? left : kExpertGroup;
-                tiles[t0 + i] = make_int4(t0 + g, e << 8 | size, begin + g * kExpertTile, end);
-            }
-            const int32_t b0 = begin / kExpertPad, nb = (end - begin) / kExpertPad, last = a.plan[E + 1 + e] - (nb - 1) * kExpertPad;
-            for (int32_t i = lane; i < nb; i += 32)
-                blocks[b0 + i] = make_int4(e, b0, nb, i + 1 < nb ? kExpertPad : last);
+    const bool again = per > 32 * kSortBatch;
+    for (int64_t i = from; i < to; i += 32 * kSortBatch) {
+        if (again) batch(i);
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            const int64_t at = i + 32 * b + lane;
+            const int32_t e = id[b];
+            if (at < to) row_of[at] = e >= 0 ? base[e] + rank_of[b] + (again ? 0 : mine[e]) : -1;
         }
+    }
+    // row tiles of the products, in groups of neighbours of one expert, and blocks
+    int4* tiles = reinterpret_cast<int4*>(a.plan + a.tiles_at);
+    int4* blocks = reinterpret_cast<int4*>(a.plan + a.blocks_at);
+    for (int e = rank + ctas * warp; e < E; e += ctas * kSortWarps) {
+        const int32_t begin = first_row[e], n = count[e], end = begin + ((n + kExpertPad - 1) & ~(kExpertPad - 1));
+        const int32_t m = (end - begin + kExpertTile - 1) / kExpertTile, t0 = first_tile[e];
+        for (int32_t i = lane; i < m; i += 32) {
+            const int32_t g = i / kExpertGroup * kExpertGroup, left = m - g;
+            const int32_t size = left < kExpertGroup ? left : kExpertGroup;
+            tiles[t0 + i] = make_int4(t0 + g, e << 8 | size, begin + g * kExpertTile, end);
+        }
+        const int32_t b0 = begin / kExpertPad, nb = (end - begin) / kExpertPad, last = n - (nb - 1) * kExpertPad;
+        for (int32_t i = lane; i < nb; i += 32) blocks[b0 + i] = make_int4(e, b0, nb, i + 1 < nb ? kExpertPad : last);
     }
 }
 
@@ -195,53 +209,53 @@ struct Segments {
 
 constexpr int kMoveThreads = 256;
 
-// An item is one chunk of kMoveThreads vectors of a token's row: one load, k
-// stores a thread.  Before them the experts' padding, a chunk of all of an
-// expert's (at most 31) rows an item.
+// CTAs of a column (blockIdx.y: a chunk of kMoveThreads vectors of the rows) take
+// the tokens in turn: one load, k stores a thread, the next token's load on its way
+// while this one is stored.  Before them the experts' padding (at most 31 rows
+// each), shared out likewise.
 template <typename V>
 __global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __restrict__ x, const int32_t* __restrict__ row_of,
                                                                   Segments seg, int64_t T, int k, int64_t vecs,
-                                                                  int64_t chunks, V* __restrict__ out)
+                                                                  V* __restrict__ out)
 {
     pdl_enter();
     pdl_trigger();                      // (resident as a whole: the next kernel prepares under this one)
-    const int64_t pads = (int64_t)seg.E * chunks, items = pads + T * chunks;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        if (it < pads) {
-            const int e = (int)(it / chunks);
-            const int64_t c = (it - (int64_t)e * chunks) * kMoveThreads + threadIdx.x;
-            const int64_t end = seg.pad_end(e);
-            if (c < vecs)
-                for (int64_t r = seg.pad_begin(e); r < end; ++r) out[r * vecs + c] = V{};
-            continue;
-        }
-        const int64_t t = (it - pads) / chunks, c = (it - pads - t * chunks) * kMoveThreads + threadIdx.x;
-        if (c >= vecs) continue;
-        const V v = x[t * vecs + c];
+    const int64_t c = (int64_t)blockIdx.y * kMoveThreads + threadIdx.x;
+    if (c >= vecs) return;
+    int64_t t = blockIdx.x;
+    V next{};
+    if (t < T) next = x[t * vecs + c];
+    for (int e = blockIdx.x; e < seg.E; e += gridDim.x) {
+        const int64_t end = seg.pad_end(e);
+        for (int64_t r = seg.pad_begin(e); r < end; ++r) out[r * vecs + c] = V{};
+    }
+    for (; t < T; t += gridDim.x) {
+        const V v = next;
+        if (t + gridDim.x < T) next = x[(t + gridDim.x) * vecs + c];
         const int32_t* to = row_of + t * k;
 #pragma unroll 4
         for (int j = 0; j < k; ++j) {
-            const int64_t r = __ldg(to + j);
+            const int32_t r = __ldg(to + j);
             if (r >= 0 && r < seg.rows) out[r * vecs + c] = v;
         }
     }
 }
 
 // ------------------------------------------------------------------ combine
-// An item is a chunk of kMoveThreads vectors of a token's row, up to eight rows'
-// loads in flight a thread; fp32 sums in the order of the slots, the residual
-// last.  y may be the residual itself.
+// CTAs of a column (blockIdx.y: a chunk of kMoveThreads vectors) take the tokens in
+// turn, up to eight rows' loads in flight a thread; fp32 sums in the order of the
+// slots, the residual last.  y may be the residual itself.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* __restrict__ rows, const int32_t* __restrict__ row_of,
                                                                  const float* __restrict__ w, const T* res, int64_t nt,
-                                                                 int k, int64_t K, int64_t chunks, int64_t R, T* y)
+                                                                 int k, int64_t K, int64_t R, T* y)
 {
     using P = Pack<T, VEC>;
     using Raw = typename P::Raw;
     pdl_enter();
-    for (int64_t it = blockIdx.x; it < nt * chunks; it += gridDim.x) {
-        const int64_t t = it / chunks, c = ((it - t * chunks) * kMoveThreads + threadIdx.x) * VEC;
-        if (c >= K) continue;
+    const int64_t c = ((int64_t)blockIdx.y * kMoveThreads + threadIdx.x) * VEC;
+    if (c >= K) return;
+    for (int64_t t = blockIdx.x; t < nt; t += gridDim.x) {
         float acc[VEC] = {};
         Raw rr{};
         if (res) rr = *reinterpret_cast<const Raw*>(res + t * K + c);
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* __rest
             float wj[FLY];
 #pragma unroll
             for (int j = 0; j < FLY; ++j) {
-                int64_t r = -1;
+                int32_t r = -1;
                 if (j0 + j < k) r = __ldg(row_of + t * k + j0 + j);
                 wj[j] = 0.0f;
                 raw[j] = Raw{};
@@ -307,7 +321,7 @@ struct CombineBwdOut {
     float* dw;
 };
 template <typename T, int VEC, int JB>
-__global__ void __launch_bounds__(256) k_expert_combine_bwd(const T* __restrict__ dy, const T* __restrict__ rows,
+__global__ void __launch_bounds__(256, JB <= 4 ? 4 : 2) k_expert_combine_bwd(const T* __restrict__ dy, const T* __restrict__ rows,
                                                             const int32_t* __restrict__ row_of, const float* __restrict__ w,
                                                             Segments seg, int64_t nt, int k, int64_t K, CombineBwdOut o)
 {
@@ -331,11 +345,11 @@ __global__ void __launch_bounds__(256) k_expert_combine_bwd(const T* __restrict_
     int par = 0;
     for (int64_t t = blockIdx.x; t < nt; t += gridDim.x) {
         for (int j0 = 0; j0 < k; j0 += JB) {
-            int64_t at[JB];
+            int32_t at[JB];
             float wj[JB], dot[JB] = {};
 #pragma unroll
             for (int j = 0; j < JB; ++j) {
-                int64_t r = j0 + j < k ? __ldg(row_of + t * k + j0 + j) : -1;
+                const int32_t r = j0 + j < k ? __ldg(row_of + t * k + j0 + j) : -1;
                 at[j] = r < seg.rows ? r : -1;
                 wj[j] = at[j] >= 0 ? __ldg(w + t * k + j0 + j) : 0.0f;
             }
@@ -346,7 +360,7 @@ __global__ void __launch_bounds__(256) k_expert_combine_bwd(const T* __restrict_
                 if (o.dw) {
 #pragma unroll
                     for (int j = 0; j < JB; ++j)
-                        if (at[j] >= 0) raw[j] = __ldg(reinterpret_cast<const Raw*>(rows + at[j] * K + c));
+                        if (at[j] >= 0) raw[j] = __ldg(reinterpret_cast<const Raw*>(rows + (int64_t)at[j] * K + c));
                 }
 #pragma unroll
                 for (int j = 0; j < JB; ++j) {
@@ -359,11 +373,11 @@ __global__ void __launch_bounds__(256) k_expert_combine_bwd(const T* __restrict_
                     }
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) v[i] = d[i] * wj[j];
-                    if (drows) *reinterpret_cast<Raw*>(drows + at[j] * K + c) = P::from_floats(v);
+                    if (drows) *reinterpret_cast<Raw*>(drows + (int64_t)at[j] * K + c) = P::from_floats(v);
                     if (o.q) {
 #pragma unroll
                         for (int i = 0; i < VEC; ++i) amax = max_nan(amax, fabsf(v[i]));
-                        store_codes<VEC>(o.q + at[j] * K + c, v, m, o.fmt);
+                        store_codes<VEC>(o.q + (int64_t)at[j] * K + c, v, m, o.fmt);
                     }
                 }
             }
@@ -401,10 +415,10 @@ cudaError_t combine(const ExpertRowsArgs& a, cudaStream_t st, int sms)
 {
     auto kern = k_expert_combine<T, VEC>;
     const int64_t chunks = cdiv(a.K, kMoveThreads * VEC);
-    const int64_t cap = resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms), items = a.T * chunks;
-    launch_k(kern, (unsigned)(items < cap ? items : cap), kMoveThreads, 0, st, static_cast<const T*>(a.rows),
-             a.plan + a.layout.row_of_at, a.weights, static_cast<const T*>(a.residual), a.T, a.k, a.K, chunks,
-             a.layout.rows, static_cast<T*>(a.y));
+    const int64_t cap = cdiv(resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms), chunks);
+    launch_k(kern, dim3((unsigned)(a.T < cap ? a.T : cap), (unsigned)chunks), kMoveThreads, 0, st,
+             static_cast<const T*>(a.rows), a.plan + a.layout.row_of_at, a.weights, static_cast<const T*>(a.residual), a.T,
+             a.k, a.K, a.layout.rows, static_cast<T*>(a.y));
     return cudaGetLastError();
 }
 template <typename T, int VEC, int JB>
@@ -459,10 +473,10 @@ cudaError_t launch_expert_plan(const ExpertRowsArgs& a, cudaStream_t st)
 {
     const int64_t n = a.T * a.k;
     // one CTA as long as a warp has four rounds of 32 ids (or no more to gain)
-    const int ctas = n <= 4 * 32 * kSortWarps ? 1 : 8;
-    const int smem = (kSortWarps + 3) * a.E * (int)sizeof(int32_t);
+    const int ctas = n <= 4 * 32 * kSortWarps ? 1 : kSortCtas;
+    const int smem = (kSortWarps + 5) * a.E * (int)sizeof(int32_t);
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(k_expert_plan),
-                                   (kSortWarps + 3) * kExpertMax * (int)sizeof(int32_t));
+                                   (kSortWarps + 5) * kExpertMax * (int)sizeof(int32_t));
     if (e != cudaSuccess) return e;
     SortArgs s{a.ids, n, a.E, a.plan_out, (int)a.layout.tiles_at, (int)a.layout.blocks_at, (int)a.layout.row_of_at};
     cudaLaunchConfig_t cfg = {};
@@ -489,10 +503,10 @@ cudaError_t launch_expert_dispatch(const ExpertRowsArgs& a, cudaStream_t st, int
         using V = decltype(v);
         auto kern = k_expert_dispatch<V>;
         const int64_t vecs = bytes / (int64_t)sizeof(V), chunks = cdiv(vecs, kMoveThreads);
-        const int64_t cap = resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms);
-        const int64_t items = (a.T + a.E) * chunks;
-        launch_k(kern, (unsigned)(items < cap ? items : cap), kMoveThreads, 0, st, static_cast<const V*>(a.x),
-                 a.plan + a.layout.row_of_at, Segments{a.plan, a.E, a.layout.rows}, a.T, a.k, vecs, chunks,
+        const int64_t cap = resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms) / chunks;   // resident as a whole
+        const int64_t most = a.T > a.E ? a.T : a.E, ctas = cap < 1 ? 1 : most < cap ? most : cap;
+        launch_k(kern, dim3((unsigned)ctas, (unsigned)chunks), kMoveThreads, 0, st, static_cast<const V*>(a.x),
+                 a.plan + a.layout.row_of_at, Segments{a.plan, a.E, a.layout.rows}, a.T, a.k, vecs,
                  static_cast<V*>(a.rows_out));
         return cudaGetLastError();
     });

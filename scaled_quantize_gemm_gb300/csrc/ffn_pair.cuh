@@ -56,8 +56,8 @@ struct FfnParams {
 // five stages, not six (2000 x 1616 -> 5440 with an fp32 residual 40.0 -> 36.8 us;
 // gated backward of 1056 tokens, 928 -> 7776, 109 -> 106).  Without such reads
 // six are as fast or faster (256 tokens, 4096 -> 2 x 14336: 29.9 against 30.9).
-template <int KIND>
-constexpr int kFfnStages = KIND == kEpiGlu ? 6 : 5;
+template <int KIND, int GROUP = 0>
+constexpr int kFfnStages = KIND == kEpiGlu || (KIND == kEpiAct && GROUP != 0) ? 6 : 5;
 // Epilogue warps: two per TMEM lane quarter; four for glu_bwd, whose epilogue is
 // the longest (an exponential and a reciprocal an element, two outputs) and has
 // more latency to cover than two warps of an SM quarter do.
@@ -66,8 +66,13 @@ constexpr int kFfnEpiWarps = KIND == kEpiGluBwd ? 16 : 8;
 template <int KIND>
 constexpr int kFfnThreads = 32 * (2 + kFfnEpiWarps<KIND>);
 constexpr int kFfnBN = 256, kFfnBH = 128;
-template <int KIND>
-using FfnSmem = Smem<kFfnBH, kFfnStages<KIND>, 2, 32>;      // 32 staging boxes of 1 KB, shared out among the epilogue warps
+template <int KIND, int GROUP = 0>
+struct FfnSmem : Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, 32> {
+    using Base = Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, 32>;
+    // (stage_lines: the swizzle wants the staging areas on 1 KB boundaries)
+    static constexpr int STG_OFF = KIND == kEpiAct && GROUP != 0 ? Base::BAR_OFF + 1024 : Base::STG_OFF;
+    static constexpr int BYTES = STG_OFF + Base::BYTES - Base::STG_OFF;
+};      // 32 staging boxes of 1 KB, shared out among the epilogue warps
 
 // ------------------------------------------------------------------ epilogue pieces
 __device__ __forceinline__ uint32_t pack_bf16(float2 v)
@@ -188,46 +193,37 @@ struct Stager {
     }
 };
 
-// 32 columns of sums, scaled, as bf16 or fp32 through two halves of a warp's
-// staging area in turn: a half is written again once the bulk stores of two
-// turns ago have read it.
-__device__ __forceinline__ void stage_halves(uint8_t* buf, int lane, uint32_t& half, const CUtensorMap* m,
-                                             const uint32_t (&r)[32], float scale, bool f32, int col, int row0, int left)
+// One epilogue warp's 32 rows x 128 bytes of the output (64 bf16 or 32 fp32 columns)
+// through its 4 KB staging area and one bulk store, in the tensor map's 128-byte
+// swizzle (16-byte piece j of row r at piece j ^ (r & 7): no bank conflicts).  Whole
+// 128-byte lines, because the TMA unit takes the stores row by row beside the
+// loads: with 32-byte boxes they were as many requests as eight K blocks of loads.
+template <bool F32>
+__device__ __forceinline__ void stage_lines(uint8_t* buf, int lane, const CUtensorMap* m, const uint32_t* r, float scale,
+                                            int col, int row0)
 {
-    auto turn = [&](auto&& fill, int cols, int at) {
-        uint8_t* p = buf + half * 2 * kStageBytes;
-        half ^= 1u;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();
-        fill(p + 32 * lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            for (int i = 0; i < 2; ++i)
-                if (at + i * cols < left) bulk_store_2d(m, col + at + i * cols, row0, p + i * kStageBytes);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    uint8_t* row = buf + 128 * lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+                w[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[4 * j + i]), scale));
+            } else {
+                const int k = 8 * j + 2 * i;
+                w[i] = pack_bf16(__fmul2_rn(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), f2(scale)));
+            }
         }
-    };
-    auto v = [&](int j) {
-        return __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
-    };
-    if (!f32) {
-        turn([&](uint8_t* p) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4*>(p + (c >> 1) * kStageBytes + (c & 1) * 16) =
-                    make_uint4(pack_bf16(v(4 * c)), pack_bf16(v(4 * c + 1)), pack_bf16(v(4 * c + 2)), pack_bf16(v(4 * c + 3)));
-        }, 16, 0);
-    } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            turn([&](uint8_t* p) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float2 a = v(8 * h + 2 * c), b = v(8 * h + 2 * c + 1);
-                    *reinterpret_cast<float4*>(p + (c >> 1) * kStageBytes + (c & 1) * 16) = make_float4(a.x, a.y, b.x, b.y);
-                }
-            }, 8, 16 * h);
+        *reinterpret_cast<uint4*>(row + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        bulk_store_2d(m, col, row0, buf);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
 
@@ -364,10 +360,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                uint32_t idesc, TileSched sched, const __grid_constant__ CUtensorMap tmO0,
                const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2)
 {
-    constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = kFfnStages<KIND>;
+    constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = kFfnStages<KIND, GROUP>;
     constexpr bool b_mn = KIND == kEpiGluBwd || GROUP >= kRowsMn;          // (glu_bwd: Wd [K][F])
     constexpr bool a_mn = GROUP == kWgrad;
-    using L = FfnSmem<KIND>;
+    using L = FfnSmem<KIND, GROUP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -544,7 +540,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             }
         };
         int lt = 0;
-        [[maybe_unused]] uint32_t half = 0;
         for (int t = cid; t < num_tiles; t += ncl) {
             const PairTile x = pair_tile<GROUP>(p, sched, t);
             const bool some = GROUP != kWgrad || x.nkb > 0;          // (else zeros)
@@ -569,36 +564,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             tc_fence_after();
             if constexpr (GROUP != kNoGroups && KIND == kEpiAct) {
                 // The product alone: short contractions (a weight gradient's few
-                // hundred rows) leave it little time, so the next 32 columns leave
-                // tensor memory while these are stored, and the accumulator is handed
-                // back before the last are.
-                constexpr int CHUNKS = TN / PARTS / 32;
-                uint32_t r[2][32];
-                auto load = [&](int i) {
+                // hundred rows) leave it little time, so it stores whole lines, and
+                // hands the accumulator back before its last are on their way.
+                constexpr int HALF = TN / PARTS / 2;                   // 64 columns
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[2][32];
                     if (some) {
-                        tmem_ld_32x32b_x32(taddr + (uint32_t)(c_begin + 32 * i), r[i & 1]);
+                        __syncwarp();                  // tcgen05.ld takes a converged warp
+                        tmem_ld_32x32b_x32(taddr + (uint32_t)(c_begin + HALF * h), r[0]);
+                        tmem_ld_32x32b_x32(taddr + (uint32_t)(c_begin + HALF * h + 32), r[1]);
+                        tmem_ld_wait_for(r[0]);
+                        tmem_ld_wait_for(r[1]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[i & 1][j] = 0;
+                        for (int j = 0; j < 64; ++j) r[j >> 5][j & 31] = 0;
                     }
-                };
-                __syncwarp();                  // tcgen05.ld takes a converged warp
-                load(0);
-                if (some) tmem_ld_wait_for(r[0]);
-#pragma unroll
-                for (int i = 0; i < CHUNKS; ++i) {
-                    if (i + 1 < CHUNKS) {
-                        load(i + 1);
-                    } else {
+                    if (h == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (some && lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
                     }
-                    const int col = nb * TN + c_begin + 32 * i, left = p.N - col;
-                    if (row0 < end && left > 0)
-                        stage_halves(out.buf, lane, half, &tmO1, r[i & 1], some ? scale : 0.0f, p.d_f32, col, store0, left);
-                    __syncwarp();
-                    if (i + 1 < CHUNKS && some) tmem_ld_wait_for(r[(i + 1) & 1]);
+                    const int col = nb * TN + c_begin + HALF * h;
+                    if (row0 < end && col < p.N) {
+                        const float sc = some ? scale : 0.0f;
+                        if (p.d_f32) {
+                            stage_lines<true>(out.buf, lane, &tmO1, r[0], sc, col, store0);
+                            if (col + 32 < p.N) stage_lines<true>(out.buf, lane, &tmO1, r[1], sc, col + 32, store0);
+                        } else {
+                            stage_lines<false>(out.buf, lane, &tmO1, &r[0][0], sc, col, store0);
+                        }
+                    }
                 }
             } else {
 #pragma unroll 1

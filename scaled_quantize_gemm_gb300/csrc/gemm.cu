@@ -1306,6 +1306,20 @@ bool make_tmap_out(CUtensorMap* m, void* D, int64_t M, int64_t N, bool bf16, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_lines(CUtensorMap* m, void* D, int64_t M, int64_t N, bool bf16)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const uint64_t esz = bf16 ? 2 : 4;
+    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    cuuint64_t strides[1] = {(cuuint64_t)(N * esz)};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / esz), 32u};
+    cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, D, dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Co-resident CTA pairs of the pair kernel on the current device (queried
 // once per device and output type; the kernel's resources never change).
 // The cache entries are atomics: concurrent first calls may both query and
