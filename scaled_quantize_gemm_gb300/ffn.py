@@ -35,63 +35,15 @@ def _capturing() -> bool:
     return torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
 
 
-class GatedFFN:
-    """One sublayer's weights, scaling states and buffers.
+class Buffers:
+    """A block's scratch: buffers by name that live as long as the block."""
 
-    gamma [K] fp32, beta [K] fp32 or None, w_gate_up [2F][K] bf16 (the gate's
-    rows, then the up projection's), w_down [K][F] bf16; K, F multiples of 16.
-    A training step takes a number of tokens that is a multiple of 16 (the
-    weight gradients contract over them); ``decode`` takes any number.
-
-    The buffers are the block's own, one set for all calls, so its calls follow
-    one another on one stream (or in streams that wait for each other), and one
-    forward is kept at a time.  Calls may be captured into CUDA graphs, also
-    for several numbers of tokens: a buffer that a call was given lives as long
-    as the block.
-    """
-
-    def __init__(self, gamma, beta, w_gate_up, w_down, act: int = sq.ACT_SILU, eps: float = 1e-5,
-                 history_len: int = 16):
-        F2, K = w_gate_up.shape
-        if F2 % 32 or K % 16 or tuple(w_down.shape) != (K, F2 // 2):
-            raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not make a "
-                             "gated block of sizes that are multiples of 16")
-        self.gamma, self.beta, self.w_gate_up, self.w_down = gamma, beta, w_gate_up, w_down
-        self.K, self.F, self.act, self.eps, self.H = K, F2 // 2, act, eps, history_len
-        dev = w_gate_up.device
-        self._states = torch.empty(6 * sq.state_floats(history_len), device=dev)
-        sq.fp8_scale_init(self.states, 6, history_len)
-        self.q_gate_up = torch.empty((F2, K), dtype=torch.uint8, device=dev)
-        self.q_down = torch.empty((K, self.F), dtype=torch.uint8, device=dev)
-        self._frozen = torch.empty_like(self.states)     # the states as they were when the weights were last cast
-        self._cast = False                   # ... which they have been
-        self._live, self._kept_scales = self._split(self.states), self._split(self._frozen)
+    def __init__(self, device):
+        self._device = device
         self._buffers = {}                   # name -> the largest buffer so far, in bytes
         self._views = {}                     # name -> its last view
         self._kept = []                      # every buffer: a captured graph may replay on it
         self._spaces = []                    # the workspaces among them
-        self._saved = None
-
-    # ------------------------------------------------------------ states and scratch
-    @property
-    def states(self):
-        """the six delayed-scaling states, one after another; assigning copies into them (views and graphs hold them)"""
-        return self._states
-
-    @states.setter
-    def states(self, values):
-        self._states.copy_(values)
-
-    def _split(self, states):
-        """the six states and the dequantisation steps of their codes (one element each), as views"""
-        blocks = states.view(6, sq.state_floats(self.H))
-        return list(blocks), list(blocks[:, -1:])
-
-    def _state(self, i):
-        return self._live[0][i]
-
-    def _scale(self, i):
-        return self._live[1][i]
 
     def _bytes(self, name, nbytes, zero=False):
         """A buffer of at least `nbytes` that lives as long as the block.  A larger one than before is at least twice
@@ -100,7 +52,7 @@ class GatedFFN:
         t = self._buffers.get(name)
         if t is None or t.numel() < nbytes:
             n = max(nbytes, 0 if t is None else 2 * t.numel())
-            t = (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=self.states.device)
+            t = (torch.zeros if zero else torch.empty)(n, dtype=torch.uint8, device=self._device)
             self._kept.append(t)
             if zero:
                 self._spaces.append(t)
@@ -128,6 +80,62 @@ class GatedFFN:
         up leaves its counters as they were, and later calls would join their sums too early or never."""
         for t in self._spaces:
             t.zero_()
+
+
+class GatedFFN(Buffers):
+    """One sublayer's weights, scaling states and buffers.
+
+    gamma [K] fp32, beta [K] fp32 or None, w_gate_up [2F][K] bf16 (the gate's
+    rows, then the up projection's), w_down [K][F] bf16; K, F multiples of 16.
+    A training step takes a number of tokens that is a multiple of 16 (the
+    weight gradients contract over them); ``decode`` takes any number.
+
+    The buffers are the block's own, one set for all calls, so its calls follow
+    one another on one stream (or in streams that wait for each other), and one
+    forward is kept at a time.  Calls may be captured into CUDA graphs, also
+    for several numbers of tokens: a buffer that a call was given lives as long
+    as the block.
+    """
+
+    def __init__(self, gamma, beta, w_gate_up, w_down, act: int = sq.ACT_SILU, eps: float = 1e-5,
+                 history_len: int = 16):
+        F2, K = w_gate_up.shape
+        if F2 % 32 or K % 16 or tuple(w_down.shape) != (K, F2 // 2):
+            raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not make a "
+                             "gated block of sizes that are multiples of 16")
+        self.gamma, self.beta, self.w_gate_up, self.w_down = gamma, beta, w_gate_up, w_down
+        self.K, self.F, self.act, self.eps, self.H = K, F2 // 2, act, eps, history_len
+        dev = w_gate_up.device
+        super().__init__(dev)
+        self._states = torch.empty(6 * sq.state_floats(history_len), device=dev)
+        sq.fp8_scale_init(self.states, 6, history_len)
+        self.q_gate_up = torch.empty((F2, K), dtype=torch.uint8, device=dev)
+        self.q_down = torch.empty((K, self.F), dtype=torch.uint8, device=dev)
+        self._frozen = torch.empty_like(self.states)     # the states as they were when the weights were last cast
+        self._cast = False                   # ... which they have been
+        self._live, self._kept_scales = self._split(self.states), self._split(self._frozen)
+        self._saved = None
+
+    # ------------------------------------------------------------ states and scratch
+    @property
+    def states(self):
+        """the six delayed-scaling states, one after another; assigning copies into them (views and graphs hold them)"""
+        return self._states
+
+    @states.setter
+    def states(self, values):
+        self._states.copy_(values)
+
+    def _split(self, states):
+        """the six states and the dequantisation steps of their codes (one element each), as views"""
+        blocks = states.view(6, sq.state_floats(self.H))
+        return list(blocks), list(blocks[:, -1:])
+
+    def _state(self, i):
+        return self._live[0][i]
+
+    def _scale(self, i):
+        return self._live[1][i]
 
     def calibrate(self, x):
         """One forward pass that sets the activations' and weights' scales from what it records."""
