@@ -546,8 +546,9 @@ FP8SQ_API int fp8_glu_bwd(const uint8_t* dY, int dy_format, const float* dy_scal
  * an expert lie together, in the order of (token, slot), in buffers of
  * R = fp8_expert_rows(T, k, E) rows; an expert's segment begins and ends on a
  * multiple of 32 rows, and the rows that fill it up hold zeros: dispatch and
- * combine_bwd write them so, and the products of zero rows are zero rows.  Rows
- * behind the last segment are neither read nor written.
+ * combine_bwd write them so, and the products of zero rows (with finite weights
+ * and scales) are zero rows.  Rows behind the last segment are neither read nor
+ * written.
  * fp8_expert_plan: writes the plan of a routing, int32 [fp8_expert_plan_ints],
  *   16-byte aligned.  The first 2 E + 1 are offsets [E + 1] (the first row of each
  *   expert, and the end of the last) and counts [E]; the last T k are the sorted

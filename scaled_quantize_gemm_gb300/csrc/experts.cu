@@ -96,6 +96,7 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
     } else {
         ok = make_tmap_lines(&o[1], p.D, GROUP == kWgrad ? a.E * a.M : R, a.N, a.d_dtype == kBF16);
     }
+    if (GROUP != kWgrad) ok = ok && make_tmap(&o[2], a.A, a.K, R, 32);       // A in boxes of 32 rows (pair_rows)
     if (!ok) {
         *why = "cuTensorMapEncodeTiled failed (output)";
         return cudaErrorInvalidValue;

@@ -34,7 +34,8 @@ namespace {
 // to 32), after which each assignment gets its row.  The
 // lanes of a warp that hold the same expert find each other with match_any, so
 // the order within an expert is that of the assignments.  One launch for any
-// size; bound by the latency of its few passes (SORT_US us).
+// size; bound by the latency of its few passes (one GB300, under the profiler: 512
+// slots 5.0 us in one CTA, 65536 slots 8.5).
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortBatch = 8;       // loads of ids in flight per lane
 constexpr int kSortCtas = 8;        // of the cluster, where one CTA is not enough

@@ -95,7 +95,7 @@ __device__ __forceinline__ RowsTile rows_tile(const FfnParams& p, const RowsPara
         const int i = tile - d.y * w.wtiles, size = max(d.z, 1);
         x.wt = i / size;
         x.mt = min(max(d.y + i - x.wt * size, 0), p.max_blocks - 1);
-        x.expert = min(d.x, p.E - 1);
+        x.expert = min(max(d.x, 0), p.E - 1);
         x.wrow = x.expert * p.wrows;
         x.live = x.mt == tile / w.wtiles ? d.w : load(p.blocks + x.mt).w;
     } else {
