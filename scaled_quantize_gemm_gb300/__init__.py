@@ -641,34 +641,43 @@ def fp8_rmsnorm_bwd(dy, x, gamma, rstd, dx, dgamma, workspace, dres=None, stream
         _mat(dx, "dx", M, K, dt), _vec(dgamma, "dgamma", K), *_ws(workspace), _stream(stream)))
 
 
+_routing_sizes = {}
+
+
+def _expert_sizes(tokens: int, top_k: int, experts: int) -> tuple:
+    """(integers of the plan, rows of the sorted buffers) of a routing's sizes, asked of the library once"""
+    key = (tokens, top_k, experts)
+    size = _routing_sizes.get(key)
+    if size is None:
+        if len(_routing_sizes) >= 4096:
+            _routing_sizes.clear()
+        L = lib()
+        size = _routing_sizes[key] = (L.fp8_expert_plan_ints(*key), L.fp8_expert_rows(*key))
+    return size
+
+
 def fp8_expert_rows(tokens: int, top_k: int, experts: int) -> int:
     """rows of the sorted buffers of a routing of `tokens` tokens to top_k experts each"""
-    return (_lib or lib()).fp8_expert_rows(tokens, top_k, experts)
+    return _expert_sizes(tokens, top_k, experts)[1]
 
 
 def fp8_expert_plan_ints(tokens: int, top_k: int, experts: int) -> int:
-    return (_lib or lib()).fp8_expert_plan_ints(tokens, top_k, experts)
+    return _expert_sizes(tokens, top_k, experts)[0]
 
 
 def expert_plan_views(plan, tokens: int, top_k: int, experts: int) -> tuple:
     """(offsets [E + 1], counts [E], row_of [tokens][top_k]) of a plan: each expert's first sorted row, its rows, and
     the sorted row of every slot or -1"""
-    n = fp8_expert_plan_ints(tokens, top_k, experts)
-    return (plan[:experts + 1], plan[experts + 1:2 * experts + 1],
-            plan[n - tokens * top_k:n].view(tokens, top_k))
-
-
-_plan_sizes = {}
+    n = _expert_sizes(tokens, top_k, experts)[0]
+    _need(plan, "plan", _t().int32, 4 * n)
+    at, view = plan.storage_offset(), plan.as_strided           # (half the host time of slices)
+    return (view((experts + 1,), (1,), at), view((experts,), (1,), at + experts + 1),
+            view((tokens, top_k), (top_k, 1), at + n - tokens * top_k))
 
 
 def _routing(plan, tokens: int, top_k: int, experts: int) -> tuple:
     """(pointer of the plan, rows of the sorted buffers)"""
-    key = (tokens, top_k, experts)
-    size = _plan_sizes.get(key)
-    if size is None:
-        if len(_plan_sizes) >= 4096:
-            _plan_sizes.clear()
-        size = _plan_sizes[key] = (fp8_expert_plan_ints(*key), fp8_expert_rows(*key))
+    size = _expert_sizes(tokens, top_k, experts)
     if plan is None or plan.dtype is not _torch.int32 or plan.numel() < size[0] or not plan.is_contiguous():
         _need(plan, "plan", _torch.int32, 4 * size[0])
     return plan.data_ptr(), size[1]

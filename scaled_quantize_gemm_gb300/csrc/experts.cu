@@ -111,28 +111,30 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
 // Whether k_ffn_rows takes a product with N weight rows an expert (glu: 2F).  The
 // routing is known on the device alone, so the rule goes by its sizes: n = T k
 // assignments make a = n / min(E, n) rows an expert.  The tiles of 256 rows read
-// each weight once whatever the rows; the few-rows kernel shares the weights' bytes out
-// evenly and starts sooner, but reads a weight tile again (from L2) for every 32 rows
-// of an expert.  One GB300, us, few rows / tiles (the weights at the copy rate): 8
-// of 64 experts, 4096 -> 2 x 1792, 1 token 26.3 / 29.5 (17.4), 16 tokens 98.8 / 102.7, 64
-// tokens (a = 9) 138 / 141, 128 tokens (17) 159 / 150, 512 tokens (64) 298 / 162; 4 of 32,
-// 2304 -> 2 x 1040, 64 tokens (9) 27.6 / 32.2, 128 tokens (16) 32.0 / 32.9, 256
-// tokens (32) 38.4 / 33.4; 2 of 16, 3584 -> 4096, 64 tokens (9) 43 / 48, 128 tokens (17) 44 /
-// 49, 256 tokens (34) 54 / 49.
+// each weight once whatever the rows, and store whole lines; the few-rows kernel
+// shares the weights' bytes out evenly and starts sooner, which tells where K is long
+// or the tiles do not go round, but it reads a weight tile again (from L2) for every
+// 32 rows of an expert.  One GB300, us, few rows / tiles (the weights at the copy
+// rate).  Gated: 8 of 64 experts, 4096 -> 2 x 1792, 1 token 25.9 / 29.7 (17.4), 16 tokens
+// 97.0 / 103.5, a = 8 137.5 / 139.4, 12 145.5 / 140.9, 32 201 / 151; 4 of 32, 2304 -> 2 x
+// 1040, 1 token 10.4 / 12.4, a = 8 30.1 / 32.4, 12 31.6 / 32.8; 6 of 96, 1024 -> 2 x 512, 1
+// token 7.4 / 8.9, 8 tokens 12.5 / 12.4, a = 8 23.0 / 21.5.  Plain: 3584 -> 4096, 2 of 16,
+// 8 tokens 28.1 / 31.3, a = 8 43.2 / 46.5; 1792 -> 4096, 8 of 64, 1 token 17.1 / 16.5, a = 8
+// 74.9 / 73.8; 1040 -> 2304, 4 of 32, 1 token 8.3 / 8.4, 16 tokens 18.3 / 14.9; 512 -> 1024, 6 of
+// 96, 1 token 6.8 / 7.3, 16 tokens 13.0 / 10.4.
 constexpr int kExpertNT = 32;
-constexpr double kExpertFewRows = 12.0;
-static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, int sms)
+static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool glu, int sms)
 {
     const ExpertLayout l = expert_layout(T, k, E);
     const int64_t wtiles = (N + BM - 1) / BM, nkb = (K + BK - 1) / BK, most = l.rows / kExpertNT * wtiles;
     if (most > kRowsMaxTiles || most * nkb >= ((int64_t)1 << 31) || sms > kRowsMaxCtas) return false;
-    const double n = (double)T * k, active = E < n ? E : n, a = n / active;
-    return a <= kExpertFewRows;
+    const int64_t n = T * k, active = E < n ? E : n, tiles = active * wtiles;
+    return n <= 10 * active && (nkb > 16 || tiles <= (glu ? 2 * sms : sms / 2));
 }
 
 size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K)
 {
-    if (!expert_few_rows(T, k, E, N, K, 152)) return 0;
+    if (!expert_few_rows(T, k, E, N, K, true, 152)) return 0;          // (the wider rule)
     return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * kExpertNT * BM * sizeof(float);
 }
 
@@ -192,7 +194,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int sms
     if (e != cudaSuccess) return e;
     static_assert(kExpertNT == kExpertPad, "a token tile is one of the plan's blocks");
     if ((a.kind == kExpertGlu || (a.kind == kExpertGemm && !a.b_mn)) &&
-        expert_few_rows(a.T, a.k, a.E, a.kind == kExpertGlu ? 2 * a.N : a.N, a.K, sms))
+        expert_few_rows(a.T, a.k, a.E, a.kind == kExpertGlu ? 2 * a.N : a.N, a.K, a.kind == kExpertGlu, sms))
         return a.kind == kExpertGlu ? launch_few_rows<kEpiGlu>(a, p, st, sms, why) : launch_few_rows<kEpiAct>(a, p, st, sms, why);
     switch (a.kind) {
     case kExpertGlu: return launch_pair<kEpiGlu, kRows>(a, p, st, why);
