@@ -89,7 +89,7 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
     // outputs stored in bulk; a map that the epilogue does not use is a copy of A's
     CUtensorMap o[3] = {ta, ta, ta};
     if constexpr (KIND == kEpiGluBwd) {
-        ok = make_tmap_codes(&o[0], a.q_out, R, a.N, 2 * a.N) && make_tmap_codes(&o[1], a.q_out + a.N, R, a.N, 2 * a.N);
+        ok = make_tmap_codes64(&o[0], a.q_out, R, a.N, 2 * a.N) && make_tmap_codes64(&o[1], a.q_out + a.N, R, a.N, 2 * a.N);
     } else if constexpr (GLU) {
         __nv_bfloat16* z = p.Z;
         if (z) ok = make_tmap_out(&o[0], z, R, a.N, true, 2 * a.N) && make_tmap_out(&o[1], z + a.N, R, a.N, true, 2 * a.N);
@@ -190,6 +190,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int sms
     p.ntiles = a.plan + 2 * a.E + 1;
     p.tiles = reinterpret_cast<const int4*>(a.plan + a.layout.tiles_at);
     p.max_tiles = (int)a.layout.max_tiles;
+    p.rows = (int)a.layout.rows;
     const cudaError_t e = device_error_word(&p.err);
     if (e != cudaSuccess) return e;
     static_assert(kExpertNT == kExpertPad, "a token tile is one of the plan's blocks");

@@ -200,11 +200,16 @@ struct Segments {
     const int32_t* plan;
     int E;
     int64_t rows;                   // of the sorted buffers; nothing is touched past them
-    __device__ __forceinline__ int64_t pad_begin(int e) const { return (int64_t)plan[e] + plan[E + 1 + e]; }
+    // (at most kExpertPad - 1 of them, inside the buffers, whatever the plan holds)
     __device__ __forceinline__ int64_t pad_end(int e) const
     {
         const int64_t end = plan[e + 1];
         return end < rows ? end : rows;
+    }
+    __device__ __forceinline__ int64_t pad_begin(int e) const
+    {
+        const int64_t begin = (int64_t)plan[e] + plan[E + 1 + e], least = pad_end(e) - (kExpertPad - 1);
+        return max(max(begin, least), (int64_t)0);
     }
 };
 

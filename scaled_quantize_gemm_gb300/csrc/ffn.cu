@@ -525,9 +525,8 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     static const Kern kerns[3] = {k_ffn_pair<kEpiAct>, k_ffn_pair<kEpiGlu>, k_ffn_pair<kEpiGluBwd>};
     Kern kern = kerns[a.kind];
     int clusters = 0;
-    static_assert((int)FfnSmem<kEpiAct>::BYTES == (int)FfnSmem<kEpiGluBwd>::BYTES, "one size for both");
     const int threads = bwd ? kFfnThreads<kEpiGluBwd> : kFfnThreads<kEpiAct>;
-    const int smem = glu ? FfnSmem<kEpiGlu>::BYTES : FfnSmem<kEpiAct>::BYTES;
+    const int smem = glu ? FfnSmem<kEpiGlu>::BYTES : bwd ? FfnSmem<kEpiGluBwd>::BYTES : FfnSmem<kEpiAct>::BYTES;
     e = ffn_clusters(reinterpret_cast<const void*>(kern), a.kind, 2, threads, smem, &clusters);
     if (e != cudaSuccess) {
         *why = "cluster occupancy query failed";
@@ -549,7 +548,7 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t st, int sms, const char** 
     CUtensorMap o[3] = {ta, ta, ta};
     bool ok = true;
     if (bwd) {
-        ok = make_tmap_codes(&o[0], a.q_out, a.M, a.N, 2 * a.N) && make_tmap_codes(&o[1], a.q_out + a.N, a.M, a.N, 2 * a.N);
+        ok = make_tmap_codes64(&o[0], a.q_out, a.M, a.N, 2 * a.N) && make_tmap_codes64(&o[1], a.q_out + a.N, a.M, a.N, 2 * a.N);
     } else if (glu) {
         __nv_bfloat16* z = p.Z;
         if (z) ok = make_tmap_out(&o[0], z, a.M, a.N, true, 2 * a.N) && make_tmap_out(&o[1], z + a.N, a.M, a.N, true, 2 * a.N);

@@ -45,7 +45,7 @@ struct FfnParams {
     const int32_t* offsets;
     const int32_t* ntiles;
     const int4* tiles;
-    int E, max_tiles;
+    int E, max_tiles, rows;              // rows of the sorted buffers
     // experts, few rows: the plan's blocks of 32 rows, and the weight rows of an expert
     const int4* blocks;
     int max_blocks, wrows;
@@ -66,13 +66,17 @@ constexpr int kFfnEpiWarps = KIND == kEpiGluBwd ? 16 : 8;
 template <int KIND>
 constexpr int kFfnThreads = 32 * (2 + kFfnEpiWarps<KIND>);
 constexpr int kFfnBN = 256, kFfnBH = 128;
+// Staging boxes of 1 KB, shared out among the epilogue warps.
+template <int KIND>
+constexpr int kFfnBoxes = KIND == kEpiGluBwd ? 64 : 32;
 template <int KIND, int GROUP = 0>
-struct FfnSmem : Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, 32> {
-    using Base = Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, 32>;
-    // (stage_lines: the swizzle wants the staging areas on 1 KB boundaries)
-    static constexpr int STG_OFF = KIND == kEpiAct && GROUP != 0 ? Base::BAR_OFF + 1024 : Base::STG_OFF;
+struct FfnSmem : Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, kFfnBoxes<KIND>> {
+    using Base = Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, kFfnBoxes<KIND>>;
+    // (swizzled staging wants its areas on 1 KB boundaries: stage_lines, the codes of glu_bwd)
+    static constexpr int STG_OFF = KIND == kEpiGluBwd || (KIND == kEpiAct && GROUP != 0) ? Base::BAR_OFF + 1024 : Base::STG_OFF;
     static constexpr int BYTES = STG_OFF + Base::BYTES - Base::STG_OFF;
-};      // 32 staging boxes of 1 KB, shared out among the epilogue warps
+};
+     // 32 staging boxes of 1 KB, shared out among the epilogue warps
 
 // ------------------------------------------------------------------ epilogue pieces
 __device__ __forceinline__ uint32_t pack_bf16(float2 v)
@@ -302,7 +306,7 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 // One GB300, us, a few passes on a cool GPU / back to back at the power limit:
 // glu_fwd 16384 x 4096 -> 2 x 14336 with g, u and codes 1040-1070 / 1170-1240 (3640 /
 // 3200 TFLOP/s); gemm_act 16384 x 4096 -> 14336 with bias, gelu_tanh, z and codes
-// 553-569 / 632-667; glu_bwd 2048 x 4096 -> 14336 86 (under the profiler).
+// 553-569 / 632-667; glu_bwd 2048 x 4096 -> 14336 83.
 // A tile of a pair's work: its first row (of A and D), the row its rows end
 // before, its column tile, its expert, and the range of the contraction: the
 // first coordinate, K blocks, 32-wide steps of the last block.
@@ -327,8 +331,9 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
         sched.coords(t - x.expert * per, mb, x.nb);
         x.row0 = mb * 2 * BM;
         x.end = p.M;
-        x.k0 = __ldg(p.offsets + x.expert);
-        const int rows = __ldg(p.offsets + x.expert + 1) - x.k0;
+        // (whatever the plan holds, here and below, the work is bounded and every row inside the buffers)
+        x.k0 = min(max(__ldg(p.offsets + x.expert), 0), p.rows);
+        const int rows = max(min(__ldg(p.offsets + x.expert + 1), p.rows) - x.k0, 0);
         x.nkb = (rows + BK - 1) / BK;
         x.last = (rows - (x.nkb - 1) * BK + 31) / 32;
     } else if constexpr (GROUP != kNoGroups) {
@@ -534,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
     } else {
         const int quarter = warp & 3;       // the TMEM lane quarter this warp may read
         const int part = (warp - 2) >> 2;   // share of the columns
-        constexpr int PARTS = kFfnEpiWarps<KIND> / 4, BOXES = 32 / kFfnEpiWarps<KIND>;
+        constexpr int PARTS = kFfnEpiWarps<KIND> / 4, BOXES = kFfnBoxes<KIND> / kFfnEpiWarps<KIND>;
         float scale = __ldg(p.sA) * __ldg(p.sB);
         const float qm = p.Q ? p.qstate[p.qH] : 1.0f;
         uint32_t amax = 0;
@@ -619,128 +624,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                 }
             } else {
 #pragma unroll 1
-            for (int c = c_begin; c < c_end && row0 < end; c += 32) {
-                const int col = nb * TN + c, left = p.N - col;
-                if (left <= 0) break;
-                __syncwarp();                  // tcgen05.ld takes a converged warp
-                float2 v[16];
-                if constexpr (KIND == kEpiGlu) {
-                    uint32_t rg[32], ru[32];
-                    tmem_ld_32x32b_x32(taddr + (uint32_t)c, rg);
-                    tmem_ld_32x32b_x32(taddr + (uint32_t)(BH + c), ru);
-                    tmem_ld_wait();
-                    float2 g[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        g[j] = __fmul2_rn(make_float2(__uint_as_float(rg[2 * j]), __uint_as_float(rg[2 * j + 1])), f2(scale));
-                        v[j] = __fmul2_rn(make_float2(__uint_as_float(ru[2 * j]), __uint_as_float(ru[2 * j + 1])), f2(scale));
-                    }
-                    if (p.Z) {
-                        out.next_chunk();
-                        out.bf16(&tmO0, g, col, store0, left);
-                        out.bf16(&tmO1, v, col, store0, left);
-                    }
-                    act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = __fmul2_rn(v[j], act_f2<decltype(tag)::act>(g[j]));
-                    });
-                    if (p.Q) max32(amax, v, left, keep);
-                    if (keep) {
-                        if (p.D) store32_bf16(static_cast<__nv_bfloat16*>(p.D) + (int64_t)row * p.N + col, left, v);
-                        if (p.Q) store32_codes(p.Q + (int64_t)row * p.N + col, left, v, qm, p.qfmt);
-                    }
-                    __syncwarp();
-                } else if constexpr (KIND == kEpiAct) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
-                    out.next_chunk();
-                    if (p.bias) {
-                        const int from = (c - c_begin) / 4;       // the lane that holds column c
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const int s = from + j / 2;
-                            v[j] = __fadd2_rn(v[j], make_float2(__shfl_sync(0xFFFFFFFFu, bias.x, s),
-                                                                __shfl_sync(0xFFFFFFFFu, bias.y, s)));
-                            v[j + 1] = __fadd2_rn(v[j + 1], make_float2(__shfl_sync(0xFFFFFFFFu, bias.z, s),
-                                                                        __shfl_sync(0xFFFFFFFFu, bias.w, s)));
-                        }
-                    }
-                    if (p.Z) out.bf16(&tmO0, v, col, store0, left);
-                    act_dispatch(p.act, [&](auto tag) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = act_f2<decltype(tag)::act>(v[j]);
-                    });
-                    if (p.res) {
-                        if (p.res_f32) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_f32(pre, j));
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_bf16(pre, j));
-                        }
-                        if (c + 32 < c_end) fetch(row, col + 32, end);
-                    }
-                    if (p.D) {
-                        if (p.d_f32) out.f32(&tmO1, v, col, store0, left);
-                        else out.bf16(&tmO1, v, col, store0, left);
-                    }
-                    if (p.Q) {
-                        max32(amax, v, left, keep);
-                        out.codes(&tmO2, v, qm, p.qfmt, col, store0, left);
-                    }
-                } else {
-                    // two halves of 16 columns, each 16 bytes of the two boxes' rows
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[16];
-                        __syncwarp();
-                        tmem_ld_32x32b_x16(taddr + (uint32_t)(c + 16 * h), r);
+                for (int c = c_begin; c < c_end && row0 < end; c += 32) {
+                    const int col = nb * TN + c, left = p.N - col;
+                    if (left <= 0) break;
+                    __syncwarp();                  // tcgen05.ld takes a converged warp
+                    float2 v[16];
+                    if constexpr (KIND == kEpiGlu) {
+                        uint32_t rg[32], ru[32];
+                        tmem_ld_32x32b_x32(taddr + (uint32_t)c, rg);
+                        tmem_ld_32x32b_x32(taddr + (uint32_t)(BH + c), ru);
                         tmem_ld_wait();
-                        float2 dg[8], du[8];
+                        float2 g[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            g[j] = __fmul2_rn(make_float2(__uint_as_float(rg[2 * j]), __uint_as_float(rg[2 * j + 1])), f2(scale));
+                            v[j] = __fmul2_rn(make_float2(__uint_as_float(ru[2 * j]), __uint_as_float(ru[2 * j + 1])), f2(scale));
+                        }
+                        if (p.Z) {
+                            out.next_chunk();
+                            out.bf16(&tmO0, g, col, store0, left);
+                            out.bf16(&tmO1, v, col, store0, left);
+                        }
                         act_dispatch(p.act, [&](auto tag) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float2 dh = __fmul2_rn(
-                                    make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
-                                float2 f, d;
-                                act_fd2<decltype(tag)::act>(raw_bf16(pre, j), f, d);
-                                dg[j] = __fmul2_rn(__fmul2_rn(dh, raw_bf16(pre + 2, j)), d);
-                                du[j] = __fmul2_rn(dh, f);
-                            }
+                            for (int j = 0; j < 16; ++j) v[j] = __fmul2_rn(v[j], act_f2<decltype(tag)::act>(g[j]));
                         });
-                        const int cn = c + 16 * (h + 1);
-                        if (cn < c_end) fetch(row, nb * TN + cn, end);
-                        float m = 0.0f;
-                        if (left > 16 * h) {
+                        if (p.Q) max32(amax, v, left, keep);
+                        if (keep) {
+                            if (p.D) store32_bf16(static_cast<__nv_bfloat16*>(p.D) + (int64_t)row * p.N + col, left, v);
+                            if (p.Q) store32_codes(p.Q + (int64_t)row * p.N + col, left, v, qm, p.qfmt);
+                        }
+                        __syncwarp();
+                    } else if constexpr (KIND == kEpiAct) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                m = max3_nan(m, fabsf(dg[j].x), fabsf(dg[j].y));
-                                m = max3_nan(m, fabsf(du[j].x), fabsf(du[j].y));
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = __fmul2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
+                        out.next_chunk();
+                        if (p.bias) {
+                            const int from = (c - c_begin) / 4;       // the lane that holds column c
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                const int s = from + j / 2;
+                                v[j] = __fadd2_rn(v[j], make_float2(__shfl_sync(0xFFFFFFFFu, bias.x, s),
+                                                                    __shfl_sync(0xFFFFFFFFu, bias.y, s)));
+                                v[j + 1] = __fadd2_rn(v[j + 1], make_float2(__shfl_sync(0xFFFFFFFFu, bias.z, s),
+                                                                            __shfl_sync(0xFFFFFFFFu, bias.w, s)));
                             }
                         }
-                        amax = max(amax, __float_as_uint(m) & keep);
-                        const uint4 qg = codes16(dg, qm, p.qfmt), qu = codes16(du, qm, p.qfmt);
-                        if (h == 0) out.reset();        // the previous chunk's boxes have been read
-                        uint8_t* q = out.buf + 32 * lane + 16 * h;
-                        *reinterpret_cast<uint4*>(q) = qg;
-                        *reinterpret_cast<uint4*>(q + kStageBytes) = qu;
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        bulk_store_2d(&tmO0, col, row0, out.buf);
-                        bulk_store_2d(&tmO1, col, row0, out.buf + kStageBytes);
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        if (p.Z) out.bf16(&tmO0, v, col, store0, left);
+                        act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = act_f2<decltype(tag)::act>(v[j]);
+                        });
+                        if (p.res) {
+                            if (p.res_f32) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_f32(pre, j));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __fadd2_rn(v[j], raw_bf16(pre, j));
+                            }
+                            if (c + 32 < c_end) fetch(row, col + 32, end);
+                        }
+                        if (p.D) {
+                            if (p.d_f32) out.f32(&tmO1, v, col, store0, left);
+                            else out.bf16(&tmO1, v, col, store0, left);
+                        }
+                        if (p.Q) {
+                            max32(amax, v, left, keep);
+                            out.codes(&tmO2, v, qm, p.qfmt, col, store0, left);
+                        }
+                    } else {
+                        // two halves of 16 columns, each a 16-byte piece of the two boxes' rows
+                        // (32 rows x 64 codes of dg, then of du, in the maps' 64-byte swizzle:
+                        // piece j of row r at j ^ ((r >> 1) & 3)), which go out as the warp's
+                        // 64 columns are complete.  Boxes of 32 codes were twice as many
+                        // requests to the TMA unit, beside the loads (4096 -> 14336, 8192 tokens 322 ->
+                        // 307 us, 2048 tokens 86.4 -> 83.2).
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[16];
+                            __syncwarp();
+                            tmem_ld_32x32b_x16(taddr + (uint32_t)(c + 16 * h), r);
+                            tmem_ld_wait();
+                            float2 dg[8], du[8];
+                            act_dispatch(p.act, [&](auto tag) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const float2 dh = __fmul2_rn(
+                                        make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), f2(scale));
+                                    float2 f, d;
+                                    act_fd2<decltype(tag)::act>(raw_bf16(pre, j), f, d);
+                                    dg[j] = __fmul2_rn(__fmul2_rn(dh, raw_bf16(pre + 2, j)), d);
+                                    du[j] = __fmul2_rn(dh, f);
+                                }
+                            });
+                            const int cn = c + 16 * (h + 1);
+                            if (cn < c_end) fetch(row, nb * TN + cn, end);
+                            float m = 0.0f;
+                            if (left > 16 * h) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    m = max3_nan(m, fabsf(dg[j].x), fabsf(dg[j].y));
+                                    m = max3_nan(m, fabsf(du[j].x), fabsf(du[j].y));
+                                }
+                            }
+                            amax = max(amax, __float_as_uint(m) & keep);
+                            const uint4 qg = codes16(dg, qm, p.qfmt), qu = codes16(du, qm, p.qfmt);
+                            if (c == c_begin && h == 0) out.reset();        // the last tile's boxes have been read
+                            const int piece = (c - c_begin) / 16 + h;
+                            uint8_t* q = out.buf + 64 * lane + 16 * (piece ^ ((lane >> 1) & 3));
+                            *reinterpret_cast<uint4*>(q) = qg;
+                            *reinterpret_cast<uint4*>(q + 2 * kStageBytes) = qu;
+                        }
+                        if (c + 32 >= c_end || left <= 32) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                bulk_store_2d(&tmO0, nb * TN + c_begin, row0, out.buf);
+                                bulk_store_2d(&tmO1, nb * TN + c_begin, row0, out.buf + 2 * kStageBytes);
+                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                            }
+                        }
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
             }
         }
         stage_store_drain(lane);

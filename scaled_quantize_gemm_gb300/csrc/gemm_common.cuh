@@ -143,7 +143,9 @@ bool make_tmap_codes(CUtensorMap* m, void* Q, int64_t M, int64_t N, int64_t pitc
 // for the staged epilogue stores: box 32 rows x 32 bytes, no swizzle (stores
 // clip at the matrix edge)
 bool make_tmap_out(CUtensorMap* m, void* D, int64_t M, int64_t N, bool bf16, int64_t pitch = 0);
-// the same in boxes of 32 rows x 128 bytes, 128-byte swizzle
+// codes in boxes of 32 rows x 64 bytes, 64-byte swizzle
+bool make_tmap_codes64(CUtensorMap* m, void* Q, int64_t M, int64_t N, int64_t pitch);
+// an output in boxes of 32 rows x 128 bytes, 128-byte swizzle
 bool make_tmap_lines(CUtensorMap* m, void* D, int64_t M, int64_t N, bool bf16);
 // instruction descriptor, kind::f8f6f4: D fp32, A/B format, both K-major, N, M = 128
 uint32_t make_idesc(int a_fmt, int b_fmt, int n);

@@ -37,8 +37,9 @@ __device__ __forceinline__ void pdl_enter()
 // Lets the next kernel on the stream launch before this grid has ended (its
 // pdl_enter still waits for the end).  Only for grids that are resident as a
 // whole, so that no CTA of theirs waits for a place that a dependent has taken:
-// k_ffn_rows once it has issued its loads, and the LayerNorm forward, whose
-// dependents then prepare (and prefetch weights) under it.  A decoded token's
+// k_ffn_rows and the experts' k_ffn_pair once they have issued their loads, and
+// the norms' forward passes, the experts' plan and dispatch, whose dependents then
+// prepare (and prefetch weights) under them.  A decoded token's
 // three kernels (4096 -> 14336 -> 4096): 45.3 us without, 42.4 with.
 __device__ __forceinline__ void pdl_trigger()
 {

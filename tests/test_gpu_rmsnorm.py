@@ -85,6 +85,16 @@ def test_codes_with_scales(M, K, gran, kmul, mmul, fmt):
     assert torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("M,K", [(3, 32), (50, 96), (7, 16416)])
+def test_mx_rows_of_odd_numbers_of_blocks(M, K):
+    _, x, gamma = _inputs(M, K, F32, K)
+    y, q, q2 = torch.empty_like(x), torch.empty((M, K), dtype=U8, device=DEV), torch.empty((M, K), dtype=U8, device=DEV)
+    s, s2 = (torch.full((M * K // 32,), 0x33, dtype=U8, device=DEV) for _ in range(2))
+    sq.fp8_rmsnorm_fwd(x, gamma, EPS, y, q_out=q, gran=sq.MX32, scales_out=s)
+    sq.fp8_quantize(y, sq.E4M3, sq.MX32, q2, scales_out=s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
 @pytest.mark.parametrize("M,K", [(1, 256), (300, 4096), (17, 17024)])
 def test_bf16_tiles(M, K):
     g, x, gamma = _inputs(M, K, BF, 3)
