@@ -28,14 +28,15 @@ namespace fp8sq {
 namespace {
 
 // ------------------------------------------------------------------ plan
-// One cluster of CL CTAs, each warp a contiguous share of the assignments:
-// counts per warp and expert in shared memory, a sum over the warps of a CTA,
-// over the CTAs through distributed shared memory and over the experts (padded
-// to 32), after which each assignment gets its row.  The
-// lanes of a warp that hold the same expert find each other with match_any, so
-// the order within an expert is that of the assignments.  One launch for any
-// size; bound by the latency of its few passes (one GB300, under the profiler: 512
-// slots 5.0 us in one CTA, 65536 slots 8.5).
+// One cluster of up to kSortCtas CTAs, each warp a contiguous share of the
+// assignments: counts per warp and expert in shared memory, a sum over the warps of
+// a CTA, over the CTAs through distributed shared memory and over the experts (padded
+// to 32), after which each assignment gets its row.  The lanes of a warp that hold
+// the same expert find each other by one vote a bit of its number, eight rounds of 32
+// side by side, so the order within an expert is that of the assignments.  One
+// launch for any size; bound by the latency of its few steps.  One GB300, us (with
+// match_any, and found twice instead of kept): 8 slots 4.2 (3.8), 512 slots of 64 experts 5.1
+// (4.8), 65536 of 16 8.4 (8.5), 131072 of 256 19.6 (34), 262144 of 1024 42 (65).
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortBatch = 8;       // loads of ids in flight per lane
 constexpr int kSortCtas = 8;        // of the cluster, where one CTA is not enough
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
     const int64_t from = ((int64_t)rank * kSortWarps + warp) * per, to = from + per < a.n ? from + per : a.n;
     const uint32_t below = (1u << lane) - 1u;
     int32_t* mine = hist + warp * E;
+    const int bits = 32 - __clz(E - 1);                 // of an expert's number (0 for one expert)
     // A batch of ids from index i on: the expert of each (or -1) and its rank among
     // the warp's so far, whose counts go up.
     int32_t id[kSortBatch], rank_of[kSortBatch];
@@ -78,20 +80,42 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
             const int64_t at = i + 32 * b + lane;
             id[b] = at < to ? a.ids[at] : -1;
         }
+        uint32_t same[kSortBatch];
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            if ((uint32_t)id[b] >= (uint32_t)E) id[b] = -1;
+            same[b] = __ballot_sync(0xFFFFFFFFu, id[b] >= 0);           // (those without an expert need no mates)
+        }
+        for (int bit = 0; bit < bits; ++bit)
+#pragma unroll
+            for (int b = 0; b < kSortBatch; ++b) {
+                if (i + 32 * b >= to) break;
+                const bool on = (id[b] >> bit) & 1;
+                const uint32_t v = __ballot_sync(0xFFFFFFFFu, on);
+                same[b] &= on ? v : ~v;
+            }
 #pragma unroll
         for (int b = 0; b < kSortBatch; ++b) {
             if (i + 32 * b >= to) break;
-            if ((uint32_t)id[b] >= (uint32_t)E) id[b] = -1;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[b]);
             const int32_t seen = id[b] >= 0 ? mine[id[b]] : 0;
-            rank_of[b] = seen + __popc(same & below);
+            rank_of[b] = seen + __popc(same[b] & below);
             __syncwarp();
-            if (id[b] >= 0 && (same & below) == 0) mine[id[b]] = seen + __popc(same);
+            if (id[b] >= 0 && (same[b] & below) == 0) mine[id[b]] = seen + __popc(same[b]);
             __syncwarp();
         }
     };
     __syncwarp();
-    for (int64_t i = from; i < to; i += 32 * kSortBatch) batch(i);
+    // a warp's only batch stays in registers; of several the ranks wait in row_of
+    int32_t* row_of = a.plan + a.row_of_at;
+    const bool several = per > 32 * kSortBatch;
+    for (int64_t i = from; i < to; i += 32 * kSortBatch) {
+        batch(i);
+        if (several) {
+#pragma unroll
+            for (int b = 0; b < kSortBatch; ++b)
+                if (i + 32 * b + lane < to) row_of[i + 32 * b + lane] = rank_of[b];
+        }
+    }
     __syncthreads();
     for (int e = t; e < E; e += kSortThreads) {
         int32_t run = 0;
@@ -164,17 +188,21 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_expert_plan(SortArgs a, int
     }
     if (ctas > 1) cluster_sync_all();                   // the totals have been read: a CTA may end
     else __syncthreads();
-    // the rows: the only batch's ranks are at hand, more are found once more
-    // (counting on from the warps before)
-    int32_t* row_of = a.plan + a.row_of_at;
-    const bool again = per > 32 * kSortBatch;
     for (int64_t i = from; i < to; i += 32 * kSortBatch) {
-        if (again) batch(i);
+        if (several) {
+#pragma unroll
+            for (int b = 0; b < kSortBatch; ++b) {
+                const int64_t at = i + 32 * b + lane;
+                if (at >= to) continue;
+                id[b] = a.ids[at];
+                if ((uint32_t)id[b] >= (uint32_t)E) id[b] = -1;
+                rank_of[b] = row_of[at];
+            }
+        }
 #pragma unroll
         for (int b = 0; b < kSortBatch; ++b) {
             const int64_t at = i + 32 * b + lane;
-            const int32_t e = id[b];
-            if (at < to) row_of[at] = e >= 0 ? base[e] + rank_of[b] + (again ? 0 : mine[e]) : -1;
+            if (at < to) row_of[at] = id[b] >= 0 ? base[id[b]] + mine[id[b]] + rank_of[b] : -1;
         }
     }
     // row tiles of the products, in groups of neighbours of one expert, and blocks
@@ -249,10 +277,12 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __res
 
 // ------------------------------------------------------------------ combine
 // CTAs of a column (blockIdx.y: a chunk of kMoveThreads vectors) take the tokens in
-// turn, up to eight rows' loads in flight a thread; fp32 sums in the order of the
-// slots, the residual last.  y may be the residual itself.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* __restrict__ rows, const int32_t* __restrict__ row_of,
+// turn, FLY rows' loads in flight a thread; fp32 sums in the order of the slots, in
+// packed instructions, the residual last.  y may be the residual itself.  (8192
+// tokens of 4 rows of 4096 bf16 with residual, 59.5 us at the copy rate: 59.6; one element at a
+// time and eight rows' registers for any k 75.)
+template <typename T, int VEC, int FLY>
+__global__ void __launch_bounds__(kMoveThreads, FLY <= 4 ? 6 : 4) k_expert_combine(const T* __restrict__ rows, const int32_t* __restrict__ row_of,
                                                                  const float* __restrict__ w, const T* res, int64_t nt,
                                                                  int k, int64_t K, int64_t R, T* y)
 {
@@ -262,10 +292,10 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* __rest
     const int64_t c = ((int64_t)blockIdx.y * kMoveThreads + threadIdx.x) * VEC;
     if (c >= K) return;
     for (int64_t t = blockIdx.x; t < nt; t += gridDim.x) {
-        float acc[VEC] = {};
+        constexpr int PAIRS = (VEC + 1) / 2;
+        float2 acc[PAIRS] = {};
         Raw rr{};
         if (res) rr = *reinterpret_cast<const Raw*>(res + t * K + c);
-        constexpr int FLY = 8;
         for (int j0 = 0; j0 < k; j0 += FLY) {
             Raw raw[FLY];
             float wj[FLY];
@@ -282,19 +312,20 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_combine(const T* __rest
             }
 #pragma unroll
             for (int j = 0; j < FLY; ++j) {
-                float v[VEC];
-                P::to_floats(raw[j], v);
+                float v[2 * PAIRS] = {};
+                P::to_floats(raw[j], reinterpret_cast<float(&)[VEC]>(v));
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) acc[i] = fmaf(wj[j], v[i], acc[i]);
+                for (int i = 0; i < PAIRS; ++i) acc[i] = __ffma2_rn(f2(wj[j]), make_float2(v[2 * i], v[2 * i + 1]), acc[i]);
             }
         }
-        if (res) {
-            float v[VEC];
-            P::to_floats(rr, v);
+        float out[VEC], v[2 * PAIRS] = {};
+        if (res) P::to_floats(rr, reinterpret_cast<float(&)[VEC]>(v));
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[i] += v[i];
+        for (int i = 0; i < VEC; ++i) {
+            out[i] = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+            if (res) out[i] += v[i];
         }
-        *reinterpret_cast<Raw*>(y + t * K + c) = P::from_floats(acc);
+        *reinterpret_cast<Raw*>(y + t * K + c) = P::from_floats(out);
     }
 }
 
@@ -416,16 +447,21 @@ cudaError_t with_vector(int64_t row_bytes, F&& f)
     return f(uint8_t{});
 }
 
-template <typename T, int VEC>
-cudaError_t combine(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+template <typename T, int VEC, int FLY>
+cudaError_t combine_slots(const ExpertRowsArgs& a, cudaStream_t st, int sms)
 {
-    auto kern = k_expert_combine<T, VEC>;
+    auto kern = k_expert_combine<T, VEC, FLY>;
     const int64_t chunks = cdiv(a.K, kMoveThreads * VEC);
     const int64_t cap = cdiv(resident(reinterpret_cast<const void*>(kern), kMoveThreads, 0, sms), chunks);
     launch_k(kern, dim3((unsigned)(a.T < cap ? a.T : cap), (unsigned)chunks), kMoveThreads, 0, st,
              static_cast<const T*>(a.rows), a.plan + a.layout.row_of_at, a.weights, static_cast<const T*>(a.residual), a.T,
              a.k, a.K, a.layout.rows, static_cast<T*>(a.y));
     return cudaGetLastError();
+}
+template <typename T, int VEC>
+cudaError_t combine(const ExpertRowsArgs& a, cudaStream_t st, int sms)
+{
+    return a.k <= 4 ? combine_slots<T, VEC, 4>(a, st, sms) : combine_slots<T, VEC, 8>(a, st, sms);
 }
 template <typename T, int VEC, int JB>
 cudaError_t combine_bwd_slots(const ExpertRowsArgs& a, cudaStream_t st, int sms)
