@@ -53,8 +53,8 @@ static cudaError_t expert_pairs(int smem, int* pairs)
     return cudaSuccess;
 }
 
-template <int KIND, int GROUP>
-static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cudaStream_t st, const char** why)
+template <int KIND, int GROUP, bool PAIR = true>
+static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cudaStream_t st, int sms, const char** why)
 {
     constexpr bool GLU = KIND == kEpiGlu;
     const int64_t R = a.layout.rows;
@@ -67,23 +67,29 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
-    constexpr int smem = FfnSmem<KIND, GROUP>::BYTES;
-    int pairs = 0;
-    const cudaError_t e = expert_pairs<KIND, GROUP>(smem, &pairs);
-    if (e != cudaSuccess) {
-        *why = "cluster occupancy query failed";
-        return e;
-    }
-    if (pairs < 1) {
-        *why = "no CTA pair of this kernel fits on the device";
-        return cudaErrorNotSupported;
+    constexpr int smem = FfnSmem<KIND, GROUP, PAIR>::BYTES;
+    auto kern = k_ffn_pair<KIND, GROUP, PAIR>;
+    int groups = sms;                        // CTA pairs, or CTAs
+    if constexpr (PAIR) {
+        const cudaError_t e = expert_pairs<KIND, GROUP>(smem, &groups);
+        if (e != cudaSuccess) {
+            *why = "cluster occupancy query failed";
+            return e;
+        }
+        if (groups < 1) {
+            *why = "no CTA pair of this kernel fits on the device";
+            return cudaErrorNotSupported;
+        }
+    } else {
+        const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(kern), smem);
+        if (e != cudaSuccess) return e;
     }
     // the tiles in use are known on the device alone: at most this many
     constexpr int tile_n = GLU ? kFfnBH : kFfnBN;
     TileSched sched{(int)((a.M + 2 * BM - 1) / (2 * BM)), (int)((a.N + tile_n - 1) / tile_n), 8};
-    const int64_t most = (GROUP == kWgrad ? (int64_t)a.E * sched.num_m : a.layout.max_tiles) * sched.num_n;
+    const int64_t most = (GROUP == kWgrad ? (int64_t)a.E * sched.num_m : (PAIR ? 1 : 2) * a.layout.max_tiles) * sched.num_n;
     uint32_t idesc = make_idesc(a.a_format, a.b_format, kFfnBN);
-    idesc = (idesc & ~(0x1Fu << 24)) | ((uint32_t)((2 * BM) >> 4) << 24);   // M = 256 over the pair
+    if (PAIR) idesc = (idesc & ~(0x1Fu << 24)) | ((uint32_t)((2 * BM) >> 4) << 24);   // M = 256 over the pair
     if (GROUP == kWgrad) idesc |= 1u << 15;                                  // A MN-major
     if (GROUP >= kRowsMn) idesc |= 1u << 16;                                 // B MN-major
     // outputs stored in bulk; a map that the epilogue does not use is a copy of A's
@@ -101,35 +107,45 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
         *why = "cuTensorMapEncodeTiled failed (output)";
         return cudaErrorInvalidValue;
     }
-    auto kern = k_ffn_pair<KIND, GROUP>;
-    launch_k(kern, (unsigned)(2 * (most < pairs ? most : pairs)), kFfnThreads<KIND>, (size_t)smem, st, ta, tb, p, idesc,
+    launch_k(kern, (unsigned)((PAIR ? 2 : 1) * (most < groups ? most : groups)), kFfnThreads<KIND>, (size_t)smem, st, ta, tb, p, idesc,
              sched, o[0], o[1], o[2]);
     return cudaGetLastError();
 }
 
-// ------------------------------------------------------------------ few rows
-// Whether k_ffn_rows takes a product with N weight rows an expert (glu: 2F).  The
-// routing is known on the device alone, so the rule goes by its sizes: n = T k
-// assignments make a = n / min(E, n) rows an expert.  The tiles of 256 rows read
-// each weight once whatever the rows, and store whole lines; the few-rows kernel
-// shares the weights' bytes out evenly and starts sooner, which tells where K is long
-// or the tiles do not go round, but it reads a weight tile again (from L2) for every
-// 32 rows of an expert.  One GB300, us, few rows / tiles (the weights at the copy
-// rate).  Gated: 8 of 64 experts, 4096 -> 2 x 1792, 1 token 25.9 / 29.7 (17.4), 16 tokens
-// 97.0 / 103.5, a = 8 137.5 / 139.4, 12 145.5 / 140.9, 32 201 / 151; 4 of 32, 2304 -> 2 x
-// 1040, 1 token 10.4 / 12.4, a = 8 30.1 / 32.4, 12 31.6 / 32.8; 6 of 96, 1024 -> 2 x 512, 1
-// token 7.4 / 8.9, 8 tokens 12.5 / 12.4, a = 8 23.0 / 21.5.  Plain: 3584 -> 4096, 2 of 16,
-// 8 tokens 28.1 / 31.3, a = 8 43.2 / 46.5; 1792 -> 4096, 8 of 64, 1 token 17.1 / 16.5, a = 8
-// 74.9 / 73.8; 1040 -> 2304, 4 of 32, 1 token 8.3 / 8.4, 16 tokens 18.3 / 14.9; 512 -> 1024, 6 of
-// 96, 1 token 6.8 / 7.3, 16 tokens 13.0 / 10.4.
+// ------------------------------------------------------------------ which kernel
+// The routing is known on the device alone, so the rules go by its sizes: n = T k
+// assignments make a = n / active rows for each of active = min(E, n) experts.
+//
+// One CTA a tile of 128 rows up to a = 40, CTA pairs and 256 rows from there on.
+// One GB300, us, one CTA / pairs (the weights at the copy rate): 8 of 64 experts, 4096 ->
+// 2 x 1792, a = 4 123 / 128 (117), 16 144 / 151 (132), 32 157 / 154, 64 184 / 161; 1792 ->
+// 4096, 1 token 14.5 / 16.2 (8.7), a = 16 77.3 / 77.9, 64 96.8 / 85.3; 4 of 32, 2304 -> 2 x 1040,
+// a = 4 27.5 / 34.6 (19.1), 32 32.1 / 33.3, 64 37.2 / 34.1; 1040 -> 2304, a = 8 15.0 / 17.6
+// (10.3), 32 17.2 / 19.9; 2 of 8, 2048 -> 4096, a = 8 11.3 / 15.6 (9.9), 96 18.2 / 17.8; 2 of
+// 16, 4096 -> 2 x 3584, a = 16 77.2 / 80.6 (65), 64 89.8 / 81.9.
+static bool expert_single_ctas(int64_t T, int k, int E)
+{
+    const int64_t n = T * k, active = E < n ? E : n;
+    return n <= 40 * active;
+}
+// k_ffn_rows where those tiles do not go round, or where single tokens stream long
+// gated weights: it shares the bytes out evenly, but reads a weight tile again (from
+// L2) for every 32 rows of an expert, and stores column by column.  N: weight rows of
+// an expert (glu: 2F).  Few rows / one CTA a tile: 4096 -> 2 x 1792, 8 of 64, 1 token 25.9 /
+// 26.0, 4 tokens 58.6 / 62.0, a = 4 125 / 123; 4096 -> 2 x 3584, 2 of 16, 1 token (56 tiles) 16.1
+// / 19.0, 4 tokens 35.7 / 41.6, a = 4 68.3 / 70.4, 8 75.5 / 74.9; 2304 -> 2 x 1040, 4 of 32, 1
+// token (36 tiles) 10.4 / 12.0, 4 tokens 17.1 / 14.5; plain, 3584 -> 4096, 1 token (32 tiles)
+// 13.2 / 15.2, 4 tokens 21.6 / 19.3; 1792 -> 4096, 1 token (128 tiles) 17.2 / 14.5; 512 ->
+// 1024, 6 of 96, 1 token 6.8 / 5.7.
 constexpr int kExpertNT = 32;
 static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool glu, int sms)
 {
     const ExpertLayout l = expert_layout(T, k, E);
     const int64_t wtiles = (N + BM - 1) / BM, nkb = (K + BK - 1) / BK, most = l.rows / kExpertNT * wtiles;
     if (most > kRowsMaxTiles || most * nkb >= ((int64_t)1 << 31) || sms > kRowsMaxCtas) return false;
-    const int64_t n = T * k, active = E < n ? E : n, tiles = active * wtiles;
-    return n <= 10 * active && (nkb > 16 || tiles <= (glu ? 2 * sms : sms / 2));
+    const int64_t n = T * k, active = E < n ? E : n, tiles = active * ((N + kFfnBN - 1) / kFfnBN);
+    if (!expert_single_ctas(T, k, E) || nkb < 8) return false;
+    return tiles <= 64 || (glu && nkb > 20 && n <= 3 * active);
 }
 
 size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K)
@@ -197,11 +213,15 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int sms
     if ((a.kind == kExpertGlu || (a.kind == kExpertGemm && !a.b_mn)) &&
         expert_few_rows(a.T, a.k, a.E, a.kind == kExpertGlu ? 2 * a.N : a.N, a.K, a.kind == kExpertGlu, sms))
         return a.kind == kExpertGlu ? launch_few_rows<kEpiGlu>(a, p, st, sms, why) : launch_few_rows<kEpiAct>(a, p, st, sms, why);
+    const bool single = expert_single_ctas(a.T, a.k, a.E);
     switch (a.kind) {
-    case kExpertGlu: return launch_pair<kEpiGlu, kRows>(a, p, st, why);
-    case kExpertGluBwd: return launch_pair<kEpiGluBwd, kRowsMn>(a, p, st, why);
-    case kExpertWgrad: return launch_pair<kEpiAct, kWgrad>(a, p, st, why);
-    default: return a.b_mn ? launch_pair<kEpiAct, kRowsMn>(a, p, st, why) : launch_pair<kEpiAct, kRows>(a, p, st, why);
+    case kExpertGlu:
+        return single ? launch_pair<kEpiGlu, kRows, false>(a, p, st, sms, why) : launch_pair<kEpiGlu, kRows>(a, p, st, sms, why);
+    case kExpertGluBwd: return launch_pair<kEpiGluBwd, kRowsMn>(a, p, st, sms, why);
+    case kExpertWgrad: return launch_pair<kEpiAct, kWgrad>(a, p, st, sms, why);
+    default:
+        if (a.b_mn) return launch_pair<kEpiAct, kRowsMn>(a, p, st, sms, why);
+        return single ? launch_pair<kEpiAct, kRows, false>(a, p, st, sms, why) : launch_pair<kEpiAct, kRows>(a, p, st, sms, why);
     }
 }
 

@@ -69,9 +69,9 @@ constexpr int kFfnBN = 256, kFfnBH = 128;
 // Staging boxes of 1 KB, shared out among the epilogue warps.
 template <int KIND>
 constexpr int kFfnBoxes = KIND == kEpiGluBwd ? 64 : 32;
-template <int KIND, int GROUP = 0>
-struct FfnSmem : Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, kFfnBoxes<KIND>> {
-    using Base = Smem<kFfnBH, kFfnStages<KIND, GROUP>, 2, kFfnBoxes<KIND>>;
+template <int KIND, int GROUP = 0, bool PAIR = true>
+struct FfnSmem : Smem<PAIR ? kFfnBH : kFfnBN, PAIR ? kFfnStages<KIND, GROUP> : 4, 2, kFfnBoxes<KIND>> {
+    using Base = Smem<PAIR ? kFfnBH : kFfnBN, PAIR ? kFfnStages<KIND, GROUP> : 4, 2, kFfnBoxes<KIND>>;
     // (swizzled staging wants its areas on 1 KB boundaries: stage_lines, the codes of glu_bwd)
     static constexpr int STG_OFF = KIND == kEpiGluBwd || (KIND == kEpiAct && GROUP != 0) ? Base::BAR_OFF + 1024 : Base::STG_OFF;
     static constexpr int BYTES = STG_OFF + Base::BYTES - Base::STG_OFF;
@@ -313,17 +313,25 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 struct PairTile {
     int row0, end, nb, expert, k0, nkb, last;
 };
-template <int GROUP>
+template <int GROUP, bool PAIR>
 __device__ __forceinline__ int pair_tiles(const FfnParams& p, const TileSched& sched)
 {
     if constexpr (GROUP == kNoGroups) return sched.num_m * sched.num_n;
     else if constexpr (GROUP == kWgrad) return p.E * sched.num_m * sched.num_n;
-    else return min(__ldg(p.ntiles), p.max_tiles) * sched.num_n;
+    else return (PAIR ? 1 : 2) * min(__ldg(p.ntiles), p.max_tiles) * sched.num_n;
 }
-template <int GROUP>
+// (One CTA a tile: the plan's tiles in halves of 128 rows, all first halves before
+// all second ones, of which those past their expert's rows have no K blocks.)
+template <int GROUP, bool PAIR>
 __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSched& sched, int t)
 {
     PairTile x;
+    [[maybe_unused]] int half = 0;
+    if constexpr (!PAIR) {
+        const int n = min(__ldg(p.ntiles), p.max_tiles) * sched.num_n;
+        half = t >= n ? 1 : 0;
+        t -= half * n;
+    }
     if constexpr (GROUP == kWgrad) {
         const int per = sched.num_m * sched.num_n;
         int mb;
@@ -342,10 +350,10 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
         const int r = t - d.x * sched.num_n, size = max(d.y & 0xFF, 1);
         x.nb = r / size;
         x.expert = min(d.y >> 8, p.E - 1);
-        x.row0 = max(d.z + (r - x.nb * size) * 2 * BM, 0);
+        x.row0 = max(d.z + (r - x.nb * size) * 2 * BM + half * BM, 0);
         x.end = min(d.w, p.M);
         x.k0 = 0;
-        x.nkb = (p.K + BK - 1) / BK;
+        x.nkb = PAIR || x.row0 < x.end ? (p.K + BK - 1) / BK : 0;
         x.last = (p.K - (x.nkb - 1) * BK + 31) / 32;
     } else {
         int mb;
@@ -371,16 +379,21 @@ __device__ __forceinline__ int pair_rows(const PairTile& x, int rank)
     else return BM;
 }
 
-template <int KIND, int GROUP = kNoGroups>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1)
+// PAIR false (experts' rows): the same on one CTA a tile of 128 x 256 with MMAs of its
+// own (M = 128), for experts of few rows: with 128 rows or less a pair's second CTA
+// multiplies nothing but padding, and 256 rows of it take as long as the weights'
+// bytes (experts.cu has both sides measured).
+template <int KIND, int GROUP = kNoGroups, bool PAIR = true>
+__global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1)
     k_ffn_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FfnParams p,
                uint32_t idesc, TileSched sched, const __grid_constant__ CUtensorMap tmO0,
                const __grid_constant__ CUtensorMap tmO1, const __grid_constant__ CUtensorMap tmO2)
 {
-    constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = kFfnStages<KIND, GROUP>;
+    static_assert(PAIR || (GROUP == kRows && KIND != kEpiGluBwd), "one CTA a tile: experts' rows, weights K-major");
+    constexpr int BN = kFfnBN, BH = kFfnBH, STAGES = PAIR ? kFfnStages<KIND, GROUP> : 4;
     constexpr bool b_mn = KIND == kEpiGluBwd || GROUP >= kRowsMn;          // (glu_bwd: Wd [K][F])
     constexpr bool a_mn = GROUP == kWgrad;
-    using L = FfnSmem<KIND, GROUP>;
+    using L = FfnSmem<KIND, GROUP, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
@@ -405,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&afull[b], 1);
-            mbar_init(&aempty[b], 2 * kFfnEpiWarps<KIND>);
+            mbar_init(&aempty[b], (PAIR ? 2 : 1) * kFfnEpiWarps<KIND>);
         }
         mbar_init(drain, 1);
         fence_mbar_init();
@@ -413,21 +426,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         prefetch_tmap(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc_pair(holder, TMEM_COLS);
-        tmem_relinquish_pair();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(holder, TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(holder, TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     pdl_enter();
     if (threadIdx.x == 0) s_skip = rank == 0 ? *reinterpret_cast<volatile int*>(p.err) : 0;
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();                        // both CTAs' barriers initialised, the leader's flag written
+    if constexpr (PAIR) cluster_sync_all();    // both CTAs' barriers initialised, the leader's flag written
     tc_fence_after();
     int skip = s_skip;
     if (rank != 0) skip = (int)ld_shared_cluster_u32(cluster_map(smem_addr(&s_skip), 0));
     const uint32_t tmem_base = *holder;
 
-    const int num_tiles = pair_tiles<GROUP>(p, sched);
-    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const int num_tiles = pair_tiles<GROUP, PAIR>(p, sched);
+    const int cid = PAIR ? blockIdx.x >> 1 : blockIdx.x, ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err_cluster(bar, parity, p.err); };
 
     if (skip) {
@@ -439,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             uint32_t phase = 0;
             bool aborted = false;
             for (int t = cid; t < num_tiles && !aborted; t += ncl) {
-                const PairTile x = pair_tile<GROUP>(p, sched, t);
+                const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
                 const int ar = x.row0 + (int)rank * BM;
                 // glu_fwd: gate rows in the even CTA, the up rows of the same
                 // features in the odd one
@@ -447,7 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                 if constexpr (GROUP == kRows) br += x.expert * (KIND == kEpiGlu ? 2 * p.N : p.N);
                 const int bk = GROUP == kRowsMn ? x.expert * p.K : x.k0;
                 const int rows = pair_rows<GROUP>(x, (int)rank);
-                const uint32_t tx = 2u * (uint32_t)L::B_BYTES + (uint32_t)(BK * (pair_rows<GROUP>(x, 0) + pair_rows<GROUP>(x, 1)));
+                const uint32_t tx = (uint32_t)((PAIR ? 2 : 1) * L::B_BYTES) +
+                                    (uint32_t)(BK * (pair_rows<GROUP>(x, 0) + (PAIR ? pair_rows<GROUP>(x, 1) : 0)));
                 for (int kb = 0; kb < x.nkb; ++kb) {
                     if (!wait(&empty[stage], phase ^ 1u)) {
                         aborted = true;
@@ -456,13 +475,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                     uint8_t* sa = smem + stage * L::STAGE;
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], tx);
                     const int ka = x.k0 + kb * BK, kr = bk + kb * BK;
-                    if (rows == BM) {
-                        tma_load_2d_pair(sa, &tmA, a_mn ? ar : ka, a_mn ? ka : ar, full0 + 8u * stage);
+                    if constexpr (PAIR) {
+                        if (rows == BM) {
+                            tma_load_2d_pair(sa, &tmA, a_mn ? ar : ka, a_mn ? ka : ar, full0 + 8u * stage);
+                        } else {
+                            for (int i = 0; i < rows; i += 32)         // (experts: tmO2 is A in boxes of 32 rows)
+                                tma_load_2d_pair(sa + i * BK, &tmO2, ka, ar + i, full0 + 8u * stage);
+                        }
+                        tma_load_2d_pair(sa + A_BYTES, &tmB, b_mn ? br : kr, b_mn ? kr : br, full0 + 8u * stage);
                     } else {
-                        for (int i = 0; i < rows; i += 32)             // (experts: tmO2 is A in boxes of 32 rows)
-                            tma_load_2d_pair(sa + i * BK, &tmO2, ka, ar + i, full0 + 8u * stage);
+                        if (rows == BM) tma_load_2d(sa, &tmA, ka, ar, &full[stage]);
+                        else
+                            for (int i = 0; i < rows; i += 32) tma_load_2d(sa + i * BK, &tmO2, ka, ar + i, &full[stage]);
+                        // gate rows, then up rows; or 256 rows
+                        tma_load_2d(sa + A_BYTES, &tmB, kr, br, &full[stage]);
+                        tma_load_2d(sa + A_BYTES + BH * BK, &tmB, kr, br + (KIND == kEpiGlu ? p.N : BH), &full[stage]);
                     }
-                    tma_load_2d_pair(sa + A_BYTES, &tmB, b_mn ? br : kr, b_mn ? kr : br, full0 + 8u * stage);
                     ++issued;
                     if (++stage == STAGES) {
                         stage = 0;
@@ -473,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
             // (experts: the next product's CTAs start as this grid's leave their SMs; 4 of
             // 32 experts, 2304 -> 1040 and back, 192 tokens 56.5 -> 55.3 us)
             if (GROUP != kNoGroups) pdl_trigger();
-            if (__builtin_expect(aborted, 0)) pair_stop(s_stop, rank, issued);
+            if (PAIR && __builtin_expect(aborted, 0)) pair_stop(s_stop, rank, issued);
             bool released = !aborted;
             for (int i = 0; i < STAGES && released; ++i) {     // every stage's last release has landed
                 released = wait(&empty[stage], phase ^ 1u);
@@ -487,12 +515,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
+            auto commit = [](uint64_t* bar) {
+                if constexpr (PAIR) mma_pair_commit(bar, 3);
+                else mma_commit(bar);
+            };
             int stage = 0, lt = 0;
             uint32_t phase = 0;
             bool aborted = false;
             for (int t = cid; t < num_tiles && !aborted; t += ncl) {
-                const PairTile x = pair_tile<GROUP>(p, sched, t);
-                if (GROUP == kWgrad && x.nkb == 0) continue;          // an expert without rows: zeros, no product
+                const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
+                if ((GROUP == kWgrad || !PAIR) && x.nkb == 0) continue;          // an expert without rows: zeros, no product
                 const int b = lt & 1;
                 const uint32_t u = (uint32_t)(lt >> 1);
                 ++lt;
@@ -516,15 +548,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                     const int steps = GROUP != kNoGroups && kb + 1 == x.nkb ? x.last : BK / 32;
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
-                        if (GROUP == kNoGroups || k < steps)
-                            mma_pair_f8f6f4(d, da + sta * k, db + stb * k, idesc, (kb | k) != 0 ? 1u : 0u);
-                    mma_pair_commit(&empty[stage], 3);
+                        if (GROUP == kNoGroups || k < steps) {
+                            if constexpr (PAIR) mma_pair_f8f6f4(d, da + sta * k, db + stb * k, idesc, (kb | k) != 0 ? 1u : 0u);
+                            else mma_f8f6f4(d, da + sta * k, db + stb * k, idesc, (kb | k) != 0 ? 1u : 0u);
+                        }
+                    commit(&empty[stage]);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (!aborted) mma_pair_commit(&afull[b], 3);
+                if (!aborted) commit(&afull[b]);
             }
             bool released = !aborted;
             for (int j = 0; j < 2 && released; ++j) {       // both accumulators' last releases have landed
@@ -532,7 +566,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                 released = wait(&aempty[l2 & 1], ((uint32_t)(l2 >> 1) & 1u) ^ 1u);
             }
             if (__builtin_expect(!released, 0)) {
-                mma_pair_commit(drain, 1);                  // completes once every issued MMA is done
+                if constexpr (PAIR) mma_pair_commit(drain, 1);          // completes once every issued MMA is done
+                else mma_commit(drain);
                 wait_drain(drain, 0);
             }
         }
@@ -543,7 +578,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         float scale = __ldg(p.sA) * __ldg(p.sB);
         const float qm = p.Q ? p.qstate[p.qH] : 1.0f;
         uint32_t amax = 0;
-        const uint32_t aempty0 = cluster_map(smem_addr(aempty), 0);
+        const uint32_t aempty0 = PAIR ? cluster_map(smem_addr(aempty), 0) : 0u;
+        auto hand_back = [&](int b) {
+            if constexpr (PAIR) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+            else mbar_arrive(&aempty[b]);
+        };
         Stager out{smem + L::STG_OFF + (warp - 2) * BOXES * kStageBytes, lane, 0};
         // columns of a tile in this warp's share; what its epilogue reads
         // beside the sums (the residual, or g and u) is fetched one chunk of
@@ -567,7 +606,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         };
         int lt = 0;
         for (int t = cid; t < num_tiles; t += ncl) {
-            const PairTile x = pair_tile<GROUP>(p, sched, t);
+            const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
+            if (!PAIR && x.nkb == 0) continue;
             const bool some = GROUP != kWgrad || x.nkb > 0;          // (else zeros)
             const int b = lt & 1;
             const uint32_t u = (uint32_t)(lt >> 1);
@@ -609,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                     if (h == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (some && lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+                        if (some && lane == 0) hand_back(b);
                     }
                     const int col = nb * TN + c_begin + HALF * h;
                     if (row0 < end && col < p.N) {
@@ -753,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(aempty0 + 8u * b);
+                if (lane == 0) hand_back(b);
             }
         }
         stage_store_drain(lane);
@@ -763,15 +803,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
         }
     }
     __syncthreads();
-    cluster_sync_all();
-    if (__builtin_expect(s_stop[0] >= 0, 0)) {                      // (the same in both CTAs)
+    if constexpr (PAIR) cluster_sync_all();
+    if (PAIR && __builtin_expect(s_stop[0] >= 0, 0)) {                      // (the same in both CTAs)
         // what the odd CTA had loaded for stages that the leader never issued is
         // expected now, and waited for (with a limit)
         if (rank == 0 && threadIdx.x == 0) {
             auto odd = [&](auto&& f) {
                 int i = 0;
                 for (int t = cid; t < num_tiles; t += ncl) {
-                    const PairTile x = pair_tile<GROUP>(p, sched, t);
+                    const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
                     for (int kb = 0; kb < x.nkb; ++kb, ++i) {
                         if (s_stop[1] >= 0 && i >= s_stop[1]) return;
                         if (i >= s_stop[0]) f(i, (uint32_t)(L::B_BYTES + BK * pair_rows<GROUP>(x, 1)));
@@ -786,7 +826,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads<KIND>, 1
     // nothing is pending into either CTA any more
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 

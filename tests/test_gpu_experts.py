@@ -49,7 +49,8 @@ class Case:
 # T, k, E, routing, hidden, inner
 CASES = [(1, 1, 1, "spread", 32, 16), (1, 8, 64, "spread", 1024, 272), (7, 2, 3, "masked", 160, 144), (37, 3, 5, "skewed", 544, 80),
          (300, 1, 2, "one", 96, 528), (333, 4, 7, "masked", 256, 320), (1000, 2, 16, "last", 64, 256),
-         (5000, 1, 2, "skewed", 32, 48), (5, 2, 4, "none", 64, 32), (64, 8, 24, "spread", 4096, 512), (40, 4, 40, "skewed", 2304, 144), (1200, 2, 3, "spread", 2080, 1040)]
+         (5000, 1, 2, "skewed", 32, 48), (5, 2, 4, "none", 64, 32), (64, 8, 24, "spread", 4096, 512), (40, 4, 40, "skewed", 2304, 144),
+         (200, 4, 40, "skewed", 160, 96), (3, 2, 6, "spread", 2720, 4112), (1200, 2, 3, "spread", 2080, 1040)]
 
 
 @pytest.mark.parametrize("T,k,E,how,d,F", CASES)

@@ -114,8 +114,8 @@ def test_weight_gradients_beyond_31_bits():
         assert_within(D[e][-300:], z, ez, f"expert {e}")
 
 
-# the few-rows kernel with K split, tiles of 256 rows, the weights MN-major, weight gradients
-@pytest.mark.parametrize("how,T,k,E,N,K", [("few", 4, 4, 24, 2064, 4096), ("tiles", 2000, 2, 5, 1040, 1056), ("mn", 2000, 2, 5, 1040, 1056),
+# the few-rows kernel with K split, one CTA a tile, tiles of 256 rows, the weights MN-major, weight gradients
+@pytest.mark.parametrize("how,T,k,E,N,K", [("few", 4, 1, 4, 2064, 4096), ("single", 30, 4, 24, 2064, 4096), ("tiles", 2000, 2, 5, 1040, 1056), ("mn", 2000, 2, 5, 1040, 1056),
                                           ("wgrad", 2000, 2, 5, 1040, 1056)])
 def test_a_word_set_while_products_start(how, T, k, E, N, K):
     c = Case(T, k, E, "spread", seed=T)
