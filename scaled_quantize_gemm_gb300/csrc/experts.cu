@@ -114,38 +114,50 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
 
 // ------------------------------------------------------------------ which kernel
 // The routing is known on the device alone, so the rules go by its sizes: n = T k
-// assignments make a = n / active rows for each of active = min(E, n) experts.
+// assignments make a = n / active rows for each of active = min(E, n) experts, and
+// `tiles` of 256 weight rows (glu: 128 of the gate and of the up projection).
+// Figures: one GB300, us, weights from DRAM (in brackets their bytes at the copy rate).
 //
-// One CTA a tile of 128 rows up to a = 40, CTA pairs and 256 rows from there on.
-// One GB300, us, one CTA / pairs (the weights at the copy rate): 8 of 64 experts, 4096 ->
-// 2 x 1792, a = 4 123 / 128 (117), 16 144 / 151 (132), 32 157 / 154, 64 184 / 161; 1792 ->
-// 4096, 1 token 14.5 / 16.2 (8.7), a = 16 77.3 / 77.9, 64 96.8 / 85.3; 4 of 32, 2304 -> 2 x 1040,
-// a = 4 27.5 / 34.6 (19.1), 32 32.1 / 33.3, 64 37.2 / 34.1; 1040 -> 2304, a = 8 15.0 / 17.6
-// (10.3), 32 17.2 / 19.9; 2 of 8, 2048 -> 4096, a = 8 11.3 / 15.6 (9.9), 96 18.2 / 17.8; 2 of
-// 16, 4096 -> 2 x 3584, a = 16 77.2 / 80.6 (65), 64 89.8 / 81.9.
-static bool expert_single_ctas(int64_t T, int k, int E)
+// One CTA a tile of 128 rows up to a = 20, up to 40 where an SM gets three tiles at
+// most; from there on CTA pairs and 256 rows, whose operands cost less traffic.
+// One CTA / pairs: 4096 -> 2 x 1792, 8 of 64 (896 tiles), 1 token 26.6 / 30.4 (17.4),
+// a = 4 122 / 128 (111), 16 146 / 153 (133), 32 162 / 156, 64 193 / 166; 2304 -> 2 x 1040, 4
+// of 32 (288 tiles), a = 4 28.4 / 30.4 (18.6), 16 31.0 / 33.1, 32 31.6 / 33.5, 48 37.5 / 33.7;
+// 4096 -> 2 x 3584, 2 of 16 (448), a = 16 79.5 / 82.3 (69.4), 32 79.9 / 82.6, 64 92.0 / 84.0;
+// 2048 -> 2 x 768, 8 of 128 (768), a = 8 63.9 / 65.0 (52.8), 16 69.1 / 68.4, 32 77.2 / 70.0;
+// 1024 -> 2 x 512, 6 of 96 (384), a = 4 20.6 / 21.1 (11.7), 32 25.5 / 24.2; plain, 3584 -> 4096, 2
+// of 16 (256), a = 8 42.3 / 48.1 (33.6), 32 44.3 / 49.3, 64 54.3 / 49.7; 2048 -> 4096, 2 of 8
+// (128), a = 8 15.9 / 18.0 (9.5).
+struct ExpertSizes {
+    int64_t n, active, tiles;
+    ExpertSizes(int64_t T, int k, int E, int64_t N)
+        : n(T * k), active(E < n ? E : n), tiles(active * ((N + kFfnBN - 1) / kFfnBN))
+    {
+    }
+};
+static bool expert_single_ctas(const ExpertSizes& s, int sms)
 {
-    const int64_t n = T * k, active = E < n ? E : n;
-    return n <= 40 * active;
+    return s.n <= (s.tiles <= 3 * sms ? 40 : 20) * s.active;
 }
 // k_ffn_rows where those tiles do not go round, or where single tokens stream long
-// gated weights: it shares the bytes out evenly, but reads a weight tile again (from
-// L2) for every 32 rows of an expert, and stores column by column.  N: weight rows of
-// an expert (glu: 2F).  Few rows / one CTA a tile: 4096 -> 2 x 1792, 8 of 64, 1 token 25.9 /
-// 26.0, 4 tokens 58.6 / 62.0, a = 4 125 / 123; 4096 -> 2 x 3584, 2 of 16, 1 token (56 tiles) 16.1
-// / 19.0, 4 tokens 35.7 / 41.6, a = 4 68.3 / 70.4, 8 75.5 / 74.9; 2304 -> 2 x 1040, 4 of 32, 1
-// token (36 tiles) 10.4 / 12.0, 4 tokens 17.1 / 14.5; plain, 3584 -> 4096, 1 token (32 tiles)
-// 13.2 / 15.2, 4 tokens 21.6 / 19.3; 1792 -> 4096, 1 token (128 tiles) 17.2 / 14.5; 512 ->
-// 1024, 6 of 96, 1 token 6.8 / 5.7.
+// gated weights in one or two of them an SM: it shares the bytes out evenly, but reads
+// a weight tile again (from L2) for every 32 rows of an expert, and stores column by
+// column.  N: weight rows of an expert (glu: 2F).  Few rows / one CTA a tile, glu as
+// above: 2 of 16, 1 token (56 tiles) 17.6 / 20.4, 4 tokens (224) 36.0 / 43.1, a = 2 67.2 / 69.3, 8
+// 77.7 / 77.9, 16 85.0 / 79.5; 8 of 64, 1 token (112) 27.0 / 26.6, 4 tokens (448) 57.3 / 58.1, a = 2
+// 93.5 / 94.7, 4 124 / 122; 4 of 32, 1 token (36) 10.5 / 11.9, 4 tokens (144) 17.9 / 16.3; 8 of 128,
+// 1 token (48) 11.6 / 11.4, a = 2 48.2 / 49.8; 4096 -> 2 x 2048, 2 of 8, 1 token (32) 13.5 / 17.2,
+// 4 tokens (128) 20.8 / 22.1; plain, 2 of 16, 1 token (32) 13.6 / 14.6, 4 tokens (128) 24.0 /
+// 21.8; 1792 -> 4096, 8 of 64, 1 token (128) 18.0 / 15.7; 512 -> 1024, 6 of 96, 1 token 6.8 / 5.8.
 constexpr int kExpertNT = 32;
 static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool glu, int sms)
 {
     const ExpertLayout l = expert_layout(T, k, E);
     const int64_t wtiles = (N + BM - 1) / BM, nkb = (K + BK - 1) / BK, most = l.rows / kExpertNT * wtiles;
     if (most > kRowsMaxTiles || most * nkb >= ((int64_t)1 << 31) || sms > kRowsMaxCtas) return false;
-    const int64_t n = T * k, active = E < n ? E : n, tiles = active * ((N + kFfnBN - 1) / kFfnBN);
-    if (!expert_single_ctas(T, k, E) || nkb < 8) return false;
-    return tiles <= 64 || (glu && nkb > 20 && n <= 3 * active);
+    const ExpertSizes s(T, k, E, N);
+    if (!expert_single_ctas(s, sms) || nkb < 8) return false;
+    return s.tiles <= 64 || (glu && nkb > 20 && s.n <= 3 * s.active && s.tiles > sms);
 }
 
 size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K)
@@ -213,7 +225,7 @@ cudaError_t launch_expert_gemm(const ExpertGemmArgs& a, cudaStream_t st, int sms
     if ((a.kind == kExpertGlu || (a.kind == kExpertGemm && !a.b_mn)) &&
         expert_few_rows(a.T, a.k, a.E, a.kind == kExpertGlu ? 2 * a.N : a.N, a.K, a.kind == kExpertGlu, sms))
         return a.kind == kExpertGlu ? launch_few_rows<kEpiGlu>(a, p, st, sms, why) : launch_few_rows<kEpiAct>(a, p, st, sms, why);
-    const bool single = expert_single_ctas(a.T, a.k, a.E);
+    const bool single = expert_single_ctas(ExpertSizes(a.T, a.k, a.E, a.kind == kExpertGlu ? 2 * a.N : a.N), sms);
     switch (a.kind) {
     case kExpertGlu:
         return single ? launch_pair<kEpiGlu, kRows, false>(a, p, st, sms, why) : launch_pair<kEpiGlu, kRows>(a, p, st, sms, why);
