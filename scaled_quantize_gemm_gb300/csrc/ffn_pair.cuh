@@ -348,8 +348,8 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
         // a group's tiles share t / num_n with its first num_n * size tiles' range
         const int4 d = __ldg(p.tiles + t / sched.num_n);
         const int r = t - d.x * sched.num_n, size = max(d.y & 0xFF, 1);
-        x.nb = r / size;
-        x.expert = min(d.y >> 8, p.E - 1);
+        x.nb = min(max(r / size, 0), sched.num_n - 1);
+        x.expert = min(max(d.y >> 8, 0), p.E - 1);
         x.row0 = max(d.z + (r - x.nb * size) * 2 * BM + half * BM, 0);
         x.end = min(d.w, p.M);
         x.k0 = 0;

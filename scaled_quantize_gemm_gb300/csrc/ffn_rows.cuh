@@ -93,7 +93,7 @@ __device__ __forceinline__ RowsTile rows_tile(const FfnParams& p, const RowsPara
         const LOAD load;
         const int4 d = load(p.blocks + tile / w.wtiles);
         const int i = tile - d.y * w.wtiles, size = max(d.z, 1);
-        x.wt = i / size;
+        x.wt = min(max(i / size, 0), w.wtiles - 1);          // (whatever the plan holds, all of it inside the buffers)
         x.mt = min(max(d.y + i - x.wt * size, 0), p.max_blocks - 1);
         x.expert = min(max(d.x, 0), p.E - 1);
         x.wrow = x.expert * p.wrows;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             while (i < to) {
                 const int tile = (h0 + i) / hint.nkb, kb0 = h0 + i - tile * hint.nkb, n = min(to - i, hint.nkb - kb0);
                 const RowsTile x = rows_tile<true, LoadPlanL2>(p, hint, tile, NT);
-                const int row = x.wrow + min(max(x.wt, 0), w.wtiles - 1) * BOX;
+                const int row = x.wrow + x.wt * BOX;
                 for (int k = kb0; k < kb0 + n; ++k) {
                     prefetch_l2_2d(&tmW, k * BK, row);
                     if (GLU) prefetch_l2_2d(&tmW, k * BK, p.N + row);

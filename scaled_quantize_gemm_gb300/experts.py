@@ -10,7 +10,8 @@
 with per-tensor delayed scaling for the activations and a scale of its own for every
 expert's weights.  The router is the caller's: ``ids`` int32 [T][k] (an id outside
 [0, experts) leaves a slot out, as for padding) and ``weights`` fp32 [T][k], whose
-gradient ``backward`` returns.  Nothing of the routing is read on the host, so a
+gradient ``backward`` returns.  A token without any expert still passes through the
+norm, its statistics and gamma's gradient: its rows of x and dy hold finite numbers.  Nothing of the routing is read on the host, so a
 captured graph follows the ids that are in place when it is replayed.
 
 ``forward`` and ``backward`` are a training step (weights cast from bf16 every step,
