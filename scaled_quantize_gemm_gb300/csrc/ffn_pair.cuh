@@ -76,7 +76,6 @@ struct FfnSmem : Smem<PAIR ? kFfnBH : kFfnBN, PAIR ? kFfnStages<KIND, GROUP> : 4
     static constexpr int STG_OFF = KIND == kEpiGluBwd || (KIND == kEpiAct && GROUP != 0) ? Base::BAR_OFF + 1024 : Base::STG_OFF;
     static constexpr int BYTES = STG_OFF + Base::BYTES - Base::STG_OFF;
 };
-     // 32 staging boxes of 1 KB, shared out among the epilogue warps
 
 // ------------------------------------------------------------------ epilogue pieces
 __device__ __forceinline__ uint32_t pack_bf16(float2 v)
