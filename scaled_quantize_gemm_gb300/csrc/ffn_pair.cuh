@@ -369,7 +369,7 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
 // Rows of A that CTA `rank` of the pair loads for a tile.  Experts' products by rows:
 // those of the expert alone (a multiple of 32, in boxes of 32 rows), as the rest of
 // the tile's sums are not stored: an expert of few rows reads little beside its
-// weights (4 of 32 experts, 1040 -> 2304, 192 tokens 20.8 -> 18.7 us; 8 of 64, 4096 ->
+// weights (on CTA pairs: 4 of 32 experts, 1040 -> 2304, 192 tokens 20.8 -> 18.7 us; 8 of 64, 4096 ->
 // 2 x 1792, 256 tokens 158.9 -> 155.4; others within 1 %).
 template <int GROUP>
 __device__ __forceinline__ int pair_rows(const PairTile& x, int rank)
@@ -498,7 +498,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
                 }
             }
             // (experts: the next product's CTAs start as this grid's leave their SMs; 4 of
-            // 32 experts, 2304 -> 1040 and back, 192 tokens 56.5 -> 55.3 us)
+            // 32 experts, 2304 -> 1040 and back, 192 tokens on CTA pairs 56.5 -> 55.3 us)
             if (GROUP != kNoGroups) pdl_trigger();
             if (PAIR && __builtin_expect(aborted, 0)) pair_stop(s_stop, rank, issued);
             bool released = !aborted;

@@ -293,11 +293,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         // The plan as it stands in L2 now, as a hint: as a rule a kernel or more
         // lies between the plan's and this one, and what is fetched for a plan that
         // is not there yet is the wrong weights, no more (every tile is within the
-        // weights).  One token,
-        // 8 of 64 experts, 4096 -> 2 x 1792 and back: 43.3 us, without 43.7.
+        // weights).  Gated products of short K, behind a dispatch, are ready as soon as it
+        // is, and working the hint out delays them.  A sublayer of one token, us,
+        // with / without: 2 of 16 experts, 4096 -> 3584 40.0 / 41.2; 2 of 8, 4096 -> 2048 33.6 /
+        // 35.2; gated K of 2304, 2048, 1024: 28.1 / 27.4, 27.8 / 27.5, 21.6 / 21.0.
         constexpr int64_t L2Q = (int64_t)64 << 20;
         const int cap = (int)(L2Q / ((int64_t)gridDim.x * A_BYTES));
-        if (threadIdx.x == 0 || threadIdx.x == 64) {
+        if ((!GLU || w.nkb > 20) && (threadIdx.x == 0 || threadIdx.x == 64)) {
             RowsParams hint = w;
             int h0, h1;
             rows_schedule<NT, L::STAGE>(p, hint, __ldcg(p.offsets + p.E), h0, h1);
