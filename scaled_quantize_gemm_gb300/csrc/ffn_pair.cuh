@@ -312,22 +312,32 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 struct PairTile {
     int row0, end, nb, expert, k0, nkb, last;
 };
-template <int GROUP, bool PAIR>
+// the plan's words
+struct LoadPlan {
+    template <typename T>
+    __device__ __forceinline__ T operator()(const T* q) const { return __ldg(q); }
+};
+// (L2 only: leaves nothing in the SM's own cache)
+struct LoadPlanL2 {
+    template <typename T>
+    __device__ __forceinline__ T operator()(const T* q) const { return __ldcg(q); }
+};
+template <int GROUP, bool PAIR, typename LOAD = LoadPlan>
 __device__ __forceinline__ int pair_tiles(const FfnParams& p, const TileSched& sched)
 {
     if constexpr (GROUP == kNoGroups) return sched.num_m * sched.num_n;
     else if constexpr (GROUP == kWgrad) return p.E * sched.num_m * sched.num_n;
-    else return (PAIR ? 1 : 2) * min(__ldg(p.ntiles), p.max_tiles) * sched.num_n;
+    else return (PAIR ? 1 : 2) * min(LOAD()(p.ntiles), p.max_tiles) * sched.num_n;
 }
 // (One CTA a tile: the plan's tiles in halves of 128 rows, all first halves before
 // all second ones, of which those past their expert's rows have no K blocks.)
-template <int GROUP, bool PAIR>
+template <int GROUP, bool PAIR, typename LOAD = LoadPlan>
 __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSched& sched, int t)
 {
     PairTile x;
     [[maybe_unused]] int half = 0;
     if constexpr (!PAIR) {
-        const int n = min(__ldg(p.ntiles), p.max_tiles) * sched.num_n;
+        const int n = min(LOAD()(p.ntiles), p.max_tiles) * sched.num_n;
         half = t >= n ? 1 : 0;
         t -= half * n;
     }
@@ -345,7 +355,7 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
         x.last = (rows - (x.nkb - 1) * BK + 31) / 32;
     } else if constexpr (GROUP != kNoGroups) {
         // a group's tiles share t / num_n with its first num_n * size tiles' range
-        const int4 d = __ldg(p.tiles + t / sched.num_n);
+        const int4 d = LOAD()(p.tiles + t / sched.num_n);
         const int r = t - d.x * sched.num_n, size = max(d.y & 0xFF, 1);
         x.nb = min(max(r / size, 0), sched.num_n - 1);
         x.expert = min(max(d.y >> 8, 0), p.E - 1);
@@ -431,6 +441,25 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
         } else {
             tmem_alloc(holder, TMEM_COLS);
             tmem_relinquish();
+        }
+    }
+    if constexpr (!PAIR) {
+        // The first tile's weights into L2 while the kernel before still runs, by the
+        // plan as it stands there now: a hint, as a kernel or more lies between the
+        // plan's and this one as a rule; for a plan that is not there yet the wrong
+        // weights, no more (pair_tile keeps any plan's tiles within them).  A
+        // sublayer, us, without / with: 8 of 64 experts, 4096 -> 1792, 1 token 53.8 / 51.2, 32
+        // tokens 241 / 237; 2 of 8, 4096 -> 2048, 16 tokens 56.0 / 53.3; 4 of 32, 2304 -> 1040, 16
+        // tokens 58.6 / 57.0; 6 of 96, 1024 -> 512, 4 tokens 28.4 / 27.2.
+        constexpr int64_t L2Q = (int64_t)64 << 20;
+        if (threadIdx.x == 64 && (int)blockIdx.x < pair_tiles<GROUP, PAIR, LoadPlanL2>(p, sched)) {
+            const PairTile x = pair_tile<GROUP, PAIR, LoadPlanL2>(p, sched, blockIdx.x);
+            const int br = x.expert * (KIND == kEpiGlu ? 2 * p.N : p.N) + x.nb * (KIND == kEpiGlu ? BH : BN);
+            const int to = min(x.nkb, (int)(L2Q / ((int64_t)gridDim.x * L::B_BYTES)));
+            for (int kb = 0; kb < to; ++kb) {
+                prefetch_l2_2d(&tmB, kb * BK, br);
+                prefetch_l2_2d(&tmB, kb * BK, br + (KIND == kEpiGlu ? p.N : BH));
+            }
         }
     }
     pdl_enter();

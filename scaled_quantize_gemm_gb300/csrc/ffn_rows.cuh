@@ -78,13 +78,6 @@ struct RowsTile {
     int wrow;                            // first of the expert's weight rows
     int expert, live;                    // rows of the token tile that are not padding
 };
-struct LoadPlan {
-    __device__ __forceinline__ int4 operator()(const int4* q) const { return __ldg(q); }
-};
-// (L2 only: leaves nothing in the SM's own cache)
-struct LoadPlanL2 {
-    __device__ __forceinline__ int4 operator()(const int4* q) const { return __ldcg(q); }
-};
 template <bool EXPERTS, typename LOAD = LoadPlan>
 __device__ __forceinline__ RowsTile rows_tile(const FfnParams& p, const RowsParams& w, int tile, int nt)
 {
