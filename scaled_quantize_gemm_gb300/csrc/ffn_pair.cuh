@@ -416,6 +416,14 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
     __shared__ int s_stop[2];                  // stages each CTA's producer had issued when it gave up, else -1
     const uint32_t rank = cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cid = PAIR ? blockIdx.x >> 1 : blockIdx.x, ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
+    // a tile's first row of B in this CTA.  glu_fwd: gate rows in the even CTA, the up
+    // rows of the same features in the odd one
+    auto weight_row = [&](const PairTile& x) {
+        int br = KIND == kEpiGlu ? (int)rank * p.N + x.nb * BH : x.nb * BN + (int)rank * BH;
+        if constexpr (GROUP == kRows) br += x.expert * (KIND == kEpiGlu ? 2 * p.N : p.N);
+        return br;
+    };
 
     // what touches no global memory of the kernel before this one runs ahead
     // of the wait on it
@@ -443,22 +451,22 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
             tmem_relinquish();
         }
     }
-    if constexpr (!PAIR) {
+    if constexpr (GROUP == kRows) {
         // The first tile's weights into L2 while the kernel before still runs, by the
         // plan as it stands there now: a hint, as a kernel or more lies between the
         // plan's and this one as a rule; for a plan that is not there yet the wrong
         // weights, no more (pair_tile keeps any plan's tiles within them).  A
         // sublayer, us, without / with: 8 of 64 experts, 4096 -> 1792, 1 token 53.8 / 51.2, 32
         // tokens 241 / 237; 2 of 8, 4096 -> 2048, 16 tokens 56.0 / 53.3; 4 of 32, 2304 -> 1040, 16
-        // tokens 58.6 / 57.0; 6 of 96, 1024 -> 512, 4 tokens 28.4 / 27.2.
+        // tokens 58.6 / 57.0; 6 of 96, 1024 -> 512, 4 tokens 28.4 / 27.2; on CTA pairs, 1024 tokens, 8
+        // of 64 293.6 / 290.0, 2 of 16, 4096 -> 3584 160.2 / 156.8, 4 of 32 82.0 / 81.8.
         constexpr int64_t L2Q = (int64_t)64 << 20;
-        if (threadIdx.x == 64 && (int)blockIdx.x < pair_tiles<GROUP, PAIR, LoadPlanL2>(p, sched)) {
-            const PairTile x = pair_tile<GROUP, PAIR, LoadPlanL2>(p, sched, blockIdx.x);
-            const int br = x.expert * (KIND == kEpiGlu ? 2 * p.N : p.N) + x.nb * (KIND == kEpiGlu ? BH : BN);
-            const int to = min(x.nkb, (int)(L2Q / ((int64_t)gridDim.x * L::B_BYTES)));
+        if (threadIdx.x == 64 && cid < pair_tiles<GROUP, PAIR, LoadPlanL2>(p, sched)) {
+            const PairTile x = pair_tile<GROUP, PAIR, LoadPlanL2>(p, sched, cid);
+            const int br = weight_row(x), to = min(x.nkb, (int)(L2Q / ((int64_t)gridDim.x * L::B_BYTES)));
             for (int kb = 0; kb < to; ++kb) {
                 prefetch_l2_2d(&tmB, kb * BK, br);
-                prefetch_l2_2d(&tmB, kb * BK, br + (KIND == kEpiGlu ? p.N : BH));
+                if (!PAIR) prefetch_l2_2d(&tmB, kb * BK, br + (KIND == kEpiGlu ? p.N : BH));
             }
         }
     }
@@ -473,7 +481,6 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
     const uint32_t tmem_base = *holder;
 
     const int num_tiles = pair_tiles<GROUP, PAIR>(p, sched);
-    const int cid = PAIR ? blockIdx.x >> 1 : blockIdx.x, ncl = PAIR ? gridDim.x >> 1 : gridDim.x;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err_cluster(bar, parity, p.err); };
 
     if (skip) {
@@ -487,10 +494,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
             for (int t = cid; t < num_tiles && !aborted; t += ncl) {
                 const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
                 const int ar = x.row0 + (int)rank * BM;
-                // glu_fwd: gate rows in the even CTA, the up rows of the same
-                // features in the odd one
-                int br = KIND == kEpiGlu ? (int)rank * p.N + x.nb * BH : x.nb * BN + (int)rank * BH;
-                if constexpr (GROUP == kRows) br += x.expert * (KIND == kEpiGlu ? 2 * p.N : p.N);
+                const int br = weight_row(x);
                 const int bk = GROUP == kRowsMn ? x.expert * p.K : x.k0;
                 const int rows = pair_rows<GROUP>(x, (int)rank);
                 const uint32_t tx = (uint32_t)((PAIR ? 2 : 1) * L::B_BYTES) +
