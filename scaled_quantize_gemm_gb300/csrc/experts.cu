@@ -118,16 +118,16 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
 // `tiles` of 256 weight rows (glu: 128 of the gate and of the up projection).
 // Figures: one GB300, us, weights from DRAM (in brackets their bytes at the copy rate).
 //
-// One CTA a tile of 128 rows up to a = 20, up to 40 where an SM gets three tiles at
-// most; from there on CTA pairs and 256 rows, whose operands cost less traffic.
-// One CTA / pairs: 4096 -> 2 x 1792, 8 of 64 (896 tiles), 1 token 26.6 / 30.4 (17.4),
-// a = 4 122 / 128 (111), 16 146 / 153 (133), 32 162 / 156, 64 193 / 166; 2304 -> 2 x 1040, 4
-// of 32 (288 tiles), a = 4 28.4 / 30.4 (18.6), 16 31.0 / 33.1, 32 31.6 / 33.5, 48 37.5 / 33.7;
-// 4096 -> 2 x 3584, 2 of 16 (448), a = 16 79.5 / 82.3 (69.4), 32 79.9 / 82.6, 64 92.0 / 84.0;
-// 2048 -> 2 x 768, 8 of 128 (768), a = 8 63.9 / 65.0 (52.8), 16 69.1 / 68.4, 32 77.2 / 70.0;
-// 1024 -> 2 x 512, 6 of 96 (384), a = 4 20.6 / 21.1 (11.7), 32 25.5 / 24.2; plain, 3584 -> 4096, 2
-// of 16 (256), a = 8 42.3 / 48.1 (33.6), 32 44.3 / 49.3, 64 54.3 / 49.7; 2048 -> 4096, 2 of 8
-// (128), a = 8 15.9 / 18.0 (9.5).
+// One CTA a tile of 128 rows up to a = 20, 40 where an SM gets three tiles at most, 64
+// where it gets one; from there on CTA pairs and 256 rows, whose operands cost less traffic.
+// One CTA / pairs: 4096 -> 2 x 1792, 8 of 64 (896 tiles), 1 token 26.0 / 30.4 (17.4),
+// a = 4 121 / 127 (111), 16 145 / 153 (133), 32 161 / 155, 64 192 / 165; 2048 -> 2 x 768, 8 of 128
+// (768), a = 8 62.8 / 64.6 (52.8), 16 68.3 / 68.2, 24 72.3 / 69.2; 2304 -> 2 x 1040, 4 of 32
+// (288), a = 4 27.4 / 30.1 (18.6), 16 30.2 / 33.2, 40 32.7 / 33.9, 48 36.5 / 34.3; 4096 -> 2 x 3584,
+// 2 of 16 (448), a = 16 78.0 / 81.5 (69.4), 40 78.6 / 82.4, 64 90.6 / 83.4; 1024 -> 2 x 512, 6 of
+// 96 (384), a = 4 19.7 / 20.8 (11.7), 40 24.8 / 24.6, 64 27.2 / 25.7; 4096 -> 2 x 2048, 2 of 8 (128),
+// a = 16 27.5 / 30.0 (19.8), 64 28.1 / 31.1; plain, 3584 -> 4096, 2 of 16 (256), a = 8 41.4 / 47.9
+// (33.6), 40 43.4 / 49.2, 64 53.8 / 49.6; 2048 -> 4096, 2 of 8 (128), a = 64 16.5 / 19.6 (9.9).
 struct ExpertSizes {
     int64_t n, active, tiles;
     ExpertSizes(int64_t T, int k, int E, int64_t N)
@@ -137,18 +137,18 @@ struct ExpertSizes {
 };
 static bool expert_single_ctas(const ExpertSizes& s, int sms)
 {
-    return s.n <= (s.tiles <= 3 * sms ? 40 : 20) * s.active;
+    return s.n <= (s.tiles <= sms ? 64 : s.tiles <= 3 * sms ? 40 : 20) * s.active;
 }
 // k_ffn_rows where those tiles do not go round, or where single tokens stream long
 // gated weights in one or two of them an SM: it shares the bytes out evenly, but reads
 // a weight tile again (from L2) for every 32 rows of an expert, and stores column by
 // column.  N: weight rows of an expert (glu: 2F).  Few rows / one CTA a tile, glu as
-// above: 2 of 16, 1 token (56 tiles) 17.6 / 20.4, 4 tokens (224) 36.0 / 43.1, a = 2 67.2 / 69.3, 8
-// 77.7 / 77.9, 16 85.0 / 79.5; 8 of 64, 1 token (112) 27.0 / 26.6, 4 tokens (448) 57.3 / 58.1, a = 2
-// 93.5 / 94.7, 4 124 / 122; 4 of 32, 1 token (36) 10.5 / 11.9, 4 tokens (144) 17.9 / 16.3; 8 of 128,
-// 1 token (48) 11.6 / 11.4, a = 2 48.2 / 49.8; 4096 -> 2 x 2048, 2 of 8, 1 token (32) 13.5 / 17.2,
-// 4 tokens (128) 20.8 / 22.1; plain, 2 of 16, 1 token (32) 13.6 / 14.6, 4 tokens (128) 24.0 /
-// 21.8; 1792 -> 4096, 8 of 64, 1 token (128) 18.0 / 15.7; 512 -> 1024, 6 of 96, 1 token 6.8 / 5.8.
+// above: 2 of 16, 1 token (56 tiles) 17.6 / 20.0, 4 tokens (224) 36.0 / 42.3, a = 2 (448) 67.5 /
+// 68.1, 8 77.2 / 76.3; 8 of 64, 1 token (112) 27.0 / 26.0, 4 tokens (448) 57.0 / 56.8, a = 4 125 /
+// 121; 4 of 32, 1 token (36) 10.4 / 13.1, 4 tokens (144) 17.9 / 15.9; 8 of 128, 1 token (48) 10.5 /
+// 12.6, a = 2 (768) 49.4 / 48.6; 2 of 8, 1 token (32) 13.8 / 19.3, 4 tokens (128) 21.3 / 22.0; plain,
+// 2 of 16, 1 token (32) 14.1 / 16.6, 4 tokens (128) 23.9 / 21.6; 1792 -> 4096, 8 of 64, 1 token
+// (128) 18.1 / 15.3; 512 -> 1024, 6 of 96, 1 token 6.7 / 5.8.
 constexpr int kExpertNT = 32;
 static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool glu, int sms)
 {
@@ -157,7 +157,7 @@ static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool 
     if (most > kRowsMaxTiles || most * nkb >= ((int64_t)1 << 31) || sms > kRowsMaxCtas) return false;
     const ExpertSizes s(T, k, E, N);
     if (!expert_single_ctas(s, sms) || nkb < 8) return false;
-    return s.tiles <= 64 || (glu && nkb > 20 && s.n <= 3 * s.active && s.tiles > sms);
+    return s.tiles <= 64 || (glu && nkb > 20 && s.n <= 3 * s.active && s.tiles > sms && s.tiles <= 2 * sms);
 }
 
 size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K)
