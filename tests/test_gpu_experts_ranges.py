@@ -150,6 +150,44 @@ def test_a_word_set_while_products_start(how, T, k, E, N, K):
         assert torch.equal(D, want) and sq.fp8_device_status(True) == sq.OK
 
 
+# one plan buffer for one routing after another, the product right behind the sort: what its CTAs fetch before their
+# wait follows the routing before
+@pytest.mark.parametrize("how,T,k,E,N,K", [("few", 4, 1, 4, 2064, 4096), ("single", 30, 4, 24, 2064, 4096), ("tiles", 2000, 2, 5, 1040, 1056), ("mn", 2000, 2, 5, 1040, 1056)])
+def test_products_right_behind_their_plan(how, T, k, E, N, K):
+    c = Case(T, k, E, "spread", seed=T + 1)
+    A, sa = to_codes(randn(c.g, c.R, K), 0)
+    B, sb = c.weights(K, N) if how == "mn" else c.weights(N, K)
+    ws = c.workspace(N, K)
+    ways = [routing(c.g, T, k, E, h) for h in ("spread", "last", "none", "masked", "one", "skewed", "spread", "masked")]
+    plan = torch.zeros_like(c.plan)
+
+    def call(p, out):
+        sq.fp8_expert_gemm(A, 0, sa, B, 0, sb, sq.MN_MAJOR if how == "mn" else sq.K_MAJOR, p, T, k, out, workspace=ws)
+    want = []
+    for ids in ways:
+        want.append(torch.zeros((c.R, N), device=DEV))
+        p = make_plan(ids, E)
+        torch.cuda.synchronize()
+        call(p, want[-1])
+        torch.cuda.synchronize()
+    got = [torch.zeros((c.R, N), device=DEV) for _ in ways]
+
+    def chain():
+        for ids, out in zip(ways, got):
+            sq.fp8_expert_plan(ids, E, plan)
+            call(plan, out)
+    chain()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(5):
+        for out in got:
+            out.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_products_refuse_outputs_over_other_buffers():
     T, k, E, d, F = 40, 2, 3, 64, 96
     c = Case(T, k, E, "spread")
