@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfp8sq.so")
 SOURCES = ["quantize.cu", "gemm.cu", "ffn.cu", "rowops.cu", "rmsnorm.cu", "experts.cu", "experts_rows.cu", "api.cu", "api_ffn.cu", "api_experts.cu", "noalloc.cu"]
-HEADERS = ["ptx.cuh", "act.cuh", "scales.cuh", "rowvec.cuh", "norm.cuh", "ffn_pair.cuh", "ffn_rows.cuh", "api_checks.h", "gemm_common.cuh", "internal.h", os.path.join("..", "..", "include", "fp8sq.h")]
+HEADERS = ["ptx.cuh", "act.cuh", "scales.cuh", "rowvec.cuh", "norm.cuh", "plan_tile.h", "ffn_pair.cuh", "ffn_rows.cuh", "api_checks.h", "gemm_common.cuh", "internal.h", os.path.join("..", "..", "include", "fp8sq.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -9,6 +9,7 @@
 #include "act.cuh"
 #include "gemm_common.cuh"
 #include "internal.h"
+#include "plan_tile.h"
 #include "ptx.cuh"
 
 namespace fp8sq {
@@ -356,11 +357,11 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
     } else if constexpr (GROUP != kNoGroups) {
         // a group's tiles share t / num_n with its first num_n * size tiles' range
         const int4 d = LOAD()(p.tiles + t / sched.num_n);
-        const int r = t - d.x * sched.num_n, size = max(d.y & 0xFF, 1);
-        x.nb = min(max(r / size, 0), sched.num_n - 1);
-        x.expert = min(max(d.y >> 8, 0), p.E - 1);
-        x.row0 = max(d.z + (r - x.nb * size) * 2 * BM + half * BM, 0);
-        x.end = min(d.w, p.M);
+        const PlanTile y = plan_tile(d.x, d.y, d.z, d.w, t, sched.num_n, p.E, p.M, half);
+        x.nb = y.nb;
+        x.expert = y.expert;
+        x.row0 = y.row0;
+        x.end = y.end;
         x.k0 = 0;
         x.nkb = PAIR || x.row0 < x.end ? (p.K + BK - 1) / BK : 0;
         x.last = (p.K - (x.nkb - 1) * BK + 31) / 32;
@@ -381,10 +382,11 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
 // the tile's sums are not stored: an expert of few rows reads little beside its
 // weights (on CTA pairs: 4 of 32 experts, 1040 -> 2304, 192 tokens 20.8 -> 18.7 us; 8 of 64, 4096 ->
 // 2 x 1792, 256 tokens 158.9 -> 155.4; others within 1 %).
+static_assert(kTileHalf == BM && kTileBox == kExpertPad, "plan_tile.h");
 template <int GROUP>
 __device__ __forceinline__ int pair_rows(const PairTile& x, int rank)
 {
-    if constexpr (GROUP == kRows || GROUP == kRowsMn) return min(max(x.end - x.row0 - rank * BM, 0), BM);
+    if constexpr (GROUP == kRows || GROUP == kRowsMn) return plan_tile_rows({x.row0, x.end, x.nb, x.expert}, rank);
     else return BM;
 }
 
