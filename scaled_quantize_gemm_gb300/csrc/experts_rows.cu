@@ -12,6 +12,9 @@
 // All are bound by memory: a token's row is read once and written (or summed
 // from) its k places, whole rows at a time.  No atomics on data: every sum runs
 // in the order of the slots, so the same call gives the same bits.
+// What they read is no constant of their run: they may be resident while the kernel
+// that writes it still runs, so inputs are not declared __restrict__ (nor read with
+// __ldg) and the loads stay behind the wait in pdl_enter.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -248,7 +251,7 @@ constexpr int kMoveThreads = 256;
 // while this one is stored.  Before them the experts' padding (at most 31 rows
 // each), shared out likewise.
 template <typename V>
-__global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __restrict__ x, const int32_t* __restrict__ row_of,
+__global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* x, const int32_t* row_of,
                                                                   Segments seg, int64_t T, int k, int64_t vecs,
                                                                   V* __restrict__ out)
 {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __res
         const int32_t* to = row_of + t * k;
 #pragma unroll 4
         for (int j = 0; j < k; ++j) {
-            const int32_t r = __ldg(to + j);
+            const int32_t r = to[j];
             if (r >= 0 && r < seg.rows) out[r * vecs + c] = v;
         }
     }
@@ -282,8 +285,8 @@ __global__ void __launch_bounds__(kMoveThreads) k_expert_dispatch(const V* __res
 // tokens of 4 rows of 4096 bf16 with residual, 59.5 us at the copy rate: 59.6; one element at a
 // time and eight rows' registers for any k 75.)
 template <typename T, int VEC, int FLY>
-__global__ void __launch_bounds__(kMoveThreads, FLY <= 4 ? 6 : 4) k_expert_combine(const T* __restrict__ rows, const int32_t* __restrict__ row_of,
-                                                                 const float* __restrict__ w, const T* res, int64_t nt,
+__global__ void __launch_bounds__(kMoveThreads, FLY <= 4 ? 6 : 4) k_expert_combine(const T* rows, const int32_t* row_of,
+                                                                 const float* w, const T* res, int64_t nt,
                                                                  int k, int64_t K, int64_t R, T* y)
 {
     using P = Pack<T, VEC>;
@@ -302,12 +305,12 @@ __global__ void __launch_bounds__(kMoveThreads, FLY <= 4 ? 6 : 4) k_expert_combi
 #pragma unroll
             for (int j = 0; j < FLY; ++j) {
                 int32_t r = -1;
-                if (j0 + j < k) r = __ldg(row_of + t * k + j0 + j);
+                if (j0 + j < k) r = row_of[t * k + j0 + j];
                 wj[j] = 0.0f;
                 raw[j] = Raw{};
                 if (r >= 0 && r < R) {
-                    raw[j] = __ldg(reinterpret_cast<const Raw*>(rows + r * K + c));
-                    wj[j] = w ? __ldg(w + t * k + j0 + j) : 1.0f;
+                    raw[j] = *reinterpret_cast<const Raw*>(rows + r * K + c);
+                    wj[j] = w ? w[t * k + j0 + j] : 1.0f;
                 }
             }
 #pragma unroll
@@ -362,8 +365,8 @@ struct CombineBwdOut {
     float* dw;
 };
 template <typename T, int VEC, int JB>
-__global__ void __launch_bounds__(256, JB <= 2 ? 6 : 4) k_expert_combine_bwd(const T* __restrict__ dy, const T* __restrict__ rows,
-                                                            const int32_t* __restrict__ row_of, const float* __restrict__ w,
+__global__ void __launch_bounds__(256, JB <= 2 ? 6 : 4) k_expert_combine_bwd(const T* dy, const T* rows,
+                                                            const int32_t* row_of, const float* w,
                                                             Segments seg, int64_t nt, int k, int64_t K, CombineBwdOut o)
 {
     using P = Pack<T, VEC>;
@@ -392,18 +395,18 @@ __global__ void __launch_bounds__(256, JB <= 2 ? 6 : 4) k_expert_combine_bwd(con
             float2 dot[JB] = {};
 #pragma unroll
             for (int j = 0; j < JB; ++j) {
-                const int32_t r = j0 + j < k ? __ldg(row_of + t * k + j0 + j) : -1;
+                const int32_t r = j0 + j < k ? row_of[t * k + j0 + j] : -1;
                 at[j] = r < seg.rows ? r : -1;
-                wj[j] = at[j] >= 0 ? __ldg(w + t * k + j0 + j) : 0.0f;
+                wj[j] = at[j] >= 0 ? w[t * k + j0 + j] : 0.0f;
             }
             for (int64_t c = (int64_t)th * VEC; c < K; c += (int64_t)blockDim.x * VEC) {
                 float d[2 * PAIRS] = {};
-                P::to_floats(__ldg(reinterpret_cast<const Raw*>(dy + t * K + c)), reinterpret_cast<float(&)[VEC]>(d));
+                P::to_floats(*reinterpret_cast<const Raw*>(dy + t * K + c), reinterpret_cast<float(&)[VEC]>(d));
                 Raw raw[JB];
                 if (o.dw) {
 #pragma unroll
                     for (int j = 0; j < JB; ++j)
-                        if (at[j] >= 0) raw[j] = __ldg(reinterpret_cast<const Raw*>(rows + (int64_t)at[j] * K + c));
+                        if (at[j] >= 0) raw[j] = *reinterpret_cast<const Raw*>(rows + (int64_t)at[j] * K + c);
                 }
 #pragma unroll
                 for (int j = 0; j < JB; ++j) {

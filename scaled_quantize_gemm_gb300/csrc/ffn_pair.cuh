@@ -313,10 +313,11 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* p, uint32_t v)
 struct PairTile {
     int row0, end, nb, expert, k0, nkb, last;
 };
-// the plan's words
+// the plan's words (ordinary loads: the kernel that writes them may still run while
+// this one is resident, so they are no constants of its run)
 struct LoadPlan {
     template <typename T>
-    __device__ __forceinline__ T operator()(const T* q) const { return __ldg(q); }
+    __device__ __forceinline__ T operator()(const T* q) const { return *q; }
 };
 // (L2 only: leaves nothing in the SM's own cache)
 struct LoadPlanL2 {
@@ -350,8 +351,8 @@ __device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSche
         x.row0 = mb * 2 * BM;
         x.end = p.M;
         // (whatever the plan holds, here and below, the work is bounded and every row inside the buffers)
-        x.k0 = min(max(__ldg(p.offsets + x.expert), 0), p.rows);
-        const int rows = max(min(__ldg(p.offsets + x.expert + 1), p.rows) - x.k0, 0);
+        x.k0 = min(max(LOAD()(p.offsets + x.expert), 0), p.rows);
+        const int rows = max(min(LOAD()(p.offsets + x.expert + 1), p.rows) - x.k0, 0);
         x.nkb = (rows + BK - 1) / BK;
         x.last = (rows - (x.nkb - 1) * BK + 31) / 32;
     } else if constexpr (GROUP != kNoGroups) {

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // wait for all of them without a limit, so a word that is set between two
     // warps' reads must not send one of them past the others.
     if (threadIdx.x == 0) s_skip = *reinterpret_cast<volatile int*>(p.err);
-    if constexpr (EXPERTS) ctas = rows_schedule<NT, L::STAGE>(p, w, __ldg(p.offsets + p.E), u0, u1);
+    if constexpr (EXPERTS) ctas = rows_schedule<NT, L::STAGE>(p, w, LoadPlan()(p.offsets + p.E), u0, u1);
     __syncthreads();
     const uint32_t tmem_base = *holder;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_bounded_err(bar, parity, p.err); };

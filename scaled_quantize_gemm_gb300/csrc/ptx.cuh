@@ -18,11 +18,13 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p)
 // stream serialisation (launch_k), so a kernel's launch is processed while
 // the previous kernel on the stream runs and its CTAs are placed as that
 // kernel's CTAs exit.  Every kernel of this library calls pdl_enter() before it
-// reads or writes anything that another kernel may touch; it waits until every
-// kernel it depends on has completed with its memory operations visible, so
+// uses what another kernel may write, and before it writes anything; it waits until
+// every kernel it depends on has completed with its memory operations visible, so
 // reads and writes keep plain stream order.  Most call it first; the
-// feed-forward products and the LayerNorms initialise barriers, allocate tensor
-// memory and prefetch weights into L2 (where all SMs meet) ahead of it.
+// feed-forward products and the norms initialise barriers, allocate tensor
+// memory and prefetch weights into L2 (where all SMs meet) ahead of it.  The one
+// exception: the experts' products read the plan ahead of it too, through L2, for
+// nothing but what to prefetch; behind the wait they read it again.
 // Kernels do not trigger their dependents early
 // (griddepcontrol.launch_dependents; but see pdl_trigger): measured on the GB300, an early
 // trigger let chains of waiting CTAs build up behind the persistent GEMMs
