@@ -116,18 +116,13 @@ static cudaError_t launch_pair(const ExpertGemmArgs& a, const FfnParams& p, cuda
 // The routing is known on the device alone, so the rules go by its sizes: n = T k
 // assignments make a = n / active rows for each of active = min(E, n) experts, and
 // `tiles` of 256 weight rows (glu: 128 of the gate and of the up projection).
-// Figures: one GB300, us, weights from DRAM (in brackets their bytes at the copy rate).
+// Figures: one GB300, us, weights from DRAM.
 //
 // One CTA a tile of 128 rows up to a = 20, 40 where an SM gets three tiles at most, 64
 // where it gets one; from there on CTA pairs and 256 rows, whose operands cost less traffic.
-// One CTA / pairs: 4096 -> 2 x 1792, 8 of 64 (896 tiles), 1 token 26.0 / 30.4 (17.4),
-// a = 4 121 / 127 (111), 16 145 / 153 (133), 32 161 / 155, 64 192 / 165; 2048 -> 2 x 768, 8 of 128
-// (768), a = 8 62.8 / 64.6 (52.8), 16 68.3 / 68.2, 24 72.3 / 69.2; 2304 -> 2 x 1040, 4 of 32
-// (288), a = 4 27.4 / 30.1 (18.6), 16 30.2 / 33.2, 40 32.7 / 33.9, 48 36.5 / 34.3; 4096 -> 2 x 3584,
-// 2 of 16 (448), a = 16 78.0 / 81.5 (69.4), 40 78.6 / 82.4, 64 90.6 / 83.4; 1024 -> 2 x 512, 6 of
-// 96 (384), a = 4 19.7 / 20.8 (11.7), 40 24.8 / 24.6, 64 27.2 / 25.7; 4096 -> 2 x 2048, 2 of 8 (128),
-// a = 16 27.5 / 30.0 (19.8), 64 28.1 / 31.1; plain, 3584 -> 4096, 2 of 16 (256), a = 8 41.4 / 47.9
-// (33.6), 40 43.4 / 49.2, 64 53.8 / 49.6; 2048 -> 4096, 2 of 8 (128), a = 64 16.5 / 19.6 (9.9).
+// One CTA / pairs: 896 tiles (4096 -> 2 x 1792), a = 16 145 / 153, 32 161 / 155; 288 (2304 ->
+// 2 x 1040), a = 40 32.7 / 33.9, 48 36.5 / 34.3; 152 (2048 -> 2 x 9728), a = 24 17.1 / 19.7, 64 17.4 / 20.2;
+// 160 (2048 -> 2 x 10240), a = 40 23.6 / 23.6.
 struct ExpertSizes {
     int64_t n, active, tiles;
     ExpertSizes(int64_t T, int k, int E, int64_t N)
@@ -142,13 +137,10 @@ static bool expert_single_ctas(const ExpertSizes& s, int sms)
 // k_ffn_rows where those tiles do not go round, or where single tokens stream long
 // gated weights in one or two of them an SM: it shares the bytes out evenly, but reads
 // a weight tile again (from L2) for every 32 rows of an expert, and stores column by
-// column.  N: weight rows of an expert (glu: 2F).  Few rows / one CTA a tile, glu as
-// above: 2 of 16, 1 token (56 tiles) 17.6 / 20.0, 4 tokens (224) 36.0 / 42.3, a = 2 (448) 67.5 /
-// 68.1, 8 77.2 / 76.3; 8 of 64, 1 token (112) 27.0 / 26.0, 4 tokens (448) 57.0 / 56.8, a = 4 125 /
-// 121; 4 of 32, 1 token (36) 10.4 / 13.1, 4 tokens (144) 17.9 / 15.9; 8 of 128, 1 token (48) 10.5 /
-// 12.6, a = 2 (768) 49.4 / 48.6; 2 of 8, 1 token (32) 13.8 / 19.3, 4 tokens (128) 21.3 / 22.0; plain,
-// 2 of 16, 1 token (32) 14.1 / 16.6, 4 tokens (128) 23.9 / 21.6; 1792 -> 4096, 8 of 64, 1 token
-// (128) 18.1 / 15.3; 512 -> 1024, 6 of 96, 1 token 6.7 / 5.8.
+// column.  N: weight rows of an expert (glu: 2F).  Few rows / one CTA a tile: one
+// token, 56 tiles (4096 -> 2 x 3584) 17.6 / 20.0, 112 (-> 2 x 1792) 27.0 / 26.0, plain 128 (1792 ->
+// 4096) 18.1 / 15.3; 208 tiles (-> 2 x 3328), K = 1536 20.0 / 19.2, 2048 23.5 / 23.8, 2816 29.9 / 31.2,
+// 4096 40.0 / 42.5; 448 (4096 -> 2 x 3584), a = 2 67.5 / 68.1, 8 77.2 / 76.3.
 constexpr int kExpertNT = 32;
 static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool glu, int sms)
 {
@@ -162,7 +154,9 @@ static bool expert_few_rows(int64_t T, int k, int E, int64_t N, int64_t K, bool 
 
 size_t expert_workspace(int64_t T, int k, int E, int64_t N, int64_t K)
 {
-    if (!expert_few_rows(T, k, E, N, K, true, 152)) return 0;          // (the wider rule)
+    // by the wider rule, the gated product's, on a GB300's 152 SMs (where the device has another number and
+    // k_ffn_rows comes without a workspace, it takes whole tiles)
+    if (!expert_few_rows(T, k, E, N, K, true, 152)) return 0;
     return kRowsCounterBytes + (size_t)kRowsMaxCtas * 2 * kExpertNT * BM * sizeof(float);
 }
 
