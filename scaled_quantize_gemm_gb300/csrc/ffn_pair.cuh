@@ -333,13 +333,14 @@ __device__ __forceinline__ int pair_tiles(const FfnParams& p, const TileSched& s
 }
 // (One CTA a tile: the plan's tiles in halves of 128 rows, all first halves before
 // all second ones, of which those past their expert's rows have no K blocks.)
+// num: pair_tiles
 template <int GROUP, bool PAIR, typename LOAD = LoadPlan>
-__device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSched& sched, int t)
+__device__ __forceinline__ PairTile pair_tile(const FfnParams& p, const TileSched& sched, int t, int num)
 {
     PairTile x;
     [[maybe_unused]] int half = 0;
     if constexpr (!PAIR) {
-        const int n = min(LOAD()(p.ntiles), p.max_tiles) * sched.num_n;
+        const int n = num / 2;
         half = t >= n ? 1 : 0;
         t -= half * n;
     }
@@ -464,8 +465,9 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
         // tokens 58.6 / 57.0; 6 of 96, 1024 -> 512, 4 tokens 28.4 / 27.2; on CTA pairs, 1024 tokens, 8
         // of 64 293.6 / 290.0, 2 of 16, 4096 -> 3584 160.2 / 156.8, 4 of 32 82.0 / 81.8.
         constexpr int64_t L2Q = (int64_t)64 << 20;
-        if (threadIdx.x == 64 && cid < pair_tiles<GROUP, PAIR, LoadPlanL2>(p, sched)) {
-            const PairTile x = pair_tile<GROUP, PAIR, LoadPlanL2>(p, sched, cid);
+        const int num = threadIdx.x == 64 ? pair_tiles<GROUP, PAIR, LoadPlanL2>(p, sched) : 0;
+        if (cid < num) {
+            const PairTile x = pair_tile<GROUP, PAIR, LoadPlanL2>(p, sched, cid, num);
             const int br = weight_row(x), to = min(x.nkb, (int)(L2Q / ((int64_t)gridDim.x * L::B_BYTES)));
             for (int kb = 0; kb < to; ++kb) {
                 prefetch_l2_2d(&tmB, kb * BK, br);
@@ -495,7 +497,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
             uint32_t phase = 0;
             bool aborted = false;
             for (int t = cid; t < num_tiles && !aborted; t += ncl) {
-                const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
+                const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t, num_tiles);
                 const int ar = x.row0 + (int)rank * BM;
                 const int br = weight_row(x);
                 const int bk = GROUP == kRowsMn ? x.expert * p.K : x.k0;
@@ -558,7 +560,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
             uint32_t phase = 0;
             bool aborted = false;
             for (int t = cid; t < num_tiles && !aborted; t += ncl) {
-                const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
+                const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t, num_tiles);
                 if ((GROUP == kWgrad || !PAIR) && x.nkb == 0) continue;          // an expert without rows: zeros, no product
                 const int b = lt & 1;
                 const uint32_t u = (uint32_t)(lt >> 1);
@@ -641,7 +643,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
         };
         int lt = 0;
         for (int t = cid; t < num_tiles; t += ncl) {
-            const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
+            const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t, num_tiles);
             if (!PAIR && x.nkb == 0) continue;
             const bool some = GROUP != kWgrad || x.nkb > 0;          // (else zeros)
             const int b = lt & 1;
@@ -846,7 +848,7 @@ __global__ void __cluster_dims__(PAIR ? 2 : 1, 1, 1) __launch_bounds__(kFfnThrea
             auto odd = [&](auto&& f) {
                 int i = 0;
                 for (int t = cid; t < num_tiles; t += ncl) {
-                    const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t);
+                    const PairTile x = pair_tile<GROUP, PAIR>(p, sched, t, num_tiles);
                     for (int kb = 0; kb < x.nkb; ++kb, ++i) {
                         if (s_stop[1] >= 0 && i >= s_stop[1]) return;
                         if (i >= s_stop[0]) f(i, (uint32_t)(L::B_BYTES + BK * pair_rows<GROUP>(x, 1)));
